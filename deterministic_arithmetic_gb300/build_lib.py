@@ -14,11 +14,13 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+CSRC_MLP = os.path.join(HERE, "csrc_mlp")     # the MLP-block operators (include/lora_mlp.h)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "liblora_delta.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["api.cu", "down.cu", "up.cu", "fwd_fused.cu", "fwd_cluster.cu", "bwd_cluster.cu", "dxda.cu", "wgrad.cu", "dy.cu", "rows.cu", "combine.cu", "noalloc.cu",
            "dvf32.cu", "exact.cu"]
+SOURCES_MLP = ["host.cu", "layer_norm.cu", "pack8.cu", "pack8_da.cu", "gated_ffn.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", *GENCODE]
 
@@ -29,9 +31,7 @@ def nvcc() -> str:
 
 
 def _deps() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(INCLUDE, "lora_delta.h"))
-    return files
+    return [os.path.join(d, f) for d in (CSRC, CSRC_MLP, INCLUDE) for f in os.listdir(d)]
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -48,8 +48,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple = (), l
     cc = nvcc()
 
     def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-        cmd = [cc, *NVFLAGS, *extra_flags, "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj]
+        obj = os.path.join(BUILD_DIR, os.path.splitext(os.path.basename(src))[0] + ".o")
+        cmd = [cc, *NVFLAGS, *extra_flags, "-I", INCLUDE, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,8 +59,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple = (), l
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
+    sources = [os.path.join(CSRC, f) for f in SOURCES] + [os.path.join(CSRC_MLP, f) for f in SOURCES_MLP]
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = list(ex.map(compile_one, sources))
     tmp = lib + ".tmp"
     cmd = [cc, "-shared", *GENCODE, "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,184 @@
+// gated_ffn.cu -- the gated feed-forward block's entry points: h = act(x Wg^T + Dg) (x Wu^T + Du), and
+// its backward pass.
+//
+// Backward: the element-wise step dU = dh act(G), dG = dh U act'(G) is a kernel of its own (bound by
+// HBM: dh, G and U read, dG and dU written once). Its outputs, rounded to bf16, are what the
+// adapters of the two projections take as dY, and the operands of the products dx and dW.
+#include "gemm.cuh"
+
+namespace mlp {
+namespace {
+
+// dG and dU of 8 elements a thread. XK: how G and U are kept (bf16 or packed).
+template <int XK>
+__global__ void __launch_bounds__(256)
+    ffn_grad_kernel(const void* __restrict__ dh, const void* __restrict__ g, const void* __restrict__ u,
+                    const void* __restrict__ gs, const void* __restrict__ us, int act, int64_t M, int F,
+                    void* __restrict__ dg, void* __restrict__ du) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int per = F / 8;
+  const int64_t items = M * per, ld = row_ld<XK>(F);
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < items; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t row = i / per;
+    const int c = int(i - row * per) * 8;
+    Raw<kBf16, 8> rh;
+    Raw<XK, 8> rg, ru;
+    rh.load(dh, nullptr, row, F, c);
+    rg.load(g, gs, row, ld, c);
+    ru.load(u, us, row, ld, c);
+    float h[8], a[8], b[8];
+    rh.get(h);
+    rg.get(a);
+    ru.get(b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = act_p(act, a[e]);
+      const float dg_e = h[e] * b[e] * act_slope(act, a[e], p);
+      b[e] = h[e] * (a[e] * p);
+      a[e] = dg_e;
+    }
+    // plain stores: the products that follow read both again, from L2 as far as they fit
+    const int64_t o = row * F + c;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dg) + o) = pack_bf16x8(a);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(du) + o) = pack_bf16x8(b);
+  }
+}
+
+// Sizes: k-blocks and tiles index with 32 bits, and a tile's reduction stays far inside the waits' limit.
+bool shape_ok(int64_t M, int64_t K, int64_t F) {
+  const int64_t most = int64_t(1) << 22;
+  return M >= 0 && M < most && K > 0 && K < most && F > 0 && F < most && K % 8 == 0 && F % 8 == 0;
+}
+bool kind_ok(int act, int keep) {
+  return (act == LORA_ACT_SILU || act == LORA_ACT_GELU) &&
+         (keep == LORA_KEEP_NONE || keep == LORA_KEEP_BF16 || keep == LORA_KEEP_PACKED8);
+}
+
+template <int MODE>
+lora_status launch(FfnArgs& P, int nsm, cudaStream_t st) {
+  constexpr int products = MODE == kDw ? 2 : 1;
+  P.stage_bytes = kABytes + (MODE == kFwd ? 2 : 1) * P.bn * 128;
+  P.stages = kRingBytes / P.stage_bytes < kMaxStages ? kRingBytes / P.stage_bytes : kMaxStages;
+  P.tiles_m = int(cdiv(P.m, kBM));
+  P.tiles_n = int(cdiv(P.n, P.bn));
+  const int64_t total = int64_t(products) * P.tiles_m * P.tiles_n;
+  if (total >= int64_t(1) << 31) return LORA_ERR_SHAPE;
+  P.total = int(total);
+  const int grid = P.total < nsm ? P.total : nsm;
+  return launch_pdl(ffn_gemm_kernel<MODE>, dim3(grid), dim3(kGemmThreads), kGemmSmem, st, P, status_block()) ==
+                 cudaSuccess
+             ? LORA_OK
+             : LORA_ERR_CUDA;
+}
+
+template <int MODE>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(ffn_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
+}
+
+}  // namespace
+
+cudaError_t prepare_ffn() {
+  cudaError_t e;
+  if ((e = prepare<kFwd>()) != cudaSuccess || (e = prepare<kDx>()) != cudaSuccess) return e;
+  return prepare<kDw>();
+}
+
+}  // namespace mlp
+
+using namespace mlp;
+
+extern "C" {
+
+lora_status lora_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_up, const float* delta_gate,
+                               const float* delta_up, int act, int64_t M, int64_t K, int64_t F, void* h, int keep,
+                               void* gate, void* up, void* gate_scales, void* up_scales, void* stream) {
+  if (!shape_ok(M, K, F) || !kind_ok(act, keep)) return LORA_ERR_SHAPE;
+  if (M == 0) return LORA_OK;
+  lora_status s = check_ptrs(x, w_gate, w_up, h);
+  if (s == LORA_OK && (delta_gate || delta_up)) s = check_ptrs(delta_gate, delta_up);
+  if (s == LORA_OK && keep != LORA_KEEP_NONE) s = check_ptrs(gate, up);
+  if (s == LORA_OK && keep == LORA_KEEP_PACKED8) s = check_ptrs(gate_scales, up_scales);
+  if (s != LORA_OK) return s;
+  int nsm = 0;
+  if ((s = device_ready(&nsm)) != LORA_OK) return s;
+  FfnArgs P{};
+  P.m = int(M);
+  P.n = int(F);
+  P.nk = int(cdiv(K, kBK));
+  P.bn = 128;
+  if (!tensor_map(&P.a[0], x, Elem::bf16, M, K, K, kBK, kBM, 128) ||
+      !tensor_map(&P.b[0], w_gate, Elem::bf16, F, K, K, kBK, P.bn, 128) ||
+      !tensor_map(&P.b[1], w_up, Elem::bf16, F, K, K, kBK, P.bn, 128))
+    return LORA_ERR_CUDA;
+  P.a[1] = P.a[0];
+  P.out[0] = static_cast<__nv_bfloat16*>(h);
+  P.delta[0] = delta_gate;
+  P.delta[1] = delta_up;
+  P.keep[0] = gate;
+  P.keep[1] = up;
+  P.keep_scales[0] = static_cast<uint8_t*>(gate_scales);
+  P.keep_scales[1] = static_cast<uint8_t*>(up_scales);
+  P.keep_kind = keep;
+  P.act = act;
+  return launch<kFwd>(P, nsm, static_cast<cudaStream_t>(stream));
+}
+
+lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, int keep,
+                               const void* gate, const void* up, const void* gate_scales, const void* up_scales, int act,
+                               int64_t M, int64_t K, int64_t F, void* dx, void* dgate, void* dup, void* dw_gate,
+                               void* dw_up, void* stream) {
+  if (!shape_ok(M, K, F) || !kind_ok(act, keep) || keep == LORA_KEEP_NONE) return LORA_ERR_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool dw = dw_gate || dw_up;
+  lora_status s = LORA_OK;
+  int nsm = 0;
+  if (dw) s = check_ptrs(dw_gate, dw_up);
+  if (s == LORA_OK && M > 0) s = check_ptrs(dh, w_gate, w_up, gate, up, dx, dgate, dup);
+  if (s == LORA_OK && M > 0 && dw) s = check_ptrs(x);
+  if (s == LORA_OK && M > 0 && keep == LORA_KEEP_PACKED8) s = check_ptrs(gate_scales, up_scales);
+  if (s != LORA_OK || (M == 0 && !dw)) return s;
+  if ((s = device_ready(&nsm)) != LORA_OK) return s;
+  if (M == 0) {                                     // sums over no rows
+    const size_t bytes = size_t(F) * size_t(K) * 2;
+    return cudaMemsetAsync(dw_gate, 0, bytes, st) == cudaSuccess && cudaMemsetAsync(dw_up, 0, bytes, st) == cudaSuccess
+               ? LORA_OK
+               : LORA_ERR_CUDA;
+  }
+  const int64_t want = cdiv(M * (F / 8), 256), most = int64_t(nsm) * 16;
+  const dim3 grid(unsigned(want < most ? want : most));
+  const int f = int(F);
+  const cudaError_t e =
+      keep == LORA_KEEP_BF16
+          ? launch_pdl(ffn_grad_kernel<kBf16>, grid, dim3(256), 0, st, dh, gate, up, gate_scales, up_scales, act, M, f, dgate, dup)
+          : launch_pdl(ffn_grad_kernel<kPacked>, grid, dim3(256), 0, st, dh, gate, up, gate_scales, up_scales, act, M, f, dgate, dup);
+  if (e != cudaSuccess) return LORA_ERR_CUDA;
+  FfnArgs P{};
+  P.m = int(M);
+  P.n = int(K);
+  P.nk = int(cdiv(F, kBK));
+  P.bn = 256;
+  if (!tensor_map(&P.a[0], dgate, Elem::bf16, M, F, F, kBK, kBM, 128) ||
+      !tensor_map(&P.a[1], dup, Elem::bf16, M, F, F, kBK, kBM, 128) ||
+      !tensor_map(&P.b[0], w_gate, Elem::bf16, F, K, K, 64, kBK, 128) ||
+      !tensor_map(&P.b[1], w_up, Elem::bf16, F, K, K, 64, kBK, 128))
+    return LORA_ERR_CUDA;
+  P.out[0] = static_cast<__nv_bfloat16*>(dx);
+  if ((s = launch<kDx>(P, nsm, st)) != LORA_OK || !dw) return s;
+  FfnArgs Q{};
+  Q.m = f;
+  Q.n = int(K);
+  Q.nk = int(cdiv(M, kBK));
+  Q.bn = 256;
+  if (!tensor_map(&Q.a[0], dgate, Elem::bf16, M, F, F, 64, kBK, 128) ||
+      !tensor_map(&Q.a[1], dup, Elem::bf16, M, F, F, 64, kBK, 128) ||
+      !tensor_map(&Q.b[0], x, Elem::bf16, M, K, K, 64, kBK, 128))
+    return LORA_ERR_CUDA;
+  Q.b[1] = Q.b[0];
+  Q.out[0] = static_cast<__nv_bfloat16*>(dw_gate);
+  Q.out[1] = static_cast<__nv_bfloat16*>(dw_up);
+  return launch<kDw>(Q, nsm, st);
+}
+
+}  // extern "C"

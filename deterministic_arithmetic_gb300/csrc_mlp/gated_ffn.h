@@ -1,0 +1,27 @@
+// gated_ffn.h -- arguments of the gated feed-forward block's tensor-core kernel.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace mlp {
+
+constexpr int kFwd = 0, kDx = 1, kDw = 2;          // the kernel's products (gemm.cuh)
+constexpr uint32_t kKindFfn = 16, kSiteFfn = 64;   // status block: kind kKindFfn + product, sites from kSiteFfn
+
+struct FfnArgs {
+  CUtensorMap a[2], b[2];          // kFwd: x | Wg, Wu.  kDx: dG, dU | Wg, Wu.  kDw: dG, dU | x
+  __nv_bfloat16* out[2];           // [m][n]: h | dx | dWg, dWu
+  const float* delta[2];           // kFwd: Dg, Du [m][n], or null
+  void* keep[2];                   // kFwd: G and U, kept as keep_kind says
+  uint8_t* keep_scales[2];
+  int keep_kind, act;
+  int m, n;                        // rows and columns of the outputs
+  int nk;                          // 64-deep blocks of one product's reduction
+  int bn;                          // tile columns (in kFwd of each projection)
+  int stages, stage_bytes;
+  int tiles_m, tiles_n, total;     // tiles of one product; of the launch
+};
+
+}  // namespace mlp

@@ -1,0 +1,320 @@
+// gemm.cuh -- the tensor-core kernel of the gated feed-forward block: bf16 operands by TMA into
+// 128-byte-swizzled shared memory, tcgen05 MMAs into FP32 accumulators in TMEM, three products:
+//   kFwd  G = x Wg^T and U = x Wu^T over the same x tile, and in the epilogue h = act(G + Dg) (U + Du),
+//         with G + Dg and U + Du kept in bf16 or in 8 bits when asked for
+//   kDx   dx = dG Wg + dU Wu, one accumulator over both products
+//   kDw   dWg = dG^T x and dWu = dU^T x
+//
+// An accumulator takes its whole reduction in order, 16 products at a time, from a cleared start:
+// no split over the reduction, so an output's bits do not depend on the tile it falls into, nor on
+// how many rows the batch has. FP32 accumulation; each output is rounded to bf16 once, in the
+// epilogue.
+//
+// Persistent CTAs take tiles in turn. Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 read the
+// accumulator and write the tile (a warp its quarter of the lanes, the two halves of the warps
+// alternate 32-column chunks); two accumulators of 256 TMEM columns let a tile's epilogue run under
+// the next tile's MMAs.
+#pragma once
+
+#include "../csrc/common.cuh"
+#include "../csrc/kernels.h"
+#include "elems.cuh"
+#include "gated_ffn.h"
+#include "mlp.h"
+#include "pack8.cuh"
+
+namespace mlp {
+
+using namespace lora;
+
+constexpr int kBM = 128, kBK = 64;                 // rows of A and depth of a k-block
+constexpr int kABytes = kBM * kBK * 2;             // 16 KB
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 208 * 1024;             // the operand ring
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
+constexpr int kAccCols = 256;                      // TMEM columns of an accumulator
+constexpr size_t kGemmSmem = kRingBytes + 1024 + (2 * kMaxStages + 6) * 8 + 16;
+static_assert(kGemmSmem < 227 * 1024, "shared memory of a CTA");
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// act(y) = y p and its slope p + y p (1 - p) z', with p = 1 / (1 + exp(-z)): z = y for silu; for gelu in
+// its tanh form 0.5 y (1 + tanh(s)) = y / (1 + exp(-2 s)), z = 2 s = sqrt(8 / pi) (y + 0.044715 y^3).
+__device__ __forceinline__ float act_p(int act, float y) {
+  const float z = act == LORA_ACT_SILU ? y : 1.5957691216057308f * fmaf(0.044715f * y * y, y, y);
+  return __fdividef(1.f, 1.f + __expf(-z));        // exp overflowing to infinity gives 0
+}
+__device__ __forceinline__ float act_slope(int act, float y, float p) {
+  const float q = 1.f - p;
+  if (p == 0.f || q == 0.f) return p;              // the tails: the second term is 0, its factors may be infinite
+  const float dz = act == LORA_ACT_SILU ? 1.f : 1.5957691216057308f * fmaf(0.134145f * y, y, 1.f);
+  return fmaf(y * p, q * dz, p);
+}
+
+// 32 consecutive columns from `col` of a row, as bf16 (columns at or past n are left alone; n % 8 == 0).
+__device__ __forceinline__ void store_row32(__nv_bfloat16* row, int col, int n, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col + 8 * j < n)
+      *reinterpret_cast<uint4*>(row + col + 8 * j) =
+          make_uint4(bf16x2_bits(v[8 * j], v[8 * j + 1]), bf16x2_bits(v[8 * j + 2], v[8 * j + 3]),
+                     bf16x2_bits(v[8 * j + 4], v[8 * j + 5]), bf16x2_bits(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// One of the forward's kept values of a row, 32 columns from `col` (a multiple of 32 when packed).
+__device__ __forceinline__ void keep_row32(const FfnArgs& P, int which, int64_t row, int col, float (&v)[32]) {
+  if (P.keep_kind == LORA_KEEP_BF16) {
+    store_row32(static_cast<__nv_bfloat16*>(P.keep[which]) + row * P.n, col, P.n, v);
+    return;
+  }
+  const int G = (P.n + 31) >> 5;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    if (col + i >= P.n) v[i] = 0.f;                // the padding of the last group (never read from here on)
+    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  }
+  const uint32_t s = scale_byte(m);
+  const float inv = inv_step(s);
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[i] |= (uint32_t(code_of(v[4 * i + e], inv, s)) & 0xFFu) << (8 * e);
+  }
+  uint4* q = reinterpret_cast<uint4*>(static_cast<int8_t*>(P.keep[which]) + (row * G + (col >> 5)) * 32);
+  q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  P.keep_scales[which][row * G + (col >> 5)] = uint8_t(s);
+}
+
+// Tiles in groups of up to 16 row tiles, row tiles fastest: the CTAs at work together then share a
+// few column tiles and the operand rows of at most 16 row tiles, which stay in L2.
+__device__ __forceinline__ void tile_of(const FfnArgs& P, int u, int* tm, int* tn) {
+  const int group = u / (16 * P.tiles_n), m0 = 16 * group;
+  const int gm = min(16, P.tiles_m - m0);
+  const int r = u - 16 * group * P.tiles_n;
+  *tm = m0 + r % gm;
+  *tn = r / gm;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs P, uint32_t* status) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kRingBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+  auto tfull = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
+  const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 4);
+  const uint32_t never = drain + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int stages = P.stages, stage_bytes = P.stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(never, 1);
+    *abort_flag = 0u;
+    mbar_fence_init();
+    for (int i = 0; i < 2; ++i) {
+      prefetch_map(&P.a[i]);
+      prefetch_map(&P.b[i]);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const Abort ab = make_abort(abort_flag, status);
+
+  const int per = P.tiles_m * P.tiles_n;           // tiles of one product (kDw has two)
+  const int blocks = MODE == kDx ? 2 * P.nk : P.nk;
+  const int bcols = MODE == kFwd ? 2 * P.bn : P.bn;  // accumulator columns
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      if (stall_requested(status, kKindFfn + MODE)) stall_wait(never, ab, kSiteFfn + 1);   // test hook
+      const uint64_t keep = policy_evict_last();
+      int idx = 0;
+      uint32_t phase = 0, issued = 0, parities = 0;
+      for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+        const int prod = MODE == kDw ? u / per : 0;
+        int tm, tn;
+        tile_of(P, u - prod * per, &tm, &tn);
+        for (int kb = 0; kb < blocks; ++kb) {
+          if (wait(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
+            const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + kABytes, bar = full(idx);
+            mbar_expect_tx(bar, uint32_t(stage_bytes));
+            if constexpr (MODE == kFwd) {
+              tma_load(st, &P.a[0], bar, kb * kBK, tm * kBM, keep);
+              tma_load(sb, &P.b[0], bar, kb * kBK, tn * P.bn, keep);
+              tma_load(sb + P.bn * 128, &P.b[1], bar, kb * kBK, tn * P.bn, keep);
+            } else if constexpr (MODE == kDx) {
+              const int h = kb >= P.nk, k0 = (kb - h * P.nk) * kBK;
+              tma_load(st, &P.a[h], bar, k0, tm * kBM, keep);
+              for (int j = 0; j < P.bn / 64; ++j) tma_load(sb + j * 8192, &P.b[h], bar, tn * P.bn + 64 * j, k0, keep);
+            } else {
+              for (int j = 0; j < 2; ++j) tma_load(st + j * 8192, &P.a[prod], bar, tm * kBM + 64 * j, kb * kBK, keep);
+              for (int j = 0; j < P.bn / 64; ++j) tma_load(sb + j * 8192, &P.b[0], bar, tn * P.bn + 64 * j, kb * kBK, keep);
+            }
+            issued |= 1u << idx;
+            parities = (parities & ~(1u << idx)) | (phase << idx);
+          }
+          if (++idx == stages) idx = 0, phase ^= 1u;
+        }
+      }
+      for (int s = 0; s < stages; ++s)
+        if (issued & (1u << s)) wait_drain(full(s), (parities >> s) & 1u, ab, kSiteFfn + 3);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer
+    const uint32_t idesc = idesc_bf16(kBM, bcols, MODE == kDw, MODE != kFwd);
+    // K-major operands step 32 bytes inside the swizzle span per 16 of the reduction; MN-major
+    // ones (64-column blocks 8 KB apart) step 16 rows of 128 bytes.
+    constexpr uint32_t a_step = MODE == kDw ? 2048u : 32u, b_step = MODE == kFwd ? 32u : 2048u;
+    const uint64_t a0 = smem_desc(base, MODE == kDw ? 8192u : 16u, 1024u, kLayoutSW128);
+    const uint64_t b0 = smem_desc(base + kABytes, MODE == kFwd ? 16u : 8192u, 1024u, kLayoutSW128);
+    int idx = 0, buf = 0;
+    uint32_t phase = 0, tphase = 0;
+    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+      bool ok = __all_sync(0xffffffffu, wait(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
+      tc_fence_after();
+      const uint32_t d = tmem + buf * kAccCols;
+      for (int kb = 0; kb < blocks; ++kb) {
+        ok = __all_sync(0xffffffffu, ok && wait(full(idx), phase, ab, kSiteFfn + 5));
+        if (ok) {
+          tc_fence_after();
+          const uint32_t off = uint32_t(idx) * stage_bytes;
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < kBK / 16; ++j)
+              mma_bf16(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
+                       (kb | j) ? 1u : 0u);
+            mma_commit(empty(idx));
+            if (kb + 1 == blocks) mma_commit(tfull(buf));
+          }
+          __syncwarp();
+        }
+        if (++idx == stages) idx = 0, phase ^= 1u;
+      }
+      buf ^= 1;
+      if (!buf) tphase ^= 1u;
+    }
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    wait_drain(drain, 0u, ab, kSiteFfn + 6);
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes = uint32_t(q * 32) << 16;
+    int buf = 0;
+    uint32_t tphase = 0;
+    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+      const int prod = MODE == kDw ? u / per : 0;
+      int tm, tn;
+      tile_of(P, u - prod * per, &tm, &tn);
+      const bool ok = __all_sync(0xffffffffu, wait(tfull(buf), tphase, ab, kSiteFfn + 7));
+      tc_fence_after();
+      const int64_t row = int64_t(tm) * kBM + q * 32 + lane;
+      const uint32_t acc = tmem + buf * kAccCols + lanes;
+      if (ok) {
+        for (int c = 32 * half; c < P.bn; c += 64) {
+          const int col = tn * P.bn + c;
+          if (col >= P.n) break;
+          uint32_t r0[32];
+          tmem_ld32(acc + c, r0);
+          if constexpr (MODE == kFwd) {
+            uint32_t r1[32];
+            tmem_ld32(acc + P.bn + c, r1);
+            tmem_ld_wait();
+            reg_fence(r0);
+            reg_fence(r1);
+            if (row < P.m) {
+              float g[32], v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                g[i] = __uint_as_float(r0[i]);
+                v[i] = __uint_as_float(r1[i]);
+              }
+              if (P.delta[0]) {
+                const float* dg = P.delta[0] + row * P.n + col;
+                const float* du = P.delta[1] + row * P.n + col;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (col + 4 * j < P.n) {
+                    const float4 a = __ldcs(reinterpret_cast<const float4*>(dg) + j);
+                    const float4 b = __ldcs(reinterpret_cast<const float4*>(du) + j);
+                    g[4 * j] += a.x; g[4 * j + 1] += a.y; g[4 * j + 2] += a.z; g[4 * j + 3] += a.w;
+                    v[4 * j] += b.x; v[4 * j + 1] += b.y; v[4 * j + 2] += b.z; v[4 * j + 3] += b.w;
+                  }
+              }
+              float h[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) h[i] = g[i] * act_p(P.act, g[i]) * v[i];
+              store_row32(P.out[0] + row * P.n, col, P.n, h);
+              if (P.keep_kind != LORA_KEEP_NONE) {
+                keep_row32(P, 0, row, col, g);
+                keep_row32(P, 1, row, col, v);
+              }
+            }
+          } else {
+            tmem_ld_wait();
+            reg_fence(r0);
+            if (row < P.m) {
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r0[i]);
+              store_row32(P.out[prod] + row * P.n, col, P.n, v);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(tempty(buf));
+      buf ^= 1;
+      if (!buf) tphase ^= 1u;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace mlp
