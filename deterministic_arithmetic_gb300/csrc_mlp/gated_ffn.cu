@@ -55,26 +55,63 @@ bool kind_ok(int act, int keep) {
          (keep == LORA_KEEP_NONE || keep == LORA_KEEP_BF16 || keep == LORA_KEEP_PACKED8);
 }
 
-template <int MODE>
-lora_status launch(FfnArgs& P, int nsm, cudaStream_t st) {
+// Pairs of CTAs that fit on the device at once (0: not yet asked).
+int g_pairs = 0;
+
+template <int MODE, int CG>
+lora_status launch_as(FfnArgs& P, int nsm, cudaStream_t st) {
   constexpr int products = MODE == kDw ? 2 : 1;
-  P.stage_bytes = kABytes + (MODE == kFwd ? 2 : 1) * P.bn * 128;
+  P.stage_bytes = kABytes + (MODE == kFwd ? 2 : 1) * P.bn * 128 / CG;
   P.stages = kRingBytes / P.stage_bytes < kMaxStages ? kRingBytes / P.stage_bytes : kMaxStages;
-  P.tiles_m = int(cdiv(P.m, kBM));
+  P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, P.bn));
   const int64_t total = int64_t(products) * P.tiles_m * P.tiles_n;
   if (total >= int64_t(1) << 31) return LORA_ERR_SHAPE;
   P.total = int(total);
-  const int grid = P.total < nsm ? P.total : nsm;
-  return launch_pdl(ffn_gemm_kernel<MODE>, dim3(grid), dim3(kGemmThreads), kGemmSmem, st, P, status_block()) ==
-                 cudaSuccess
-             ? LORA_OK
-             : LORA_ERR_CUDA;
+  const int most = CG == 2 ? g_pairs : nsm;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(CG * (P.total < most ? P.total : most)));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {unsigned(CG), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<MODE, CG>, P, status_block()) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
+// Pairs of CTAs where the output has more rows than one CTA's and the 256 x 256 tiles give every
+// pair one; CTAs alone otherwise.
+template <int MODE>
+lora_status launch(FfnArgs& P, int nsm, cudaStream_t st) {
+  const int64_t tiles = (MODE == kDw ? 2 : 1) * cdiv(P.m, 2 * kBM) * cdiv(P.n, P.bn);
+  return P.m > kBM && tiles >= g_pairs ? launch_as<MODE, 2>(P, nsm, st) : launch_as<MODE, 1>(P, nsm, st);
 }
 
 template <int MODE>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(ffn_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
+  cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<MODE, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(ffn_gemm_kernel<MODE, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<MODE, 2>, &cfg);
+  if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) g_pairs = n;
+  return e;
 }
 
 }  // namespace

@@ -10,7 +10,13 @@
 // how many rows the batch has. FP32 accumulation; each output is rounded to bf16 once, in the
 // epilogue.
 //
-// Persistent CTAs take tiles in turn. Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 read the
+// CG = 2 works in pairs of CTAs (a cluster of two neighbouring SMs, cta_group::2): a 256 x 256 tile,
+// each CTA holding 128 rows of A, half of B's columns and the accumulator of its rows, so that each
+// operand byte in shared memory feeds twice the products of a CTA alone. The pair's first CTA
+// issues the MMAs of both; copies of both arrive at its barriers. CG = 1 is a CTA alone with 128
+// rows and bn columns, for batches and outputs too small to give every pair a tile.
+//
+// Persistent CTAs (pairs) take tiles in turn. Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 read the
 // accumulator and write the tile (a warp its quarter of the lanes, the two halves of the warps
 // alternate 32-column chunks); two accumulators of 256 TMEM columns let a tile's epilogue run under
 // the next tile's MMAs.
@@ -47,6 +53,72 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+
+// ------------------------------------------------------------ pairs of CTAs
+// The same operations as common.cuh's, for cta_group::2. `bar` of a copy is the address of the first
+// CTA's barrier (peer_addr), dst the caller's own shared memory.
+template <int CG>
+__device__ __forceinline__ void load2d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, uint64_t policy) {
+  if constexpr (CG == 1) {
+    tma_load(dst, m, bar, x, y, policy);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1) {
+    mma_bf16(d, a, b, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrive on `bar` (with CG = 2: on that barrier of both CTAs) once the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1) {
+    mma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(uint16_t(3))
+        : "memory");
+  }
+}
+// The same on the caller's barrier alone.
+template <int CG>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (CG == 1)
+    mma_commit(bar);
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void acc_alloc(uint32_t slot) {
+  if constexpr (CG == 1) {
+    tmem_alloc(slot, 512);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void acc_free(uint32_t taddr) {
+  if constexpr (CG == 1)
+    tmem_dealloc(taddr, 512);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(512) : "memory");
 }
 
 // act(y) = y p and its slope p + y p (1 - p) z', with p = 1 / (1 + exp(-z)): z = y for silu; for gelu in
@@ -110,7 +182,7 @@ __device__ __forceinline__ void tile_of(const FfnArgs& P, int u, int* tm, int* t
   *tn = r / gm;
 }
 
-template <int MODE>
+template <int MODE, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs P, uint32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -127,6 +199,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const uint32_t warp = warp_id(), lane = lane_id();
+  const int rank = CG == 2 ? int(cluster_rank()) : 0;       // 0 issues the MMAs
   const int stages = P.stages, stage_bytes = P.stage_bytes;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -135,7 +208,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), kEpiWarps);
+      mbar_init(tempty(b), CG * kEpiWarps);
     }
     mbar_init(drain, 1);
     mbar_init(never, 1);
@@ -146,12 +219,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       prefetch_map(&P.b[i]);
     }
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
+  __syncwarp();
+  if (warp == 1) acc_alloc<CG>(smem_u32(tmem_slot));
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();       // the peer's barriers are set up before anything arrives there
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
@@ -161,6 +233,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   const int per = P.tiles_m * P.tiles_n;           // tiles of one product (kDw has two)
   const int blocks = MODE == kDx ? 2 * P.nk : P.nk;
   const int bcols = MODE == kFwd ? 2 * P.bn : P.bn;  // accumulator columns
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -169,25 +242,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const uint64_t keep = policy_evict_last();
       int idx = 0;
       uint32_t phase = 0, issued = 0, parities = 0;
-      for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+      for (int u = first; u < P.total; u += step) {
         const int prod = MODE == kDw ? u / per : 0;
         int tm, tn;
         tile_of(P, u - prod * per, &tm, &tn);
+        const int row0 = (tm * CG + rank) * kBM;                      // this CTA's rows of A
+        const int col0 = tn * P.bn + (CG == 2 ? rank * 128 : 0);      // kDx, kDw: its columns of B
         for (int kb = 0; kb < blocks; ++kb) {
           if (wait(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
-            const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + kABytes, bar = full(idx);
-            mbar_expect_tx(bar, uint32_t(stage_bytes));
+            const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + kABytes;
+            const uint32_t bar = CG == 2 ? peer_addr(full(idx), 0) : full(idx);
+            if (rank == 0) mbar_expect_tx(full(idx), uint32_t(CG * stage_bytes));
             if constexpr (MODE == kFwd) {
-              tma_load(st, &P.a[0], bar, kb * kBK, tm * kBM, keep);
-              tma_load(sb, &P.b[0], bar, kb * kBK, tn * P.bn, keep);
-              tma_load(sb + P.bn * 128, &P.b[1], bar, kb * kBK, tn * P.bn, keep);
-            } else if constexpr (MODE == kDx) {
-              const int h = kb >= P.nk, k0 = (kb - h * P.nk) * kBK;
-              tma_load(st, &P.a[h], bar, k0, tm * kBM, keep);
-              for (int j = 0; j < P.bn / 64; ++j) tma_load(sb + j * 8192, &P.b[h], bar, tn * P.bn + 64 * j, k0, keep);
+              load2d<CG>(st, &P.a[0], bar, kb * kBK, row0, keep);
+              if constexpr (CG == 2) {             // the pair's columns: 128 of the gate, 128 of up
+                load2d<CG>(sb, &P.b[rank], bar, kb * kBK, tn * P.bn, keep);
+              } else {
+                load2d<CG>(sb, &P.b[0], bar, kb * kBK, tn * P.bn, keep);
+                load2d<CG>(sb + P.bn * 128, &P.b[1], bar, kb * kBK, tn * P.bn, keep);
+              }
             } else {
-              for (int j = 0; j < 2; ++j) tma_load(st + j * 8192, &P.a[prod], bar, tm * kBM + 64 * j, kb * kBK, keep);
-              for (int j = 0; j < P.bn / 64; ++j) tma_load(sb + j * 8192, &P.b[0], bar, tn * P.bn + 64 * j, kb * kBK, keep);
+              const int h = MODE == kDx && kb >= P.nk;
+              const int k0 = (kb - h * P.nk) * kBK;
+              if constexpr (MODE == kDx) {
+                load2d<CG>(st, &P.a[h], bar, k0, row0, keep);
+              } else {
+                load2d<CG>(st, &P.a[prod], bar, row0, k0, keep);
+                load2d<CG>(st + 8192, &P.a[prod], bar, row0 + 64, k0, keep);
+              }
+              for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, &P.b[h], bar, col0 + 64 * j, k0, keep);
             }
             issued |= 1u << idx;
             parities = (parities & ~(1u << idx)) | (phase << idx);
@@ -195,59 +278,70 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
           if (++idx == stages) idx = 0, phase ^= 1u;
         }
       }
-      for (int s = 0; s < stages; ++s)
-        if (issued & (1u << s)) wait_drain(full(s), (parities >> s) & 1u, ab, kSiteFfn + 3);
+      if (rank == 0) {                             // the copies of both CTAs arrive here
+        for (int s = 0; s < stages; ++s)
+          if (issued & (1u << s)) wait_drain(full(s), (parities >> s) & 1u, ab, kSiteFfn + 3);
+      } else if (*ab.flag) {
+        // Giving up: this CTA's copies report to the other one's barriers, which may no longer be
+        // waited on. They land long before this; the tile loop's own waits see to them otherwise.
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainLimitNs;) {
+        }
+      }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    const uint32_t idesc = idesc_bf16(kBM, bcols, MODE == kDw, MODE != kFwd);
-    // K-major operands step 32 bytes inside the swizzle span per 16 of the reduction; MN-major
-    // ones (64-column blocks 8 KB apart) step 16 rows of 128 bytes.
-    constexpr uint32_t a_step = MODE == kDw ? 2048u : 32u, b_step = MODE == kFwd ? 32u : 2048u;
-    const uint64_t a0 = smem_desc(base, MODE == kDw ? 8192u : 16u, 1024u, kLayoutSW128);
-    const uint64_t b0 = smem_desc(base + kABytes, MODE == kFwd ? 16u : 8192u, 1024u, kLayoutSW128);
-    int idx = 0, buf = 0;
-    uint32_t phase = 0, tphase = 0;
-    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
-      bool ok = __all_sync(0xffffffffu, wait(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
-      tc_fence_after();
-      const uint32_t d = tmem + buf * kAccCols;
-      for (int kb = 0; kb < blocks; ++kb) {
-        ok = __all_sync(0xffffffffu, ok && wait(full(idx), phase, ab, kSiteFfn + 5));
-        if (ok) {
-          tc_fence_after();
-          const uint32_t off = uint32_t(idx) * stage_bytes;
-          if (elect_one()) {
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16(CG * kBM, bcols, MODE == kDw, MODE != kFwd);
+      // K-major operands step 32 bytes inside the swizzle span per 16 of the reduction; MN-major
+      // ones (64-column blocks 8 KB apart) step 16 rows of 128 bytes.
+      constexpr uint32_t a_step = MODE == kDw ? 2048u : 32u, b_step = MODE == kFwd ? 32u : 2048u;
+      const uint64_t a0 = smem_desc(base, MODE == kDw ? 8192u : 16u, 1024u, kLayoutSW128);
+      const uint64_t b0 = smem_desc(base + kABytes, MODE == kFwd ? 16u : 8192u, 1024u, kLayoutSW128);
+      int idx = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
+      for (int u = first; u < P.total; u += step) {
+        bool ok = CG == 2 ? wait_cluster(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4)
+                          : wait(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kAccCols;
+        for (int kb = 0; kb < blocks; ++kb) {
+          ok = __all_sync(0xffffffffu, ok && wait(full(idx), phase, ab, kSiteFfn + 5));
+          if (ok) {
+            tc_fence_after();
+            const uint32_t off = uint32_t(idx) * stage_bytes;
+            if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < kBK / 16; ++j)
-              mma_bf16(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
-                       (kb | j) ? 1u : 0u);
-            mma_commit(empty(idx));
-            if (kb + 1 == blocks) mma_commit(tfull(buf));
+              for (int j = 0; j < kBK / 16; ++j)
+                mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
+                        (kb | j) ? 1u : 0u);
+              commit<CG>(empty(idx));
+              if (kb + 1 == blocks) commit<CG>(tfull(buf));
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (++idx == stages) idx = 0, phase ^= 1u;
         }
-        if (++idx == stages) idx = 0, phase ^= 1u;
+        buf ^= 1;
+        if (!buf) tphase ^= 1u;
       }
-      buf ^= 1;
-      if (!buf) tphase ^= 1u;
+      if (elect_one()) commit_here<CG>(drain);
+      __syncwarp();
+      wait_drain(drain, 0u, ab, kSiteFfn + 6);
     }
-    if (elect_one()) mma_commit(drain);
-    __syncwarp();
-    wait_drain(drain, 0u, ab, kSiteFfn + 6);
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = uint32_t(q * 32) << 16;
     int buf = 0;
     uint32_t tphase = 0;
-    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+    for (int u = first; u < P.total; u += step) {
       const int prod = MODE == kDw ? u / per : 0;
       int tm, tn;
       tile_of(P, u - prod * per, &tm, &tn);
       const bool ok = __all_sync(0xffffffffu, wait(tfull(buf), tphase, ab, kSiteFfn + 7));
       tc_fence_after();
-      const int64_t row = int64_t(tm) * kBM + q * 32 + lane;
+      const int64_t row = int64_t(tm * CG + rank) * kBM + q * 32 + lane;
       const uint32_t acc = tmem + buf * kAccCols + lanes;
       if (ok) {
         for (int c = 32 * half; c < P.bn; c += 64) {
@@ -303,17 +397,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       }
       tc_fence_before();
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(tempty(buf));
+      if (ok && lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_peer(peer_addr(tempty(buf), 0));
+        else mbar_arrive(tempty(buf));
+      }
       buf ^= 1;
       if (!buf) tphase ^= 1u;
     }
   }
 
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();       // no CTA leaves while its peer may still signal it
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    acc_free<CG>(tmem);
   }
 }
 

@@ -55,7 +55,8 @@ def within(name, got, ref, bound):
 
 
 SHAPES = [(1, 8, 8), (7, 64, 40), (1, 520, 1000), (16, 72, 128), (128, 128, 256), (129, 200, 136), (300, 520, 264),
-          (257, 1000, 72), (64, 5120, 512), (600, 264, 2056), (1000, 640, 1096)]
+          (257, 1000, 72), (64, 5120, 512), (600, 264, 2056), (1000, 640, 1096), (1300, 4104, 520),
+          (2600, 72, 4104)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -163,7 +164,7 @@ def test_backward_against_differences(act):
         assert abs((ends[0] - ends[1]) / (2 * h) - got) <= 2.0 ** -6 * np.linalg.norm(R.f64(grad)) * np.linalg.norm(v)
 
 
-@pytest.mark.parametrize("M,K,F", [(700, 264, 520), (1500, 512, 1024), (2600, 128, 4104)])
+@pytest.mark.parametrize("M,K,F", [(700, 264, 520), (1500, 512, 1024), (2600, 128, 4104), (1300, 4104, 520)])
 def test_rows_do_not_depend_on_the_batch(M, K, F):
     from deterministic_arithmetic_gb300 import gated_ffn as ffn
 
