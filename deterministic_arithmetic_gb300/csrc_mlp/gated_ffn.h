@@ -20,8 +20,11 @@ struct FfnArgs {
   int m, n;                        // rows and columns of the outputs
   int nk;                          // 64-deep blocks of one product's reduction
   int bn;                          // tile columns (in kFwd of each projection)
+  int blocked;                     // kDx, kDw: the maps whose rows lie along the reduction are block_map's
   int stages, stage_bytes;
-  int tiles_m, tiles_n, total;     // tiles of one product; of the launch
+  int copy_bytes;                  // what a CTA's copies of a stage bring (a small batch's rows of A are fewer)
+  int tiles_m, tiles_n;            // tiles of one product
+  int whole, total;                // units of work: `whole` tiles, then halves of the remaining ones
 };
 
 }  // namespace mlp

@@ -70,6 +70,27 @@ __device__ __forceinline__ void load2d(uint32_t dst, const CUtensorMap* m, uint3
         : "memory");
   }
 }
+// A box of a block_map: 64-column blocks from block z, rows from y.
+template <int CG>
+__device__ __forceinline__ void load3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int y, int z, uint64_t policy) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(y), "r"(z), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t policy_normal() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 template <int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (CG == 1) {
@@ -172,14 +193,30 @@ __device__ __forceinline__ void keep_row32(const FfnArgs& P, int which, int64_t 
   P.keep_scales[which][row * G + (col >> 5)] = uint8_t(s);
 }
 
-// Tiles in groups of up to 16 row tiles, row tiles fastest: the CTAs at work together then share a
-// few column tiles and the operand rows of at most 16 row tiles, which stay in L2.
-__device__ __forceinline__ void tile_of(const FfnArgs& P, int u, int* tm, int* tn) {
-  const int group = u / (16 * P.tiles_n), m0 = 16 * group;
+// A unit of work: a tile, or (pairs only, the last round's) the left or right half of one's columns.
+// Tiles lie in groups of up to 16 row tiles, row tiles fastest: the CTAs at work together then share
+// a few column tiles and the operand rows of at most 16 row tiles, which stay in L2.
+struct Unit {
+  int prod, tm, col, bn;           // product (kDw), row tile, first column and columns (of each projection in kFwd)
+};
+template <int MODE, int CG>
+__device__ __forceinline__ Unit unit_at(const FfnArgs& P, int u) {
+  int tile = u, half = -1;
+  if (CG == 2 && u >= P.whole) {
+    tile = P.whole + (u - P.whole) / 2;
+    half = (u - P.whole) & 1;
+  }
+  Unit w;
+  const int per = P.tiles_m * P.tiles_n;
+  w.prod = MODE == kDw ? tile / per : 0;
+  tile -= w.prod * per;
+  const int group = tile / (16 * P.tiles_n), m0 = 16 * group;
   const int gm = min(16, P.tiles_m - m0);
-  const int r = u - 16 * group * P.tiles_n;
-  *tm = m0 + r % gm;
-  *tn = r / gm;
+  const int r = tile - 16 * group * P.tiles_n;
+  w.tm = m0 + r % gm;
+  w.bn = half < 0 ? P.bn : P.bn / 2;
+  w.col = (r / gm) * P.bn + (half == 1 ? w.bn : 0);
+  return w;
 }
 
 template <int MODE, int CG>
@@ -230,47 +267,52 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   grid_dependents_launch();
   const Abort ab = make_abort(abort_flag, status);
 
-  const int per = P.tiles_m * P.tiles_n;           // tiles of one product (kDw has two)
   const int blocks = MODE == kDx ? 2 * P.nk : P.nk;
-  const int bcols = MODE == kFwd ? 2 * P.bn : P.bn;  // accumulator columns
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       if (stall_requested(status, kKindFfn + MODE)) stall_wait(never, ab, kSiteFfn + 1);   // test hook
-      const uint64_t keep = policy_evict_last();
+      // x is read again by every column of tiles (kFwd) or every group of row tiles (kDw): it stays
+      // in L2. The rest is shared by the CTAs at work at one time only.
+      const uint64_t keep = policy_evict_last(), once = policy_normal();
+      const uint64_t pa = MODE == kFwd ? keep : once, pb = MODE == kDw ? keep : once;
       int idx = 0;
       uint32_t phase = 0, issued = 0, parities = 0;
       for (int u = first; u < P.total; u += step) {
-        const int prod = MODE == kDw ? u / per : 0;
-        int tm, tn;
-        tile_of(P, u - prod * per, &tm, &tn);
-        const int row0 = (tm * CG + rank) * kBM;                      // this CTA's rows of A
-        const int col0 = tn * P.bn + (CG == 2 ? rank * 128 : 0);      // kDx, kDw: its columns of B
+        const Unit w = unit_at<MODE, CG>(P, u);
+        const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
+        const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
+        // the boxes are a whole tile's: half a tile uses half of what it loads
         for (int kb = 0; kb < blocks; ++kb) {
           if (wait(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
             const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + kABytes;
             const uint32_t bar = CG == 2 ? peer_addr(full(idx), 0) : full(idx);
-            if (rank == 0) mbar_expect_tx(full(idx), uint32_t(CG * stage_bytes));
+            if (rank == 0) mbar_expect_tx(full(idx), uint32_t(CG * P.copy_bytes));
             if constexpr (MODE == kFwd) {
-              load2d<CG>(st, &P.a[0], bar, kb * kBK, row0, keep);
+              load2d<CG>(st, &P.a[0], bar, kb * kBK, row0, pa);
               if constexpr (CG == 2) {             // the pair's columns: 128 of the gate, 128 of up
-                load2d<CG>(sb, &P.b[rank], bar, kb * kBK, tn * P.bn, keep);
+                load2d<CG>(sb, &P.b[rank], bar, kb * kBK, w.col, pb);
               } else {
-                load2d<CG>(sb, &P.b[0], bar, kb * kBK, tn * P.bn, keep);
-                load2d<CG>(sb + P.bn * 128, &P.b[1], bar, kb * kBK, tn * P.bn, keep);
+                load2d<CG>(sb, &P.b[0], bar, kb * kBK, w.col, pb);
+                load2d<CG>(sb + P.bn * 128, &P.b[1], bar, kb * kBK, w.col, pb);
               }
             } else {
               const int h = MODE == kDx && kb >= P.nk;
               const int k0 = (kb - h * P.nk) * kBK;
               if constexpr (MODE == kDx) {
-                load2d<CG>(st, &P.a[h], bar, k0, row0, keep);
+                load2d<CG>(st, &P.a[h], bar, k0, row0, pa);
+              } else if (P.blocked) {
+                load3d<CG>(st, &P.a[w.prod], bar, k0, row0 / 64, pa);
               } else {
-                load2d<CG>(st, &P.a[prod], bar, row0, k0, keep);
-                load2d<CG>(st + 8192, &P.a[prod], bar, row0 + 64, k0, keep);
+                load2d<CG>(st, &P.a[w.prod], bar, row0, k0, pa);
+                load2d<CG>(st + 8192, &P.a[w.prod], bar, row0 + 64, k0, pa);
               }
-              for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, &P.b[h], bar, col0 + 64 * j, k0, keep);
+              if (P.blocked)
+                load3d<CG>(sb, &P.b[h], bar, k0, col0 / 64, pb);
+              else
+                for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, &P.b[h], bar, col0 + 64 * j, k0, pb);
             }
             issued |= 1u << idx;
             parities = (parities & ~(1u << idx)) | (phase << idx);
@@ -291,7 +333,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
     if (rank == 0) {
-      const uint32_t idesc = idesc_bf16(CG * kBM, bcols, MODE == kDw, MODE != kFwd);
       // K-major operands step 32 bytes inside the swizzle span per 16 of the reduction; MN-major
       // ones (64-column blocks 8 KB apart) step 16 rows of 128 bytes.
       constexpr uint32_t a_step = MODE == kDw ? 2048u : 32u, b_step = MODE == kFwd ? 32u : 2048u;
@@ -304,6 +345,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                           : wait(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
+        const int bn = unit_at<MODE, CG>(P, u).bn;
+        const uint32_t idesc = idesc_bf16(CG * kBM, MODE == kFwd ? 2 * bn : bn, MODE == kDw, MODE != kFwd);
         const uint32_t d = tmem + buf * kAccCols;
         for (int kb = 0; kb < blocks; ++kb) {
           ok = __all_sync(0xffffffffu, ok && wait(full(idx), phase, ab, kSiteFfn + 5));
@@ -336,22 +379,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     int buf = 0;
     uint32_t tphase = 0;
     for (int u = first; u < P.total; u += step) {
-      const int prod = MODE == kDw ? u / per : 0;
-      int tm, tn;
-      tile_of(P, u - prod * per, &tm, &tn);
+      const Unit w = unit_at<MODE, CG>(P, u);
       const bool ok = __all_sync(0xffffffffu, wait(tfull(buf), tphase, ab, kSiteFfn + 7));
       tc_fence_after();
-      const int64_t row = int64_t(tm * CG + rank) * kBM + q * 32 + lane;
+      const int64_t row = int64_t(w.tm * CG + rank) * kBM + q * 32 + lane;
       const uint32_t acc = tmem + buf * kAccCols + lanes;
       if (ok) {
-        for (int c = 32 * half; c < P.bn; c += 64) {
-          const int col = tn * P.bn + c;
+        for (int c = 32 * half; c < w.bn; c += 64) {
+          const int col = w.col + c;
           if (col >= P.n) break;
           uint32_t r0[32];
           tmem_ld32(acc + c, r0);
           if constexpr (MODE == kFwd) {
             uint32_t r1[32];
-            tmem_ld32(acc + P.bn + c, r1);
+            tmem_ld32(acc + w.bn + c, r1);
             tmem_ld_wait();
             reg_fence(r0);
             reg_fence(r1);
@@ -390,7 +431,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r0[i]);
-              store_row32(P.out[prod] + row * P.n, col, P.n, v);
+              store_row32(P.out[w.prod] + row * P.n, col, P.n, v);
             }
           }
         }

@@ -85,6 +85,16 @@ bool tensor_map(CUtensorMap* m, const void* ptr, Elem e, int64_t rows, int64_t c
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool block_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int box_rows, int blocks) {
+  cuuint64_t dims[3] = {64, cuuint64_t(rows), cuuint64_t(cols / 64)};
+  cuuint64_t strides[2] = {cuuint64_t(cols) * 2, 128};
+  cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(blocks)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace mlp
 
 extern "C" {

@@ -46,5 +46,8 @@ uint32_t* status_block();
 enum class Elem { bf16, u8 };
 bool tensor_map(CUtensorMap* m, const void* ptr, Elem e, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                 int box_rows, int swizzle);
+// The same bf16 tensor as 64-column blocks, [cols / 64][rows][64] (cols a multiple of 64): a box is
+// `blocks` neighbouring blocks of box_rows rows, one after the other, 128-byte swizzle.
+bool block_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols, int box_rows, int blocks);
 
 }  // namespace mlp
