@@ -1,15 +1,22 @@
-"""What the bindings of include/lora_mlp.h share: argument checks, the stream an operator runs on
-and the allocation of what it returns. Argument marshalling only; the library does the work."""
+"""What the bindings of include/lora_mlp.h share: argument checks, outputs, the stream an operator runs
+on. Argument marshalling only; the library does the work.
+
+A small call costs more here than on the GPU (a launch takes about 2 us of host time, a checked and
+allocating call about 12), so the checks read each property once, an output that was allocated here
+is not checked again, and a stream other than the current one is entered by one wrapper."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import lora_delta as _ld
 
 vp, i64, cint, f32, size_t = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1}
+BF16, F32, U8, I8 = torch.bfloat16, torch.float32, torch.uint8, torch.int8
+TYPE_CODES = {BF16: 0, F32: 1}
+empty = torch.empty
 
 _fns: dict = {}
 
@@ -24,43 +31,69 @@ def fn(name: str, argtypes: tuple, restype=cint):
     return f
 
 
-def check(t, name: str, shape: tuple, *dtypes, device=None):
-    """``t`` is a contiguous CUDA tensor of one of ``dtypes`` and of ``shape`` (on ``device``)."""
+def _refuse(t, name, shape, dtypes, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {' or '.join(map(str, dtypes))} {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: expected a tensor on {device or 'a CUDA device'}, got {t.device}")
+    where = "a CUDA device" if device is None or device < 0 else f"cuda:{device}"
+    raise ValueError(f"{name}: expected contiguous {' or '.join(map(str, dtypes))} {tuple(shape)} on {where}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def scratch(t, device):
+def check(t, name: str, shape: tuple, dtype, device: int) -> int:
+    """The address of ``t``, a contiguous tensor of ``dtype`` and ``shape`` on CUDA device ``device``."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and device >= 0 and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, shape, (dtype,), device)
+
+
+def check_either(t, name: str, shape: tuple, device: int) -> int:
+    """The same for a bf16 or fp32 tensor."""
+    return check(t, name, shape, F32 if getattr(t, "dtype", None) is F32 else BF16, device)
+
+
+def device_of(t, name: str) -> int:
+    """The CUDA device an operator runs on: that of its first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.get_device()
+
+
+def out(t, name: str, shape: tuple, dtype, device: int):
+    """An output: the caller's tensor, checked, or a new one."""
+    if t is None:
+        return empty(shape, dtype=dtype, device=device)
+    check(t, name, shape, dtype, device)
+    return t
+
+
+def scratch(t, device: int):
     """(address, bytes) of a workspace tensor on ``device``."""
-    if not t.is_contiguous() or t.device != device:
-        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    if not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{device}, got one on {t.device}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def run_on(stream):
-    """(handle, context) of the stream an operator runs on: memory allocated inside the context
-    belongs to that stream, so a workspace is free again only behind the operator's kernels."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()), _NONE
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return int(stream.cuda_stream), torch.cuda.stream(stream)
+def stream(device: int) -> int:
+    """Handle of the current stream of ``device``."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NONE = _Nothing()
+def on_stream(f):
+    """Gives ``f`` the argument ``stream`` (a torch stream or a handle; None: the current one). ``f`` runs
+    with that stream current, so that memory it allocates belongs to the stream: a workspace is free
+    again only behind the operator's kernels."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
 def done(rc: int, name: str):

@@ -3,7 +3,8 @@ packed activations of ``include/lora_mlp.h``).
 
 A ``Packed8`` holds int8 codes and one scale byte per group of 32 elements of a row; a code times
 its power-of-two step is a bf16 value exactly, so a backward pass from the checkpoint gives bit for
-bit what it gives for the unpacked tensor. There is no fallback.
+bit what it gives for the unpacked tensor. Every call takes ``stream=`` (default: the current
+stream). There is no fallback.
 """
 from __future__ import annotations
 
@@ -19,12 +20,10 @@ GROUP = 32
 _PACK = (c.vp, c.cint, c.i64, c.i64, c.vp, c.vp, c.vp)
 _UNPACK = (c.vp, c.vp, c.i64, c.i64, c.vp, c.cint, c.vp)
 _DA = (c.vp, c.vp, c.vp, c.i64, c.i64, c.i64, c.vp, c.vp, c.size_t, c.vp)
-
-
 _BWD = (c.vp,) * 6 + (c.f32,) + (c.i64,) * 4 + (c.vp,) * 5 + (c.size_t, c.vp)
 
 
-@dataclass(frozen=True)
+@dataclass(slots=True)
 class Packed8:
     """A [rows, cols] activation in 8 bits: ``codes`` [rows, 32 * groups] int8 (zero past ``cols``),
     ``scales`` [rows, groups] uint8."""
@@ -38,108 +37,104 @@ def groups(cols: int) -> int:
     return -(-cols // GROUP)
 
 
-def _is_packed(p, name: str):
+def _cols(p, name: str) -> int:
     if not isinstance(p, Packed8):
         raise TypeError(f"{name} must be a Packed8")
+    return p.cols
 
 
-def check_packed(p: Packed8, name: str, rows: int, cols: int, device):
-    _is_packed(p, name)
+def check_packed(p: Packed8, name: str, rows: int, cols: int, device: int) -> tuple[int, int]:
+    """The addresses of the codes and scales of a Packed8 of that size."""
+    _cols(p, name)
     if p.cols != cols:
         raise ValueError(f"{name}: expected {cols} columns, got {p.cols}")
+    g = -(-cols // GROUP)
+    return (c.check(p.codes, name + ".codes", (rows, GROUP * g), c.I8, device),
+            c.check(p.scales, name + ".scales", (rows, g), c.U8, device))
+
+
+def new_packed(rows: int, cols: int, device: int) -> Packed8:
     g = groups(cols)
-    c.check(p.codes, name + ".codes", (rows, GROUP * g), torch.int8, device=device)
-    c.check(p.scales, name + ".scales", (rows, g), torch.uint8, device=device)
+    return Packed8(c.empty((rows, GROUP * g), dtype=c.I8, device=device), c.empty((rows, g), dtype=c.U8, device=device),
+                   cols)
 
 
-def new_packed(rows: int, cols: int, device) -> Packed8:
-    g = groups(cols)
-    return Packed8(torch.empty((rows, GROUP * g), dtype=torch.int8, device=device),
-                   torch.empty((rows, g), dtype=torch.uint8, device=device), cols)
-
-
-def pack8(x, *, out: Packed8 | None = None, stream=None) -> Packed8:
+@c.on_stream
+def pack8(x, *, out: Packed8 | None = None) -> Packed8:
     """The 8-bit form of ``x`` [M, K] (bf16 or fp32)."""
+    dev = c.device_of(x, "x")
     M, K = x.shape
-    c.check(x, "x", (M, K), torch.bfloat16, torch.float32)
-    handle, on = c.run_on(stream)
-    with on:
-        out = new_packed(M, K, x.device) if out is None else out
-    check_packed(out, "out", M, K, x.device)
-    c.done(c.fn("lora_pack8", _PACK)(x.data_ptr(), c.TYPE_CODES[x.dtype], M, K, out.codes.data_ptr(),
-                                     out.scales.data_ptr(), handle), "lora_pack8")
+    xp = c.check_either(x, "x", x.shape, dev)
+    if out is None:
+        out = new_packed(M, K, dev)
+        cp, sp = out.codes.data_ptr(), out.scales.data_ptr()
+    else:
+        cp, sp = check_packed(out, "out", M, K, dev)
+    c.done(c.fn("lora_pack8", _PACK)(xp, c.TYPE_CODES[x.dtype], M, K, cp, sp, c.stream(dev)), "lora_pack8")
     return out
 
 
-def unpack8(p: Packed8, *, dtype=torch.bfloat16, out=None, stream=None):
+@c.on_stream
+def unpack8(p: Packed8, *, dtype=torch.bfloat16, out=None):
     """The values ``p`` stands for, [M, K] bf16 (exact) or fp32."""
-    _is_packed(p, "p")
-    M, K = p.codes.shape[0], p.cols
-    check_packed(p, "p", M, K, p.codes.device)
-    handle, on = c.run_on(stream)
-    with on:
-        out = torch.empty((M, K), dtype=dtype, device=p.codes.device) if out is None else out
-    c.check(out, "out", (M, K), torch.bfloat16, torch.float32, device=p.codes.device)
-    c.done(c.fn("lora_unpack8", _UNPACK)(p.codes.data_ptr(), p.scales.data_ptr(), M, K, out.data_ptr(),
-                                         c.TYPE_CODES[out.dtype], handle), "lora_unpack8")
+    K = _cols(p, "p")
+    dev, M = c.device_of(p.codes, "p.codes"), p.codes.shape[0]
+    cp, sp = check_packed(p, "p", M, K, dev)
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in c.TYPE_CODES:
+        raise ValueError(f"unpack8: values of torch.bfloat16 or torch.float32, not {dtype}")
+    out = c.out(out, "out", (M, K), dtype, dev)
+    c.done(c.fn("lora_unpack8", _UNPACK)(cp, sp, M, K, out.data_ptr(), c.TYPE_CODES[dtype], c.stream(dev)),
+           "lora_unpack8")
     return out
 
 
 def pack8_da_workspace_size(M: int, K: int, R: int) -> int:
-    return int(c.fn("lora_pack8_da_workspace_size", (c.i64,) * 3, c.size_t)(M, K, R))
+    return c.fn("lora_pack8_da_workspace_size", (c.i64,) * 3, c.size_t)(M, K, R)
 
 
-def pack8_da(du, p: Packed8, *, da=None, workspace=None, stream=None):
+@c.on_stream
+def pack8_da(du, p: Packed8, *, da=None, workspace=None):
     """``dA = du.T @ x`` (fp32 [R, K]) of a packed ``x``: ``du`` [M, R] bf16. Bit for bit the dA of
     ``lora_delta_bwd`` for the unpacked x."""
-    _is_packed(p, "p")
+    dev = c.device_of(du, "du")
     M, R = du.shape
-    K = p.cols
-    c.check(du, "du", (M, R), torch.bfloat16)
-    check_packed(p, "p", M, K, du.device)
-    handle, on = c.run_on(stream)
-    with on:
-        da = torch.empty((R, K), dtype=torch.float32, device=du.device) if da is None else da
-        if workspace is None:
-            workspace = torch.empty(pack8_da_workspace_size(M, K, R), dtype=torch.uint8, device=du.device)
-    c.check(da, "da", (R, K), torch.float32, device=du.device)
-    c.done(c.fn("lora_pack8_da", _DA)(du.data_ptr(), p.codes.data_ptr(), p.scales.data_ptr(), M, K, R, da.data_ptr(),
-                                      *c.scratch(workspace, du.device), handle), "lora_pack8_da")
+    dup = c.check(du, "du", du.shape, c.BF16, dev)
+    K = _cols(p, "p")
+    cp, sp = check_packed(p, "p", M, K, dev)
+    da = c.out(da, "da", (R, K), c.F32, dev)
+    if workspace is None:
+        workspace = c.empty(pack8_da_workspace_size(M, K, R), dtype=c.U8, device=dev)
+    c.done(c.fn("lora_pack8_da", _DA)(dup, cp, sp, M, K, R, da.data_ptr(), *c.scratch(workspace, dev), c.stream(dev)),
+           "lora_pack8_da")
     return da
 
 
 def lora_delta_bwd_packed8_workspace_size(M: int, K: int, N: int, R: int) -> int:
-    return int(c.fn("lora_delta_bwd_packed8_workspace_size", (c.i64,) * 4, c.size_t)(M, K, N, R))
+    return c.fn("lora_delta_bwd_packed8_workspace_size", (c.i64,) * 4, c.size_t)(M, K, N, R)
 
 
+@c.on_stream
 def lora_delta_bwd_packed8(dy, p: Packed8, a, b, u, alpha: float, *, dx=None, da=None, db=None, du=None,
-                           workspace=None, stream=None):
+                           workspace=None):
     """``lora_delta.lora_delta_bwd(dy, x, a, b, u, alpha)`` with x given as its 8-bit checkpoint:
     ``(dx, da, db, du)``, bit for bit those of the unpacked x. ``workspace`` (optional):
     ``lora_delta.new_workspace`` of the size above."""
-    _is_packed(p, "p")
+    dev = c.device_of(dy, "dy")
     M, N = dy.shape
-    K, R = p.cols, a.shape[0]
-    dev = dy.device
-    c.check(dy, "dy", (M, N), torch.bfloat16)
-    check_packed(p, "p", M, K, dev)
-    c.check(a, "a", (R, K), torch.bfloat16, device=dev)
-    c.check(b, "b", (N, R), torch.bfloat16, device=dev)
-    c.check(u, "u", (M, R), torch.bfloat16, device=dev)
-    handle, on = c.run_on(stream)
-    with on:
-        dx = torch.empty((M, K), dtype=torch.float32, device=dev) if dx is None else dx
-        da = torch.empty((R, K), dtype=torch.float32, device=dev) if da is None else da
-        db = torch.empty((N, R), dtype=torch.float32, device=dev) if db is None else db
-        du = torch.empty((M, R), dtype=torch.bfloat16, device=dev) if du is None else du
-        if workspace is None:
-            workspace = _ld.new_workspace(lora_delta_bwd_packed8_workspace_size(M, K, N, R), dev)
-    c.check(dx, "dx", (M, K), torch.float32, device=dev)
-    c.check(da, "da", (R, K), torch.float32, device=dev)
-    c.check(db, "db", (N, R), torch.float32, device=dev)
-    c.check(du, "du", (M, R), torch.bfloat16, device=dev)
+    K, R = _cols(p, "p"), a.shape[0]
+    dyp = c.check(dy, "dy", (M, N), c.BF16, dev)
+    cp, sp = check_packed(p, "p", M, K, dev)
+    ap, bp = c.check(a, "a", (R, K), c.BF16, dev), c.check(b, "b", (N, R), c.BF16, dev)
+    up = c.check(u, "u", (M, R), c.BF16, dev)
+    dx = c.out(dx, "dx", (M, K), c.F32, dev)
+    da = c.out(da, "da", (R, K), c.F32, dev)
+    db = c.out(db, "db", (N, R), c.F32, dev)
+    du = c.out(du, "du", (M, R), c.BF16, dev)
+    if workspace is None:
+        workspace = _ld.new_workspace(lora_delta_bwd_packed8_workspace_size(M, K, N, R), dy.device)
     c.done(c.fn("lora_delta_bwd_packed8", _BWD)(
-        dy.data_ptr(), p.codes.data_ptr(), p.scales.data_ptr(), a.data_ptr(), b.data_ptr(), u.data_ptr(), float(alpha),
-        M, K, N, R, dx.data_ptr(), da.data_ptr(), db.data_ptr(), du.data_ptr(), *c.scratch(workspace, dev), handle),
-        "lora_delta_bwd_packed8")
+        dyp, cp, sp, ap, bp, up, float(alpha), M, K, N, R, dx.data_ptr(), da.data_ptr(), db.data_ptr(), du.data_ptr(),
+        *c.scratch(workspace, dev), c.stream(dev)), "lora_delta_bwd_packed8")
     return dx, da, db, du

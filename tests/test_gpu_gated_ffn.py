@@ -232,7 +232,6 @@ def test_refusals():
     for bad in (lambda: ffn.gated_ffn_fwd(x.float(), wg, wu), lambda: ffn.gated_ffn_fwd(x, wg, wu[:8].contiguous()),
                 lambda: ffn.gated_ffn_fwd(x, wg.t(), wu), lambda: ffn.gated_ffn_fwd(x, wg, wu.cpu()),
                 lambda: ffn.gated_ffn_fwd(x, wg, wu, activation="relu"), lambda: ffn.gated_ffn_fwd(x, wg, wu, save="f32"),
-                lambda: ffn.gated_ffn_fwd(x, wg, wu, delta_gate=t["dg"]),
                 lambda: ffn.gated_ffn_fwd(x, wg, wu, delta_gate=t["dg"].bfloat16(), delta_up=t["du"].bfloat16()),
                 lambda: ffn.gated_ffn_fwd(x, wg, wu, save="packed8", gate=gate, up=up),
                 lambda: ffn.gated_ffn_bwd(dh, x, wg, wu, gate, pack8.pack8(up)),
@@ -241,6 +240,8 @@ def test_refusals():
                 lambda: ffn.gated_ffn_bwd(dh.float(), x, wg, wu, gate, up)):
         with pytest.raises(ValueError):
             bad()
+    with pytest.raises(TypeError):
+        ffn.gated_ffn_fwd(x, wg, wu, delta_gate=t["dg"])          # both deltas or neither
     from deterministic_arithmetic_gb300 import lora_delta as ld
     with pytest.raises(ld.LoraDeltaError, match="LORA_ERR_SHAPE"):
         ffn.gated_ffn_fwd(x[:, :60].contiguous(), wg[:, :60].contiguous(), wu[:, :60].contiguous())
