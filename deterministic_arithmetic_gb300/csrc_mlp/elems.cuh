@@ -16,8 +16,8 @@ __device__ __forceinline__ float scale_step(uint32_t s) {
   return __uint_as_float(s == 0u ? 0x00400000u : (s == 255u ? 0x7FC00000u : s << 23));
 }
 
-// The VEC elements as they lie in memory. VEC is 8 (bf16), 4 (fp32) or 1: whole 16-byte loads,
-// or single elements for rows whose length no vector divides.
+// The VEC elements as they lie in memory. VEC is 8 (bf16) or 4 (fp32): whole 16-byte loads; 2 (bf16)
+// or 1 for rows whose length those do not divide.
 template <int KIND, int VEC>
 struct Raw;
 template <>
@@ -52,6 +52,17 @@ struct Raw<kBf16, 1> {
   __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = __uint_as_float(uint32_t(v) << 16); }
 };
 template <>
+struct Raw<kBf16, 2> {
+  uint32_t v;
+  __device__ __forceinline__ void load(const void* p, const void*, int64_t row, int64_t ld, int c) {
+    v = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + row * ld + c));
+  }
+  __device__ __forceinline__ void get(float (&o)[2]) const {
+    o[0] = __uint_as_float(v << 16);
+    o[1] = __uint_as_float(v & 0xFFFF0000u);
+  }
+};
+template <>
 struct Raw<kF32, 1> {
   float v;
   __device__ __forceinline__ void load(const void* p, const void*, int64_t row, int64_t ld, int c) {
@@ -72,6 +83,8 @@ struct Raw<kPacked, VEC> {
       w[1] = t.y;
     } else if constexpr (VEC == 4) {
       w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+    } else if constexpr (VEC == 2) {
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(q));
     } else {
       w[0] = uint32_t(uint8_t(__ldg(q)));
     }
@@ -97,8 +110,9 @@ __device__ __forceinline__ float param_at(const void* p, int type, int64_t i) {
 // VEC consecutive ones, c a multiple of VEC.
 template <int VEC>
 __device__ __forceinline__ void params_at(const void* p, int type, int c, float (&o)[VEC]) {
-  if constexpr (VEC == 1) {
-    o[0] = param_at(p, type, c);
+  if constexpr (VEC < 4) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = param_at(p, type, c + i);
   } else if (type == kBf16) {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
@@ -132,6 +146,8 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&v)[V
     uint4 t = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
                          bf16x2_bits(v[6], v[7]));
     __stcs(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i), t);
+  } else if constexpr (KIND == kBf16 && VEC == 2) {
+    *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p) + i) = bf16x2_bits(v[0], v[1]);
   } else if constexpr (KIND == kBf16) {
     static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v[0]);
   } else if constexpr (VEC == 4) {

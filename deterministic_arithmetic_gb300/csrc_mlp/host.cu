@@ -52,7 +52,9 @@ lora_status device_ready(int* nsm) {
       void* p = nullptr;
       if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess || !p) return LORA_ERR_CUDA;
       d.status = static_cast<uint32_t*>(p);
-      if (lora::prepare_wgrad() != cudaSuccess || prepare_ffn() != cudaSuccess) return LORA_ERR_CUDA;
+      if (lora::prepare_wgrad() != cudaSuccess || prepare_ffn() != cudaSuccess ||
+          prepare_layer_norm() != cudaSuccess)
+        return LORA_ERR_CUDA;
     }
     d.probed = true;
   }

@@ -34,8 +34,9 @@ lora_status check_ptrs(const P*... p) {
 // LORA_OK on an sm_103 device (with every kernel of the operators prepared on it); *nsm its SMs.
 lora_status device_ready(int* nsm);
 
-// Raises the shared-memory limit of every instance of the tensor-core kernel (on the current device).
+// Raise the shared-memory limits of the kernels (on the current device).
 cudaError_t prepare_ffn();
+cudaError_t prepare_layer_norm();
 
 // The status block of the current device (common.cuh's layout): the operators of this folder run
 // without a workspace of their own to hold one. Valid after device_ready; zero when loaded.
