@@ -24,7 +24,10 @@ template <>
 struct Raw<kBf16, 8> {
   uint4 v;
   __device__ __forceinline__ void load(const void* p, const void*, int64_t row, int64_t ld, int c) {
-    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + row * ld + c));
+    load_at(p, nullptr, row * ld + c);
+  }
+  __device__ __forceinline__ void load_at(const void* p, const void*, int64_t at) {
+    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + at));
   }
   __device__ __forceinline__ void get(float (&o)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -76,7 +79,11 @@ struct Raw<kPacked, VEC> {
   uint32_t w[(VEC + 3) / 4];
   uint8_t s;
   __device__ __forceinline__ void load(const void* p, const void* scales, int64_t row, int64_t ld, int c) {
-    const int8_t* q = static_cast<const int8_t*>(p) + row * ld + c;
+    load_at(p, scales, row * ld + c);
+  }
+  // from code `at` of the storage (rows of ld codes one after the other, a scale byte every 32)
+  __device__ __forceinline__ void load_at(const void* p, const void* scales, int64_t at) {
+    const int8_t* q = static_cast<const int8_t*>(p) + at;
     if constexpr (VEC == 8) {
       const uint2 t = __ldg(reinterpret_cast<const uint2*>(q));
       w[0] = t.x;
@@ -88,12 +95,19 @@ struct Raw<kPacked, VEC> {
     } else {
       w[0] = uint32_t(uint8_t(__ldg(q)));
     }
-    s = __ldg(static_cast<const uint8_t*>(scales) + row * (ld >> 5) + (c >> 5));
+    s = __ldg(static_cast<const uint8_t*>(scales) + (at >> 5));
   }
   __device__ __forceinline__ void get(float (&o)[VEC]) const {
     const float step = scale_step(s);
+    if constexpr (VEC >= 4) {
+      // a code as FP32: 2^23 + (code + 128) has the byte at the bottom, and the difference is exact
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = float(int8_t(w[i / 4] >> (8 * (i % 4)))) * step;
+      for (int i = 0; i < VEC; ++i)
+        o[i] = (__uint_as_float(__byte_perm(w[i / 4] ^ 0x80808080u, 0x4B000000u, 0x7440u + i % 4)) - 8388736.f) * step;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] = float(int8_t(w[0] >> (8 * i))) * step;
+    }
   }
 };
 

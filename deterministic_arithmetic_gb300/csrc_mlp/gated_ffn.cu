@@ -9,28 +9,39 @@
 namespace mlp {
 namespace {
 
-// dG and dU of 8 elements a thread. XK: how G and U are kept (bf16 or packed).
-template <int XK>
+// dG and dU, 8 elements a thread at a time, kDeep times. XK: how G and U are kept (bf16 or packed). FLAT
+// (bf16, or F a multiple of 32): the kept rows lie one after the other as those of dh do.
+constexpr int kDeep = 2;
+template <int XK, bool FLAT>
 __global__ void __launch_bounds__(256)
     ffn_grad_kernel(const void* __restrict__ dh, const void* __restrict__ g, const void* __restrict__ u,
-                    const void* __restrict__ gs, const void* __restrict__ us, int act, int64_t M, int F,
+                    const void* __restrict__ gs, const void* __restrict__ us, int act, int64_t items, uint32_t F,
                     void* __restrict__ dg, void* __restrict__ du) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const int per = F / 8;
-  const int64_t items = M * per, ld = row_ld<XK>(F);
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < items; i += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t row = i / per;
-    const int c = int(i - row * per) * 8;
-    Raw<kBf16, 8> rh;
-    Raw<XK, 8> rg, ru;
-    rh.load(dh, nullptr, row, F, c);
-    rg.load(g, gs, row, ld, c);
-    ru.load(u, us, row, ld, c);
+  const int64_t first = int64_t(blockIdx.x) * (256 * kDeep) + threadIdx.x, ld = row_ld<XK>(F);
+  const uint32_t per_row = F / 8;
+  Raw<kBf16, 8> rh[kDeep];
+  Raw<XK, 8> rg[kDeep], ru[kDeep];
+#pragma unroll
+  for (int j = 0; j < kDeep; ++j) {
+    const int64_t i = first + 256 * j;
+    if (i < items) {
+      const int64_t row = FLAT ? 0 : i / per_row;
+      const int64_t at = FLAT ? 8 * i : row * ld + (i - row * per_row) * 8;
+      rh[j].load_at(dh, nullptr, 8 * i);
+      rg[j].load_at(g, gs, at);
+      ru[j].load_at(u, us, at);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kDeep; ++j) {
+    const int64_t i = first + 256 * j;
+    if (i >= items) continue;
     float h[8], a[8], b[8];
-    rh.get(h);
-    rg.get(a);
-    ru.get(b);
+    rh[j].get(h);
+    rg[j].get(a);
+    ru[j].get(b);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = act_p(act, a[e]);
@@ -39,9 +50,8 @@ __global__ void __launch_bounds__(256)
       a[e] = dg_e;
     }
     // plain stores: the products that follow read both again, from L2 as far as they fit
-    const int64_t o = row * F + c;
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dg) + o) = pack_bf16x8(a);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(du) + o) = pack_bf16x8(b);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dg) + 8 * i) = pack_bf16x8(a);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(du) + 8 * i) = pack_bf16x8(b);
   }
 }
 
@@ -224,13 +234,14 @@ lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate
                ? LORA_OK
                : LORA_ERR_CUDA;
   }
-  const int64_t want = cdiv(M * (F / 8), 256), most = int64_t(nsm) * 16;
-  const dim3 grid(unsigned(want < most ? want : most));
-  const int f = int(F);
-  const cudaError_t e =
-      keep == LORA_KEEP_BF16
-          ? launch_pdl(ffn_grad_kernel<kBf16>, grid, dim3(256), 0, st, dh, gate, up, gate_scales, up_scales, act, M, f, dgate, dup)
-          : launch_pdl(ffn_grad_kernel<kPacked>, grid, dim3(256), 0, st, dh, gate, up, gate_scales, up_scales, act, M, f, dgate, dup);
+  const int64_t items = M * (F / 8);
+  const dim3 grid(unsigned(cdiv(items, 256 * kDeep)));
+  auto grad = [&](auto kernel) {
+    return launch_pdl(kernel, grid, dim3(256), 0, st, dh, gate, up, gate_scales, up_scales, act, items, uint32_t(F), dgate, dup);
+  };
+  const cudaError_t e = keep == LORA_KEEP_BF16 ? grad(ffn_grad_kernel<kBf16, true>)
+                        : F % kGroup == 0      ? grad(ffn_grad_kernel<kPacked, true>)
+                                               : grad(ffn_grad_kernel<kPacked, false>);
   if (e != cudaSuccess) return LORA_ERR_CUDA;
   FfnArgs P{};
   P.m = int(M);
@@ -239,7 +250,7 @@ lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate
   P.out[0] = static_cast<__nv_bfloat16*>(dx);
   if ((s = launch<kDx>(P, Operands{{dgate, dup}, {w_gate, w_up}, M, F, F, K}, nsm, st)) != LORA_OK || !dw) return s;
   FfnArgs Q{};
-  Q.m = f;
+  Q.m = int(F);
   Q.n = int(K);
   Q.nk = int(cdiv(M, kBK));
   Q.out[0] = static_cast<__nv_bfloat16*>(dw_gate);

@@ -182,11 +182,7 @@ __device__ __forceinline__ void keep_row32(const FfnArgs& P, int which, int64_t 
   const float inv = inv_step(s);
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[i] |= (uint32_t(code_of(v[4 * i + e], inv, s)) & 0xFFu) << (8 * e);
-  }
+  for (int i = 0; i < 8; ++i) w[i] = codes4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv, s);
   uint4* q = reinterpret_cast<uint4*>(static_cast<int8_t*>(P.keep[which]) + (row * G + (col >> 5)) * 32);
   q[0] = make_uint4(w[0], w[1], w[2], w[3]);
   q[1] = make_uint4(w[4], w[5], w[6], w[7]);

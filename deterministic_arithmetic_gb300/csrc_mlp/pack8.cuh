@@ -20,11 +20,16 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
 // 1 / step of scale byte s <= 248, exactly: 2^(127 - s). (s = 255: 0, all codes of the group are 0.)
 __device__ __forceinline__ float inv_step(uint32_t s) { return s == 255u ? 0.f : __uint_as_float((254u - s) << 23); }
 
-// The code of x, one multiplication by a power of two and one rounding to nearest even away from
-// x / step; 127.5 steps, a tie that would round to 128, is held to 127.
-__device__ __forceinline__ int code_of(float x, float inv, uint32_t s) {
-  const int q = s == 255u ? 0 : __float2int_rn(x * inv);
-  return q > 127 ? 127 : (q < -127 ? -127 : q);
+// Four codes in a word: x times 1 / step (exact), held to +-127 (127.5 steps, a tie, would round to
+// 128), and one rounding to nearest even: 1.5 * 2^23 + v has round(v) in its low bits, two's
+// complement. NaN and infinity: s = 255, whose codes are 0.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv, uint32_t s) {
+  const float v[4] = {a, b, c, d};
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fminf(fmaxf(v[i] * inv, -127.f), 127.f) + 12582912.f);
+  const uint32_t w = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  return s == 255u ? 0u : w;
 }
 
 }  // namespace mlp
