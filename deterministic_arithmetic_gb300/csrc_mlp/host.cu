@@ -4,7 +4,6 @@
 
 #include <mutex>
 
-#include "../csrc/kernels.h"
 #include "mlp.h"
 
 namespace mlp {
@@ -52,7 +51,7 @@ lora_status device_ready(int* nsm) {
       void* p = nullptr;
       if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess || !p) return LORA_ERR_CUDA;
       d.status = static_cast<uint32_t*>(p);
-      if (lora::prepare_wgrad() != cudaSuccess || prepare_ffn() != cudaSuccess ||
+      if (prepare_pack8_da() != cudaSuccess || prepare_ffn() != cudaSuccess ||
           prepare_layer_norm() != cudaSuccess)
         return LORA_ERR_CUDA;
     }

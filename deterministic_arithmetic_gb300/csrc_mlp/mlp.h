@@ -37,6 +37,7 @@ lora_status device_ready(int* nsm);
 // Raise the shared-memory limits of the kernels (on the current device).
 cudaError_t prepare_ffn();
 cudaError_t prepare_layer_norm();
+cudaError_t prepare_pack8_da();
 
 // The status block of the current device (common.cuh's layout): the operators of this folder run
 // without a workspace of their own to hold one. Valid after device_ready; zero when loaded.

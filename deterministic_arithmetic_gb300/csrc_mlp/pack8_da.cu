@@ -1,41 +1,389 @@
-// pack8_da.cu -- the adapter gradients of a packed x: dA = du^T x, and the whole
-// backward pass of the LoRA delta. x is unpacked into the workspace first.
+// pack8_da.cu -- the adapter gradients of a packed x: dA = du^T x, and the whole backward pass of the
+// LoRA delta.
+//
+// dA[r][k] = sum_m du[m][r] x[m][k] from x's codes and scale bytes, with the sum's tree of the delta's own
+// weight gradients: 16-row tensor-core leaves with a fresh accumulator each, added by the canonical
+// pairwise tree in 256-row chunks, and the chunks' partials by the canonical tree (combine). The values
+// the codes stand for are bf16 values, so the leaves are those of the unpacked x, bit for bit.
+//
+// Bound by HBM in principle (33 / 32 bytes an element of x and little else); in practice by the
+// expansion of the codes, 2.5 instructions each. Work unit = (128 columns, 256 rows); a stage brings 64
+// rows of codes (one box, 128-byte swizzle) and of du. Two warps expand a stage, a thread a row of 128
+// codes, into two 64-column bf16 blocks in the layout a TMA copy of x would have left; four such teams
+// work on the four stages of a unit at once (all eight warps on one stage at a time waited out every
+// stage's latencies in turn: 25 us). The tensor core takes both operands transposed (M = 128 columns,
+// N = padded rank, K = 16 rows). At 8192 x 4096, rank 16: 38 us for unpacking x and running the delta's
+// own kernels on it, MEASURED us here.
+//
+// Warps: 0 copies, 1 issues the MMAs, 2..9 add the leaves, 10..17 expand.
 #include "../csrc/common.cuh"
 #include "../csrc/kernels.h"
+#include "elems.cuh"
 #include "mlp.h"
 
-using namespace mlp;
-
+namespace mlp {
 namespace {
+
+using namespace lora;
+
+constexpr uint32_t kKindDa = 13, kSiteDa = 56;      // status block
+
+struct DaArgs {
+  CUtensorMap codes, du;            // boxes 64 rows x 128 codes; 64 rows x RP
+  const uint8_t* scales;
+  float* part;                      // [n_ch][rows][K]
+  int M, K, G, rows;                // rows: of a partial that are written (the rank for a single chunk, else RP)
+  int n_ct, total;
+};
+
+template <int RP>
+struct DaCfg {
+  static constexpr int kRows = 64, kCols = 128;                 // of a stage
+  static constexpr int kCodeBytes = kRows * kCols, kDuBytes = kRows * RP * 2;
+  static constexpr int kRawBytes = kCodeBytes + kDuBytes, kRaw = 8;
+  static constexpr int kWideBytes = kRows * kCols * 2, kWide = 4;   // expanded: two [64 rows][64 columns] bf16 blocks
+  static constexpr int kLeaves = kRows / 16, kGroupCols = kLeaves * RP, kAcc = 512 / kGroupCols;
+  static constexpr int kEpi = 8, kTeam = 2, kXf = kTeam * kWide, kThreads = 32 * (2 + kEpi + kXf);
+  static constexpr int kSteps = kWgradChunk / kRows;            // stages of a chunk; a team and a place for each
+  static constexpr int kCPT = RP / 2;                           // accumulator columns of an epilogue thread
+  static constexpr int kCH = kCPT < 16 ? kCPT : 16;             // of them, at a time
+  static constexpr int kBars = 2 * kRaw + 2 * kWide + 2 * kAcc + 2;
+  static constexpr size_t kSmem = size_t(kWide) * kWideBytes + size_t(kRaw) * kRawBytes + 1024 + kBars * 8 + 16;
+  static_assert(kSteps == 4 && kWide == kSteps && kTeam * 32 == kRows && kRawBytes % 1024 == 0 && kSmem < 227 * 1024, "layout");
+};
+
+// 4 codes of a group with step 2^(s - 127), 1 <= s <= 246, as 4 bf16 values. With b the code's byte,
+// 128 + (b & 127) is a bf16 value (0x4300 plus the low bits), and code = that - 128, or - 256 for b >= 128:
+// one fused multiply-add by the step, exact. -256 steps is -128 steps with the exponent one higher: bit 7
+// of the byte added where the exponent's lowest bit is.
+__device__ __forceinline__ uint2 expand4(uint32_t w, uint32_t step2, uint32_t minus128) {
+  uint32_t h[2] = {__byte_perm(w, 0u, 0x4140), __byte_perm(w, 0u, 0x4342)};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = (h[i] & 0x007F007Fu) | 0x43004300u, c = minus128 + (h[i] & 0x00800080u);
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(h[i]) : "r"(a), "r"(step2), "r"(c));
+  }
+  return make_uint2(h[0], h[1]);
+}
+// The same for any s (255: NaN).
+__device__ __forceinline__ uint2 expand4_any(uint32_t w, uint32_t s) {
+  const float step = scale_step(s);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = float(int8_t(w >> (8 * i))) * step;
+  return make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+}
+
+template <int RP>
+__global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const __grid_constant__ DaArgs P, uint32_t* status) {
+  using C = DaCfg<RP>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  constexpr uint32_t raw_off = C::kWide * C::kWideBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + raw_off + C::kRaw * C::kRawBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto rfull = [&](int s) { return bar0 + 8u * s; };                                   // codes and du landed
+  auto rempty = [&](int s) { return bar0 + 8u * (C::kRaw + s); };
+  auto wfull = [&](int s) { return bar0 + 8u * (2 * C::kRaw + s); };                   // expanded
+  auto wempty = [&](int s) { return bar0 + 8u * (2 * C::kRaw + C::kWide + s); };
+  auto tfull = [&](int g) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kWide + g); };    // leaves done
+  auto tempty = [&](int g) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kWide + C::kAcc + g); };
+  const uint32_t drain = bar0 + 8u * (C::kBars - 2), never = drain + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kRaw; ++s) mbar_init(rfull(s), 1), mbar_init(rempty(s), 1);
+    for (int s = 0; s < C::kWide; ++s) mbar_init(wfull(s), C::kTeam), mbar_init(wempty(s), 1);
+    for (int g = 0; g < C::kAcc; ++g) mbar_init(tfull(g), 1), mbar_init(tempty(g), C::kEpi);
+    mbar_init(drain, 1);
+    mbar_init(never, 1);
+    *abort_flag = 0u;
+    mbar_fence_init();
+    prefetch_map(&P.codes);
+    prefetch_map(&P.du);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const Abort ab = make_abort(abort_flag, status);
+  // stages of the chunk ch
+  auto steps_of = [&](int ch) { return (min(P.M - ch * kWgradChunk, kWgradChunk) + C::kRows - 1) / C::kRows; };
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- copies
+    if (lane == 0) {
+      if (stall_requested(status, kKindDa)) stall_wait(never, ab, kSiteDa);   // test hook: a wait that runs out
+      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
+      Ring r;
+      uint32_t issued = 0, parities = 0;
+      for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+        const int ct = u % P.n_ct, ch = u / P.n_ct, n = steps_of(ch);
+        for (int i = 0; i < n; ++i) {
+          if (wait(rempty(r.idx), r.phase ^ 1u, ab, kSiteDa + 1)) {
+            const uint32_t st = base + raw_off + r.idx * C::kRawBytes;
+            const int m = ch * kWgradChunk + i * C::kRows;
+            mbar_expect_tx(rfull(r.idx), C::kRawBytes);
+            tma_load(st, &P.codes, rfull(r.idx), ct * C::kCols, m, once);
+            tma_load(st + C::kCodeBytes, &P.du, rfull(r.idx), 0, m, keep);
+            issued |= 1u << r.idx;
+            parities = (parities & ~(1u << r.idx)) | (r.phase << r.idx);
+          }
+          r.next<C::kRaw>();
+        }
+      }
+      for (int s = 0; s < C::kRaw; ++s)
+        if (issued & (1u << s)) wait_drain(rfull(s), (parities >> s) & 1u, ab, kSiteDa + 2);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = idesc_bf16(128, RP, 1, 1);
+    uint64_t xdesc[C::kLeaves], gdesc[C::kLeaves];
+#pragma unroll
+    for (int j = 0; j < C::kLeaves; ++j) {
+      // x transposed: columns contiguous, 64-column blocks 8 KB apart, 8-row groups 1 KB apart
+      xdesc[j] = smem_desc(base + j * 2048u, 8192u, 1024u, kLayoutSW128);
+      // du rows [64][RP]: one swizzle span a row
+      gdesc[j] = smem_desc(base + raw_off + C::kCodeBytes + j * 32u * RP, 16u * RP, 16u * RP, layout_for_span(RP * 2));
+    }
+    Ring r, g;
+    uint32_t wphase = 0;                                // a bit a place
+    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+      const int n = steps_of(u / P.n_ct);
+      for (int i = 0; i < n; ++i) {
+        // the stage's copies have landed when it has been expanded
+        bool ok = wait(wfull(i), (wphase >> i) & 1u, ab, kSiteDa + 3);
+        ok = __all_sync(0xffffffffu, ok && wait(tempty(g.idx), g.phase ^ 1u, ab, kSiteDa + 4));
+        if (ok) {
+          tc_fence_after();
+          const uint32_t d = tmem + g.idx * C::kGroupCols;
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < C::kLeaves; ++j)
+              mma_bf16(d + j * RP, desc_advance(xdesc[j], i * C::kWideBytes), desc_advance(gdesc[j], r.idx * C::kRawBytes),
+                       idesc, 0u);
+            mma_commit(wempty(i));
+            mma_commit(rempty(r.idx));
+            mma_commit(tfull(g.idx));
+          }
+          __syncwarp();
+        }
+        wphase ^= 1u << i;
+        r.next<C::kRaw>();
+        g.next<C::kAcc>();
+      }
+    }
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    wait_drain(drain, 0u, ab, kSiteDa + 5);
+  } else if (warp < 2 + C::kEpi) {
+    // ---------------------------------------------------- leaves to partials
+    const int q = warp & 3, h = (warp - 2) >> 2;        // a quarter of the columns of x, a half of the rank
+    const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + h * C::kCPT;
+    Ring g;
+    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+      const int ct = u % P.n_ct, ch = u / P.n_ct, n = steps_of(ch);
+      float sum[C::kCPT], left[2][C::kCPT];
+      bool all = true;
+#pragma unroll
+      for (int i = 0; i < C::kSteps; ++i) {
+        if (i < n) {
+          const bool ok = __all_sync(0xffffffffu, wait(tfull(g.idx), g.phase, ab, kSiteDa + 6));
+          all = all && ok;
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < C::kCPT; c0 += 8) {
+            uint32_t v[C::kLeaves][8];
+#pragma unroll
+            for (int j = 0; j < C::kLeaves; ++j)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[j][e] = 0u;
+            if (ok) {
+#pragma unroll
+              for (int j = 0; j < C::kLeaves; ++j) tmem_ld8(tbase + g.idx * C::kGroupCols + j * RP + c0, v[j]);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < C::kLeaves; ++j) reg_fence(v[j]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              sum[c0 + e] = tree4(__uint_as_float(v[0][e]), __uint_as_float(v[1][e]), __uint_as_float(v[2][e]),
+                                  __uint_as_float(v[3][e]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(tempty(g.idx));
+          g.next<C::kAcc>();
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::kCPT; ++c) sum[c] = 0.f;
+        }
+        // stages 0 + 1, 2 + 3, then the two (a stage past the chunk's end adds 0 to its left neighbour)
+        if (i == 0 || i == 2) {
+#pragma unroll
+          for (int c = 0; c < C::kCPT; ++c) left[i / 2][c] = sum[c];
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::kCPT; ++c) sum[c] = __fadd_rn(left[i / 2][c], sum[c]);
+          if (i == 1) {
+#pragma unroll
+            for (int c = 0; c < C::kCPT; ++c) left[0][c] = sum[c];
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::kCPT; ++c) sum[c] = __fadd_rn(left[0][c], sum[c]);
+          }
+        }
+      }
+      const int col = ct * C::kCols + q * 32 + lane;
+      if (all && col < P.K) {
+        float* dst = P.part + (size_t(ch) * P.rows + h * C::kCPT) * P.K + col;
+#pragma unroll
+        for (int c = 0; c < C::kCPT; ++c)
+          if (h * C::kCPT + c < P.rows) dst[size_t(c) * P.K] = sum[c];
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- expand
+    // Team i expands stage i of every unit into place i; a thread a row of it. The 16-byte pieces of a
+    // row are permuted by the row's lowest three bits, so eight neighbouring lanes meet all the banks.
+    const int team = (warp - 2 - C::kEpi) / C::kTeam, row = (warp - 2 - C::kEpi) % C::kTeam * 32 + lane;
+    const uint32_t sw = row & 7;
+    uint8_t* out = gbase + team * C::kWideBytes + row * 128;
+    auto scales_of = [&](int u, uint32_t (&s)[4]) {     // 127 (a step of 1, for codes that are 0) outside the tensor
+      const int grp = u % P.n_ct * 4, m = u / P.n_ct * kWgradChunk + team * C::kRows + row;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        s[k] = u < P.total && m < P.M && grp + k < P.G ? uint32_t(__ldg(P.scales + size_t(m) * P.G + grp + k)) : 127u;
+    };
+    uint32_t stage = 0, wphase = 1u;                    // stages of this CTA so far
+    uint32_t next[4];
+    scales_of(blockIdx.x, next);
+    for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
+      const int n = steps_of(u / P.n_ct);
+      const uint32_t mine = stage + team;
+      stage += n;
+      uint32_t s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] = next[k];
+      scales_of(u + gridDim.x, next);                   // the next unit's, loaded under this one's work
+      if (team >= n) continue;
+      bool ok = wait(rfull(mine % C::kRaw), (mine / C::kRaw) & 1u, ab, kSiteDa + 7);
+      ok = ok && wait(wempty(team), wphase, ab, kSiteDa + 8);
+      ok = __all_sync(0xffffffffu, ok);
+      wphase ^= 1u;
+      if (ok) {
+        const uint8_t* in = gbase + raw_off + mine % C::kRaw * C::kRawBytes + row * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {                   // a group of 32 codes: two pieces in, four out
+          const uint4 c0 = *reinterpret_cast<const uint4*>(in + (((2 * k) ^ sw) << 4));
+          const uint4 c1 = *reinterpret_cast<const uint4*>(in + (((2 * k + 1) ^ sw) << 4));
+          const uint32_t word[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          uint2 v[8];
+          if (s[k] - 1u < 246u) {
+            const uint32_t step2 = (s[k] << 7) * 0x00010001u, minus128 = (0x8000u | ((s[k] + 7u) << 7)) * 0x00010001u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = expand4(word[j], step2, minus128);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = expand4_any(word[j], s[k]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(out + (k >> 1) * 8192 + ((((k & 1) * 4 + j) ^ sw) << 4)) =
+                make_uint4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wfull(team));
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
 
 bool shape_ok(int64_t M, int64_t K) { return size_ok(M) && size_ok(K) && K > 0 && K % 8 == 0; }
 bool rank_ok(int64_t R) { return R >= 8 && R <= 64 && R % 8 == 0; }
+int64_t chunks(int64_t M) { return cdiv(M, kWgradChunk); }
 
-// Workspace of dA: the unpacked x, then one partial per 256-row chunk.
-struct DaLayout {
-  size_t part, bytes;
-};
-DaLayout da_layout(int64_t M, int64_t K, int64_t R) {
-  DaLayout l;
-  l.part = round256(size_t(M) * size_t(K) * 2);
-  l.bytes = l.part + round256(size_t(cdiv(M, lora::kWgradChunk)) * lora::padded_rank(int(R)) * size_t(K) * 4);
-  return l;
+// The chunk partials of dA (none for a single chunk, which goes straight to da).
+size_t part_bytes(int64_t M, int64_t K, int64_t R) {
+  return chunks(M) > 1 ? round256(size_t(chunks(M)) * padded_rank(int(R)) * size_t(K) * 4) : 0;
 }
 
-// The weight-gradient kernel reads its wide operand before its grid dependency wait (no kernel of
-// the delta's own passes writes it). This empty launch between it and the unpacking starts the
-// kernel's launch only after the unpacked rows are complete.
-__global__ void after_unpack_kernel() {
-  lora::grid_dependency_wait();
-  lora::grid_dependents_launch();
+template <int RP>
+cudaError_t launch_da_as(const DaArgs& P, int nsm, cudaStream_t st) {
+  return launch_pdl(pack8_da_kernel<RP>, dim3(unsigned(P.total < nsm ? P.total : nsm)), dim3(DaCfg<RP>::kThreads),
+                    DaCfg<RP>::kSmem, st, P, status_block());
+}
+
+// dA into da by way of the partials (as part_bytes says).
+lora_status run_da(const void* du, const void* codes, const void* scales, int64_t M, int64_t K, int64_t R, float* da,
+                   float* part, int nsm, cudaStream_t st) {
+  const int RP = padded_rank(int(R));
+  const int64_t C = chunks(M), ld = kGroup * groups(K);
+  DaArgs P{};
+  if (!tensor_map(&P.codes, codes, Elem::u8, M, ld, ld, 128, 64, 128) ||
+      !tensor_map(&P.du, du, Elem::bf16, M, R, R, RP, 64, RP * 2))
+    return LORA_ERR_CUDA;
+  P.scales = static_cast<const uint8_t*>(scales);
+  P.part = C > 1 ? part : da;
+  P.rows = C > 1 ? RP : int(R);
+  P.M = int(M);
+  P.K = int(K);
+  P.G = int(groups(K));
+  P.n_ct = int(cdiv(K, 128));
+  if (P.n_ct * C >= int64_t(1) << 30) return LORA_ERR_SHAPE;
+  P.total = int(P.n_ct * C);
+  const cudaError_t e = RP == 16   ? launch_da_as<16>(P, nsm, st)
+                        : RP == 32 ? launch_da_as<32>(P, nsm, st)
+                                   : launch_da_as<64>(P, nsm, st);
+  if (e != cudaSuccess) return LORA_ERR_CUDA;
+  if (C == 1) return LORA_OK;
+  CombineJobs jobs{};
+  jobs.n = 1;
+  jobs.j[0] = CombineJob{part, da, int(C), int(K), int(R), RP, 0};
+  return launch_combine(jobs, st) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
+template <int RP>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(pack8_da_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(DaCfg<RP>::kSmem));
 }
 
 }  // namespace
 
+cudaError_t prepare_pack8_da() {
+  cudaError_t e;
+  if ((e = prepare<16>()) != cudaSuccess || (e = prepare<32>()) != cudaSuccess) return e;
+  return prepare<64>();
+}
+
+}  // namespace mlp
+
+using namespace mlp;
+
 extern "C" {
 
 size_t lora_pack8_da_workspace_size(int64_t M, int64_t K, int64_t R) {
-  return shape_ok(M, K) && rank_ok(R) ? da_layout(M, K, R).bytes + 256 : 0;
+  return shape_ok(M, K) && rank_ok(R) ? part_bytes(M, K, R) + 256 : 0;
 }
 
 lora_status lora_pack8_da(const void* du, const void* codes, const void* scales, int64_t M, int64_t K, int64_t R,
@@ -45,35 +393,14 @@ lora_status lora_pack8_da(const void* du, const void* codes, const void* scales,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   lora_status s;
   int nsm = 0;
-  if (M == 0) {
+  if (M == 0) {                                     // a sum over no rows
     if ((s = check_ptrs(da)) != LORA_OK || (s = device_ready(&nsm)) != LORA_OK) return s;
     return cudaMemsetAsync(da, 0, size_t(R) * size_t(K) * 4, st) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
   }
   if ((s = check_ptrs(du, codes, scales, da, workspace)) != LORA_OK) return s;
   if (workspace_bytes < lora_pack8_da_workspace_size(M, K, R)) return LORA_ERR_WORKSPACE;
   if ((s = device_ready(&nsm)) != LORA_OK) return s;
-  const int RP = lora::padded_rank(int(R));
-  const DaLayout L = da_layout(M, K, R);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + L.part);
-  if ((s = lora_unpack8(codes, scales, M, K, workspace, LORA_BF16, stream)) != LORA_OK) return s;
-  if (lora::launch_pdl(after_unpack_kernel, dim3(1), dim3(32), 0, st) != cudaSuccess) return LORA_ERR_CUDA;
-  lora::WgArgs args{};
-  args.n = 1;
-  lora::WgSite& w = args.s[0];
-  if (!tensor_map(&w.in, workspace, Elem::bf16, M, K, K, 64, 64, 128) ||
-      !tensor_map(&w.g, du, Elem::bf16, M, R, R, RP, 64, RP * 2))
-    return LORA_ERR_CUDA;
-  w.part = part;
-  w.M = int(M);
-  w.Cw = int(K);
-  w.alpha = 1.0f;
-  const int64_t units = lora::wgrad_units(M, K, RP);
-  if (lora::launch_wgrad(RP, false, args, status_block(), int(units < nsm ? units : nsm), st) != cudaSuccess)
-    return LORA_ERR_CUDA;
-  lora::CombineJobs jobs{};
-  jobs.n = 1;
-  jobs.j[0] = lora::CombineJob{part, da, int(cdiv(M, lora::kWgradChunk)), int(K), int(R), RP, 0};
-  return lora::launch_combine(jobs, st) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  return run_da(du, codes, scales, M, K, R, da, static_cast<float*>(workspace), nsm, st);
 }
 
 size_t lora_delta_bwd_packed8_workspace_size(int64_t M, int64_t K, int64_t N, int64_t R) {
