@@ -71,7 +71,10 @@ uint32_t* status_block() {
 
 bool tensor_map(CUtensorMap* m, const void* ptr, Elem e, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                 int box_rows, int swizzle) {
-  const cuuint64_t size = e == Elem::bf16 ? 2 : 1;
+  const cuuint64_t size = e == Elem::f32 ? 4 : (e == Elem::bf16 ? 2 : 1);
+  const CUtensorMapDataType type = e == Elem::f32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : e == Elem::bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
   cuuint64_t strides[1] = {cuuint64_t(ld) * size};
   cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
@@ -80,7 +83,7 @@ bool tensor_map(CUtensorMap* m, const void* ptr, Elem e, int64_t rows, int64_t c
                                 : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                 : swizzle == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
-  return g_encode(m, e == Elem::bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+  return g_encode(m, type, 2,
                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   sw,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -45,7 +45,7 @@ uint32_t* status_block();
 
 // 2-D row-major map of a tensor [rows][cols] whose rows are `ld` elements apart; `swizzle` bytes
 // (128, 64, 32; 0: none). False: the driver refused it.
-enum class Elem { bf16, u8 };
+enum class Elem { bf16, f32, u8 };
 bool tensor_map(CUtensorMap* m, const void* ptr, Elem e, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                 int box_rows, int swizzle);
 // The same bf16 tensor as 64-column blocks, [cols / 64][rows][64] (cols a multiple of 64): a box is

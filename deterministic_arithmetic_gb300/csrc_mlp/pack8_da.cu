@@ -329,14 +329,14 @@ size_t part_bytes(int64_t M, int64_t K, int64_t R) {
 }
 
 template <int RP>
-cudaError_t launch_da_as(const DaArgs& P, int nsm, cudaStream_t st) {
+cudaError_t launch_da_as(const DaArgs& P, uint32_t* status, int nsm, cudaStream_t st) {
   return launch_pdl(pack8_da_kernel<RP>, dim3(unsigned(P.total < nsm ? P.total : nsm)), dim3(DaCfg<RP>::kThreads),
-                    DaCfg<RP>::kSmem, st, P, status_block());
+                    DaCfg<RP>::kSmem, st, P, status);
 }
 
 // dA into da by way of the partials (as part_bytes says).
 lora_status run_da(const void* du, const void* codes, const void* scales, int64_t M, int64_t K, int64_t R, float* da,
-                   float* part, int nsm, cudaStream_t st) {
+                   float* part, uint32_t* status, int nsm, cudaStream_t st) {
   const int RP = padded_rank(int(R));
   const int64_t C = chunks(M), ld = kGroup * groups(K);
   DaArgs P{};
@@ -352,15 +352,29 @@ lora_status run_da(const void* du, const void* codes, const void* scales, int64_
   P.n_ct = int(cdiv(K, 128));
   if (P.n_ct * C >= int64_t(1) << 30) return LORA_ERR_SHAPE;
   P.total = int(P.n_ct * C);
-  const cudaError_t e = RP == 16   ? launch_da_as<16>(P, nsm, st)
-                        : RP == 32 ? launch_da_as<32>(P, nsm, st)
-                                   : launch_da_as<64>(P, nsm, st);
+  const cudaError_t e = RP == 16   ? launch_da_as<16>(P, status, nsm, st)
+                        : RP == 32 ? launch_da_as<32>(P, status, nsm, st)
+                                   : launch_da_as<64>(P, status, nsm, st);
   if (e != cudaSuccess) return LORA_ERR_CUDA;
   if (C == 1) return LORA_OK;
   CombineJobs jobs{};
   jobs.n = 1;
   jobs.j[0] = CombineJob{part, da, int(C), int(K), int(R), RP, 0};
   return launch_combine(jobs, st) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+}
+
+// Workspace of the whole backward pass: lora_delta_bwd's control block, then the partials of dU, dB, dA.
+struct BwdLayout {
+  size_t du, db, da, bytes;
+};
+BwdLayout bwd_layout(int64_t M, int64_t K, int64_t N, int64_t R) {
+  const int RP = padded_rank(int(R));
+  BwdLayout l;
+  l.du = LORA_DELTA_CONTROL_BYTES;
+  l.db = l.du + round256(size_t(cdiv(N, du_slice(RP))) * size_t(M) * RP * 4);
+  l.da = l.db + round256(size_t(chunks(M)) * RP * size_t(N) * 4);
+  l.bytes = l.da + part_bytes(M, K, R);
+  return l;
 }
 
 template <int RP>
@@ -372,7 +386,9 @@ cudaError_t prepare() {
 
 cudaError_t prepare_pack8_da() {
   cudaError_t e;
-  if ((e = prepare<16>()) != cudaSuccess || (e = prepare<32>()) != cudaSuccess) return e;
+  if ((e = prepare_down()) != cudaSuccess || (e = prepare_up()) != cudaSuccess || (e = prepare_wgrad()) != cudaSuccess ||
+      (e = prepare_dy()) != cudaSuccess || (e = prepare<16>()) != cudaSuccess || (e = prepare<32>()) != cudaSuccess)
+    return e;
   return prepare<64>();
 }
 
@@ -400,29 +416,90 @@ lora_status lora_pack8_da(const void* du, const void* codes, const void* scales,
   if ((s = check_ptrs(du, codes, scales, da, workspace)) != LORA_OK) return s;
   if (workspace_bytes < lora_pack8_da_workspace_size(M, K, R)) return LORA_ERR_WORKSPACE;
   if ((s = device_ready(&nsm)) != LORA_OK) return s;
-  return run_da(du, codes, scales, M, K, R, da, static_cast<float*>(workspace), nsm, st);
+  return run_da(du, codes, scales, M, K, R, da, static_cast<float*>(workspace), status_block(), nsm, st);
 }
 
 size_t lora_delta_bwd_packed8_workspace_size(int64_t M, int64_t K, int64_t N, int64_t R) {
-  const size_t b = lora_delta_bwd_workspace_size(M, K, N, R);
-  return b ? b + round256(size_t(M) * size_t(K) * 2) : 0;
+  return lora_delta_bwd_workspace_size(M, K, N, R) ? bwd_layout(M, K, N, R).bytes : 0;
 }
 
 lora_status lora_delta_bwd_packed8(const void* dy, const void* codes, const void* scales, const void* a, const void* b,
                                    const void* u, float alpha, int64_t M, int64_t K, int64_t N, int64_t R, float* dx,
                                    float* da, float* db, void* du, void* workspace, size_t workspace_bytes,
                                    void* stream) {
-  const size_t need = lora_delta_bwd_workspace_size(M, K, N, R);
-  if (need && M > 0) {
-    lora_status s = check_ptrs(dy, codes, scales, a, b, u, dx, da, db, du, workspace);
-    if (s != LORA_OK) return s;
-    if (workspace_bytes < lora_delta_bwd_packed8_workspace_size(M, K, N, R)) return LORA_ERR_WORKSPACE;
-    if ((s = lora_unpack8(codes, scales, M, K, static_cast<uint8_t*>(workspace) + need, LORA_BF16, stream)) != LORA_OK)
-      return s;
+  if (!rank_ok(R)) return shape_ok(M, K) && shape_ok(M, N) ? LORA_ERR_RANK : LORA_ERR_SHAPE;
+  if (!shape_ok(M, K) || !shape_ok(M, N)) return LORA_ERR_SHAPE;
+  if (M == 0) return LORA_OK;                       // as lora_delta_bwd
+  lora_status s = check_ptrs(dy, codes, scales, a, b, u, dx, da, db, du, workspace);
+  if (s != LORA_OK) return s;
+  const BwdLayout L = bwd_layout(M, K, N, R);
+  if (workspace_bytes < L.bytes) return LORA_ERR_WORKSPACE;
+  int nsm = 0;
+  if ((s = device_ready(&nsm)) != LORA_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint32_t* status = reinterpret_cast<uint32_t*>(ws);
+  float *du_part = reinterpret_cast<float*>(ws + L.du), *db_part = reinterpret_cast<float*>(ws + L.db);
+  const int RP = padded_rank(int(R)), span = 2 * RP, m = int(M), n = int(N), k = int(K), C = int(chunks(M));
+  auto grid = [&](int64_t units) { return int(units < nsm ? units : nsm); };
+  // dU and dB partials: one pass over dy for ranks of up to 16, else a pass each
+  if (RP == 16) {
+    DyArgs y{};
+    y.n = 1;
+    DySite& d = y.s[0];
+    if (!tensor_map(&d.dy, dy, Elem::bf16, M, N, N, 32, 128, 64) ||
+        !tensor_map(&d.b, b, Elem::bf16, N, R, R, RP, 128, span) ||
+        !tensor_map(&d.u, u, Elem::bf16, M, R, R, RP, 128, span))
+      return LORA_ERR_CUDA;
+    d.du_part = du_part;
+    d.db_part = db_part;
+    d.M = m;
+    d.N = n;
+    d.alpha = alpha;
+    if (launch_dy(y, status, grid(cdiv(M, kDyChunk) * cdiv(N, kDySlice)), st) != cudaSuccess) return LORA_ERR_CUDA;
+  } else {
+    DownArgs down{};
+    WgArgs wg{};
+    down.n = wg.n = 1;
+    DownSite& d = down.s[0];
+    WgSite& w = wg.s[0];
+    if (!tensor_map(&d.in, dy, Elem::bf16, M, N, N, 32, 128, 64) ||
+        !tensor_map(&d.w, b, Elem::bf16, N, R, R, RP, 64, span) ||
+        !tensor_map(&w.in, dy, Elem::bf16, M, N, N, 64, 64, 128) ||
+        !tensor_map(&w.g, u, Elem::bf16, M, R, R, RP, 64, span))
+      return LORA_ERR_CUDA;
+    d.part = du_part;
+    d.M = w.M = m;
+    d.Kred = w.Cw = n;
+    d.alpha = w.alpha = alpha;
+    w.part = db_part;
+    if (launch_down(RP, true, down, status, grid(down_units(M, N, RP)), st) != cudaSuccess ||
+        launch_wgrad(RP, true, wg, status, grid(wgrad_units(M, N, RP)), st) != cudaSuccess)
+      return LORA_ERR_CUDA;
   }
-  // a shape or rank that is refused, and M = 0, are lora_delta_bwd's to answer
-  return lora_delta_bwd(dy, static_cast<uint8_t*>(workspace) + need, a, b, u, alpha, M, K, N, R, dx, da, db, du,
-                        workspace, need, stream);
+  // the rows of dU, and dB, from their partials
+  RowsArgs rows{};
+  rows.n = 1;
+  rows.R = int(R);
+  rows.RP = RP;
+  rows.s[0] = RowsSite{du_part, static_cast<__nv_bfloat16*>(du), m, int(cdiv(N, du_slice(RP))), 0};
+  CombineJobs jobs{};
+  jobs.n = 1;
+  jobs.j[0] = CombineJob{db_part, db, C, n, int(R), RP, 1};
+  if (launch_rows(rows, &jobs, nsm, st) != cudaSuccess) return LORA_ERR_CUDA;
+  // dX, then dA from the codes
+  UpArgs up{};
+  up.n = 1;
+  up.R = int(R);
+  UpSite& q = up.s[0];
+  if (!tensor_map(&q.a, du, Elem::bf16, M, R, R, RP, 128, span) || !tensor_map(&q.b, a, Elem::bf16, R, K, K, 64, RP, 128) ||
+      !tensor_map(&q.out, dx, Elem::f32, M, K, K, 32, 32, 128))
+    return LORA_ERR_CUDA;
+  q.M = m;
+  q.Nout = k;
+  q.alpha = 1.0f;
+  if (launch_up(RP, true, false, up, status, grid(up_units(M, K, RP)), st) != cudaSuccess) return LORA_ERR_CUDA;
+  return run_da(du, codes, scales, M, K, R, da, reinterpret_cast<float*>(ws + L.da), status, nsm, st);
 }
 
 }  // extern "C"
