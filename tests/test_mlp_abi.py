@@ -11,6 +11,24 @@ HEADER = os.path.join(ROOT, "include", "lora_mlp.h")
 F = 0x10000        # never dereferenced: the cases below fail their host-side checks first
 BIG = 1 << 40
 OK, NULL, SHAPE, ALIGN, RANK, WORKSPACE = range(6)
+VP, INT, I64, F32, SIZE = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+ARGS = {
+    "lora_layer_norm_fwd": (VP, INT, VP, VP, INT, F32, I64, I64, VP, VP, VP, VP),
+    "lora_layer_norm_bwd": (VP, INT, VP, VP, VP, INT, VP, VP, I64, I64, VP, VP, VP, VP, SIZE, VP),
+    "lora_pack8": (VP, INT, I64, I64, VP, VP, VP),
+    "lora_unpack8": (VP, VP, I64, I64, VP, INT, VP),
+    "lora_pack8_da": (VP, VP, VP, I64, I64, I64, VP, VP, SIZE, VP),
+    "lora_delta_bwd_packed8": (VP,) * 6 + (F32,) + (I64,) * 4 + (VP,) * 5 + (SIZE, VP),
+    "lora_gated_ffn_fwd": (VP,) * 5 + (INT,) + (I64,) * 3 + (VP, INT) + (VP,) * 5,
+    "lora_gated_ffn_bwd": (VP,) * 4 + (INT,) + (VP,) * 4 + (INT,) + (I64,) * 3 + (VP,) * 6,
+}
+
+
+def entry(name):
+    from deterministic_arithmetic_gb300 import _capi
+
+    return _capi.fn(name, ARGS[name])
+
 
 
 @pytest.fixture(scope="module")
@@ -39,9 +57,9 @@ def test_every_declared_symbol_is_exported(lib):
 
 
 def test_layer_norm_refusals(lib):
-    from deterministic_arithmetic_gb300 import _capi, layer_norm as ln
+    from deterministic_arithmetic_gb300 import layer_norm as ln
 
-    f = _capi.fn("lora_layer_norm_fwd", ln._FWD)
+    f = entry("lora_layer_norm_fwd")
 
     def fwd(x=F, xt=0, w=F, b=F, wt=0, M=4, N=64, y=F, mean=F, rstd=F):
         return f(x, xt, w, b, wt, 1e-5, M, N, y, mean, rstd, None)
@@ -50,7 +68,7 @@ def test_layer_norm_refusals(lib):
     assert fwd(N=0) == fwd(M=-1) == fwd(N=1 << 31) == fwd(xt=2) == fwd(wt=-1) == SHAPE
     assert fwd(x=None) == fwd(w=None) == fwd(y=None) == fwd(mean=None) == fwd(rstd=None) == NULL
     assert fwd(x=F + 2) == fwd(b=F + 4) == ALIGN
-    g = _capi.fn("lora_layer_norm_bwd", ln._BWD)
+    g = entry("lora_layer_norm_bwd")
     need = ln.layer_norm_bwd_workspace_size(4, 64)
     assert need > 0 and ln.layer_norm_bwd_workspace_size(4, 0) == 0
 
@@ -66,16 +84,16 @@ def test_layer_norm_refusals(lib):
 
 
 def test_pack8_refusals(lib):
-    from deterministic_arithmetic_gb300 import _capi, pack8
+    from deterministic_arithmetic_gb300 import pack8
 
-    f = _capi.fn("lora_pack8", pack8._PACK)
+    f = entry("lora_pack8")
     assert f(None, 0, 0, 64, None, None, None) == OK
     assert f(F, 0, 4, 0, F, F, None) == f(F, 5, 4, 8, F, F, None) == f(F, 0, -1, 8, F, F, None) == SHAPE
     assert f(None, 0, 4, 8, F, F, None) == f(F, 0, 4, 8, F, None, None) == NULL
     assert f(F + 2, 0, 4, 8, F, F, None) == f(F, 0, 4, 8, F + 8, F, None) == ALIGN
-    g = _capi.fn("lora_unpack8", pack8._UNPACK)
+    g = entry("lora_unpack8")
     assert g(F, F, 4, 8, F, 3, None) == SHAPE and g(F, None, 4, 8, F, 0, None) == NULL
-    h = _capi.fn("lora_pack8_da", pack8._DA)
+    h = entry("lora_pack8_da")
     need = pack8.pack8_da_workspace_size(300, 520, 16)
     assert need > 0 and pack8.pack8_da_workspace_size(300, 521, 16) == pack8.pack8_da_workspace_size(300, 520, 12) == 0
 
@@ -84,7 +102,7 @@ def test_pack8_refusals(lib):
 
     assert da(K=12) == da(M=-1) == SHAPE and da(R=72) == da(R=4) == RANK
     assert da(du=None) == da(M=0, out=None) == NULL and da(out=F + 4) == ALIGN and da(size=need - 1) == WORKSPACE
-    b = _capi.fn("lora_delta_bwd_packed8", pack8._BWD)
+    b = entry("lora_delta_bwd_packed8")
     size = pack8.lora_delta_bwd_packed8_workspace_size(64, 128, 96, 16)
 
     def bwd(dy=F, codes=F, M=64, K=128, N=96, R=16, ws=F, n=size):
@@ -98,9 +116,7 @@ def test_pack8_refusals(lib):
 
 
 def test_gated_ffn_refusals(lib):
-    from deterministic_arithmetic_gb300 import _capi, gated_ffn as ffn
-
-    f = _capi.fn("lora_gated_ffn_fwd", ffn._FWD)
+    f = entry("lora_gated_ffn_fwd")
 
     def fwd(x=F, wg=F, dg=None, du=None, act=0, M=4, K=64, N=32, h=F, keep=0, g=None, u=None, gs=None, us=None):
         return f(x, wg, F, dg, du, act, M, K, N, h, keep, g, u, gs, us, None)
@@ -110,7 +126,7 @@ def test_gated_ffn_refusals(lib):
     assert fwd(x=None) == fwd(h=None) == fwd(dg=F) == fwd(du=F) == fwd(keep=1, g=F) == NULL
     assert fwd(keep=2, g=F, u=F, gs=F) == NULL
     assert fwd(wg=F + 2) == fwd(dg=F + 4, du=F) == fwd(keep=1, g=F, u=F + 8) == ALIGN
-    b = _capi.fn("lora_gated_ffn_bwd", ffn._BWD)
+    b = entry("lora_gated_ffn_bwd")
 
     def bwd(dh=F, x=F, keep=1, g=F, gs=None, us=None, act=0, M=4, K=64, N=32, dx=F, dwg=F, dwu=F):
         return b(dh, x, F, F, keep, g, F, gs, us, act, M, K, N, dx, F, F, dwg, dwu, None)
