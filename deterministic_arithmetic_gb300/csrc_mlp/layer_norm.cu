@@ -37,6 +37,10 @@ constexpr int kPerThread = 16;                      // columns of a row a thread
 constexpr int kMaxWarps = 16;                       // warps of a row group
 constexpr int kHeldN = 32 * kPerThread * kMaxWarps; // longest row a group owns
 constexpr int kBlockWarps = 8;                      // warps of a CTA of short rows (several groups)
+// The forward kernel is built for CTAs of up to 8, 12 and 16 warps, with the registers that this many
+// CTAs on an SM leave a thread (5120 columns, bf16: 34.7 us with the 16-warp build, 27.0 with the 12).
+constexpr int kMidWarps = 12;
+constexpr int fwd_ctas(int warps) { return warps == 8 ? 3 : (warps == 12 ? 2 : 1); }
 // Rows a thread has in hand, the current one and those to come: as many as leave two CTAs of 256
 // threads (or one of 512) their shared memory in the backward pass.
 template <bool F32>
@@ -231,7 +235,7 @@ __device__ __forceinline__ void clear_slots(float* slots, int n) {
 
 
 template <int KIND, int VEC, bool FULL, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, WARPS == kMaxWarps ? 1 : 3)
+__global__ void __launch_bounds__(32 * WARPS, fwd_ctas(WARPS))
     ln_fwd_kernel(const void* __restrict__ x, const void* __restrict__ weight, const void* __restrict__ bias, int w_type,
                   float eps, uint32_t M, int N, int W, void* __restrict__ y, float* __restrict__ mean_out,
                   float* __restrict__ rstd_out) {
@@ -656,7 +660,8 @@ cudaError_t fwd(const void* x, const void* w, const void* b, int w_type, float e
                       eps, M, int(N), y, mean, rstd);
   }
   const int W = warps_per_row(N), G = groups_per_block(W), threads = 32 * W * G;
-  const int64_t work = cdiv(M, G), most = int64_t(nsm) * (threads <= 32 * kBlockWarps ? 3 : 1);
+  const int built = threads <= 32 * kBlockWarps ? kBlockWarps : (threads <= 32 * kMidWarps ? kMidWarps : kMaxWarps);
+  const int64_t work = cdiv(M, G), most = int64_t(nsm) * fwd_ctas(built);
   const dim3 grid(unsigned(work < most ? work : most));
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, dim3(threads), fwd_smem<KIND, VEC>(threads), st, x, w, b, w_type, eps, uint32_t(M),
@@ -665,8 +670,10 @@ cudaError_t fwd(const void* x, const void* w, const void* b, int w_type, float e
   // rows that fill their threads exactly take kernels without the tests of the row's end (31 against 38 us at 8192 x 4096)
   constexpr bool vec = VEC > 2;
   const bool full = vec && N == 32 * kPerThread * W;
-  if (threads <= 32 * kBlockWarps)
+  if (built == kBlockWarps)
     return full ? go(ln_fwd_kernel<KIND, VEC, vec, kBlockWarps>) : go(ln_fwd_kernel<KIND, VEC, false, kBlockWarps>);
+  if (built == kMidWarps)
+    return full ? go(ln_fwd_kernel<KIND, VEC, vec, kMidWarps>) : go(ln_fwd_kernel<KIND, VEC, false, kMidWarps>);
   return full ? go(ln_fwd_kernel<KIND, VEC, vec, kMaxWarps>) : go(ln_fwd_kernel<KIND, VEC, false, kMaxWarps>);
 }
 
@@ -697,25 +704,25 @@ cudaError_t bwd(const void* dy, const void* x, const void* xs, const void* w, in
   return full ? go(ln_bwd_kernel<KIND, XK, VEC, vec, kMaxWarps>) : go(ln_bwd_kernel<KIND, XK, VEC, false, kMaxWarps>);
 }
 
-template <int KIND, int VEC, bool FULL, int WARPS>
+template <int KIND, int VEC, bool FULL>
 cudaError_t prepare_as() {
-  const int fs = fwd_smem<KIND, VEC>(32 * WARPS), bs = bwd_smem<KIND, KIND, VEC>(32 * WARPS);
-  const int ps = bwd_smem<KIND, kPacked, VEC>(32 * WARPS);
-  cudaError_t e;
-  if ((e = set_smem(ln_fwd_kernel<KIND, VEC, FULL, WARPS>, fs)) != cudaSuccess ||
-      (e = set_smem(ln_bwd_kernel<KIND, KIND, VEC, FULL, WARPS>, bs)) != cudaSuccess)
-    return e;
-  return set_smem(ln_bwd_kernel<KIND, kPacked, VEC, FULL, WARPS>, ps);
+  cudaError_t e = cudaSuccess;
+  auto fwd_ok = [&](auto kernel, int warps) { return (e = set_smem(kernel, fwd_smem<KIND, VEC>(32 * warps))) == cudaSuccess; };
+  auto bwd_ok = [&](auto kernel, auto packed, int warps) {
+    return (e = set_smem(kernel, bwd_smem<KIND, KIND, VEC>(32 * warps))) == cudaSuccess &&
+           (e = set_smem(packed, bwd_smem<KIND, kPacked, VEC>(32 * warps))) == cudaSuccess;
+  };
+  fwd_ok(ln_fwd_kernel<KIND, VEC, FULL, kBlockWarps>, kBlockWarps) &&
+      fwd_ok(ln_fwd_kernel<KIND, VEC, FULL, kMidWarps>, kMidWarps) &&
+      fwd_ok(ln_fwd_kernel<KIND, VEC, FULL, kMaxWarps>, kMaxWarps) &&
+      bwd_ok(ln_bwd_kernel<KIND, KIND, VEC, FULL, kBlockWarps>, ln_bwd_kernel<KIND, kPacked, VEC, FULL, kBlockWarps>, kBlockWarps) &&
+      bwd_ok(ln_bwd_kernel<KIND, KIND, VEC, FULL, kMaxWarps>, ln_bwd_kernel<KIND, kPacked, VEC, FULL, kMaxWarps>, kMaxWarps);
+  return e;
 }
 template <int KIND, int VEC>
 cudaError_t prepare() {
-  constexpr bool vec = VEC > 2;
-  cudaError_t e;
-  if ((e = prepare_as<KIND, VEC, false, kBlockWarps>()) != cudaSuccess ||
-      (e = prepare_as<KIND, VEC, false, kMaxWarps>()) != cudaSuccess ||
-      (e = prepare_as<KIND, VEC, vec, kBlockWarps>()) != cudaSuccess)
-    return e;
-  return prepare_as<KIND, VEC, vec, kMaxWarps>();
+  const cudaError_t e = prepare_as<KIND, VEC, false>();
+  return e == cudaSuccess && VEC > 2 ? prepare_as<KIND, VEC, (VEC > 2)>() : e;
 }
 
 }  // namespace
