@@ -23,6 +23,8 @@
 // the row groups of a CTA add up in shared memory, and each CTA leaves one partial
 // row; a second kernel adds the partials in order. The number of CTAs depends on M
 // and N only, so reruns give the same bits on any device.
+#include <algorithm>
+
 #include "../csrc/common.cuh"
 #include "../csrc/kernels.h"
 #include "elems.cuh"
@@ -45,7 +47,7 @@ constexpr int fwd_ctas(int warps) { return warps == 8 ? 3 : (warps == 12 ? 2 : 1
 // threads (or one of 512) their shared memory in the backward pass.
 template <bool F32>
 constexpr int stages_of = F32 ? 3 : 4;
-constexpr int kMaxParts = 304;                      // partial rows of dw and db: two CTAs on each of 152 SMs
+constexpr int kSMs = 152, kMaxParts = 3 * kSMs;     // partial rows of dw and db (parts_of)
 
 inline int warps_per_row(int64_t n) { return int(cdiv(n, 32 * kPerThread)); }
 inline int groups_per_block(int w) { return w >= kBlockWarps ? 1 : kBlockWarps / w; }
@@ -605,14 +607,15 @@ __global__ void __launch_bounds__(512)
   const int64_t c = int64_t(blockIdx.x) * 64 + 2 * lane;
   float2 s = make_float2(0.f, 0.f);
   if (c < cols) {                                    // ld is even: the pair lies inside the row
-    float2 v[kMaxParts / 16];                        // all loads in flight together
+    constexpr int kDeep = (kMaxParts + 15) / 16;
+    float2 v[kDeep];                                 // all loads in flight together
 #pragma unroll
-    for (int i = 0; i < kMaxParts / 16; ++i) {
+    for (int i = 0; i < kDeep; ++i) {
       const int p = warp + 16 * i;
       v[i] = p < P ? __ldcg(reinterpret_cast<const float2*>(part + int64_t(p) * ld + c)) : make_float2(0.f, 0.f);
     }
 #pragma unroll
-    for (int i = 0; i < kMaxParts / 16; ++i) s.x += v[i].x, s.y += v[i].y;
+    for (int i = 0; i < kDeep; ++i) s.x += v[i].x, s.y += v[i].y;
   }
   sums[warp][lane] = s;
   __syncthreads();
@@ -642,12 +645,13 @@ int bwd_smem(int threads) {
   return slots > sums ? slots : sums;
 }
 
-// Partial rows of a backward pass: at most kMaxParts, and no more than there are stages of rows. The
-// looped kernels' share of rows a partial is fixed in the same way.
+// Partial rows of a backward pass, one a CTA: as many CTAs as the 152 SMs hold at once of 128 registers
+// a thread (three of 160 threads, two of 256, one above), and no more than there are rows for.
 constexpr int kLongParts = 64;
 int parts_of(int64_t M, int64_t N) {
-  const int64_t p = cdiv(M, N <= kHeldN ? groups_per_block(warps_per_row(N)) : kBlockWarps);
-  return int(p < kMaxParts ? p : kMaxParts);
+  if (N > kHeldN) return int(std::min<int64_t>(cdiv(M, kBlockWarps), kLongParts));
+  const int W = warps_per_row(N), G = groups_per_block(W), held = 512 / (32 * W * G);
+  return int(std::min<int64_t>(cdiv(M, G), kSMs * std::max(1, std::min(held, kMaxParts / kSMs))));
 }
 int64_t part_ld(int64_t N) { return (2 * N + 3) & ~int64_t(3); }
 
