@@ -88,8 +88,8 @@ template <int MODE, int CG>
 lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream_t st) {
   constexpr int products = MODE == kDw ? 2 : 1;
   P.bn = bn;
-  // a batch smaller than a tile: only its rows are copied (what the other rows of the tile hold
-  // reaches only rows of the accumulator that nobody reads)
+  // a batch smaller than a tile: only its rows are copied, and the ring holds more stages (the other
+  // rows of the tile reach only rows of the accumulator that nobody reads)
   const int a_rows = MODE != kDw && P.m < kBM ? int(round8(P.m)) : kBM;
   P.blocked = MODE == kDw ? o.a_cols % 64 == 0 && o.b_cols % 64 == 0 : o.b_cols % 64 == 0;
   for (int i = 0; i < 2; ++i) {
@@ -100,8 +100,8 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
     if (!a || !b) return LORA_ERR_CUDA;
   }
   const int b_bytes = (MODE == kFwd ? 2 : 1) * bn * 128 / CG;
-  P.stage_bytes = kABytes + b_bytes;
-  P.copy_bytes = a_rows * kBK * 2 + b_bytes;
+  P.a_bytes = a_rows * kBK * 2;
+  P.stage_bytes = P.a_bytes + b_bytes;
   P.stages = kRingBytes / P.stage_bytes < kMaxStages ? kRingBytes / P.stage_bytes : kMaxStages;
   P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, bn));

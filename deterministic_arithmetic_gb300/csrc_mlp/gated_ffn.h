@@ -21,8 +21,7 @@ struct FfnArgs {
   int nk;                          // 64-deep blocks of one product's reduction
   int bn;                          // tile columns (in kFwd of each projection)
   int blocked;                     // kDx, kDw: the maps whose rows lie along the reduction are block_map's
-  int stages, stage_bytes;
-  int copy_bytes;                  // what a CTA's copies of a stage bring (a small batch's rows of A are fewer)
+  int stages, stage_bytes, a_bytes;   // of the ring; of a stage (all of it copied); of it A's rows
   int tiles_m, tiles_n;            // tiles of one product
   int whole, total;                // units of work: `whole` tiles, then halves of the remaining ones
 };

@@ -28,6 +28,7 @@
 #include "gated_ffn.h"
 #include "mlp.h"
 #include "pack8.cuh"
+#include "waits.cuh"
 
 namespace mlp {
 
@@ -35,12 +36,15 @@ using namespace lora;
 
 constexpr int kBM = 128, kBK = 64;                 // rows of A and depth of a k-block
 constexpr int kABytes = kBM * kBK * 2;             // 16 KB
-constexpr int kMaxStages = 8;
-constexpr int kRingBytes = 208 * 1024;             // the operand ring
+constexpr int kMaxStages = 16;
+constexpr int kRingBytes = 192 * 1024;             // the operand ring
+// Behind it: a stage of a small batch holds fewer than 128 rows of A, and the MMAs' reads of the other
+// rows (whose products nobody reads) run on into what follows, in the last stage to here.
+constexpr int kRingSlack = kABytes;
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
 constexpr int kAccCols = 256;                      // TMEM columns of an accumulator
-constexpr size_t kGemmSmem = kRingBytes + 1024 + (2 * kMaxStages + 6) * 8 + 16;
+constexpr size_t kGemmSmem = kRingBytes + kRingSlack + 1024 + (2 * kMaxStages + 6) * 8 + 16;
 static_assert(kGemmSmem < 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kRingBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kRingBytes + kRingSlack);
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
@@ -252,10 +256,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       prefetch_map(&P.b[i]);
     }
   }
+  // A pair's TMEM is allocated, and at the end freed, by both CTAs together: each only once the other is
+  // known to run (the hardware starts a cluster's CTAs together, but not in the same instant, and an
+  // allocation met by no peer does not return). The same meeting shows that the peer's barriers are set up.
   __syncwarp();
+  if constexpr (CG == 2) cluster_sync_all();
   if (warp == 1) acc_alloc<CG>(smem_u32(tmem_slot));
+  __syncwarp();
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync_all();       // the peer's barriers are set up before anything arrives there
+  if constexpr (CG == 2) cluster_sync_all();
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -282,10 +291,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
         // the boxes are a whole tile's: half a tile uses half of what it loads
         for (int kb = 0; kb < blocks; ++kb) {
-          if (wait(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
-            const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + kABytes;
+          if (wait_for(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
+            const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + P.a_bytes;
             const uint32_t bar = CG == 2 ? peer_addr(full(idx), 0) : full(idx);
-            if (rank == 0) mbar_expect_tx(full(idx), uint32_t(CG * P.copy_bytes));
+            if (rank == 0) mbar_expect_tx(full(idx), uint32_t(CG * stage_bytes));
             if constexpr (MODE == kFwd) {
               load2d<CG>(st, &P.a[0], bar, kb * kBK, row0, pa);
               if constexpr (CG == 2) {             // the pair's columns: 128 of the gate, 128 of up
@@ -316,15 +325,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
           if (++idx == stages) idx = 0, phase ^= 1u;
         }
       }
-      if (rank == 0) {                             // the copies of both CTAs arrive here
-        for (int s = 0; s < stages; ++s)
-          if (issued & (1u << s)) wait_drain(full(s), (parities >> s) & 1u, ab, kSiteFfn + 3);
-      } else if (*ab.flag) {
-        // Giving up: this CTA's copies report to the other one's barriers, which may no longer be
-        // waited on. They land long before this; the tile loop's own waits see to them otherwise.
+      // Nothing may reach this CTA's shared memory once it has gone: neither copies (those of both CTAs
+      // report to the first one) nor the MMAs' last arrivals at `empty`, which come from the other CTA's
+      // tensor core and which no later copy waits for. (A CTA of the next launch may take the place at once.)
+      for (int s = 0; s < stages; ++s) {
+        if (!(issued & (1u << s))) continue;
+        if (rank == 0) wait_drain(full(s), (parities >> s) & 1u, ab, kSiteFfn + 3);
+        if (!*ab.flag) wait_for(empty(s), (parities >> s) & 1u, ab, kSiteFfn + 8);
+      }
+      if (*ab.flag)                                // giving up: what is on its way lands long before this
         for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainLimitNs;) {
         }
-      }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
@@ -333,19 +344,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       // ones (64-column blocks 8 KB apart) step 16 rows of 128 bytes.
       constexpr uint32_t a_step = MODE == kDw ? 2048u : 32u, b_step = MODE == kFwd ? 32u : 2048u;
       const uint64_t a0 = smem_desc(base, MODE == kDw ? 8192u : 16u, 1024u, kLayoutSW128);
-      const uint64_t b0 = smem_desc(base + kABytes, MODE == kFwd ? 16u : 8192u, 1024u, kLayoutSW128);
+      const uint64_t b0 = smem_desc(base + P.a_bytes, MODE == kFwd ? 16u : 8192u, 1024u, kLayoutSW128);
       int idx = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       for (int u = first; u < P.total; u += step) {
-        bool ok = CG == 2 ? wait_cluster(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4)
-                          : wait(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4);
-        ok = __all_sync(0xffffffffu, ok);
+        bool ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
         tc_fence_after();
         const int bn = unit_at<MODE, CG>(P, u).bn;
         const uint32_t idesc = idesc_bf16(CG * kBM, MODE == kFwd ? 2 * bn : bn, MODE == kDw, MODE != kFwd);
         const uint32_t d = tmem + buf * kAccCols;
         for (int kb = 0; kb < blocks; ++kb) {
-          ok = __all_sync(0xffffffffu, ok && wait(full(idx), phase, ab, kSiteFfn + 5));
+          ok = __all_sync(0xffffffffu, ok && wait_for(full(idx), phase, ab, kSiteFfn + 5));
           if (ok) {
             tc_fence_after();
             const uint32_t off = uint32_t(idx) * stage_bytes;
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     uint32_t tphase = 0;
     for (int u = first; u < P.total; u += step) {
       const Unit w = unit_at<MODE, CG>(P, u);
-      const bool ok = __all_sync(0xffffffffu, wait(tfull(buf), tphase, ab, kSiteFfn + 7));
+      const bool ok = __all_sync(0xffffffffu, wait_for(tfull(buf), tphase, ab, kSiteFfn + 7));
       tc_fence_after();
       const int64_t row = int64_t(w.tm * CG + rank) * kBM + q * 32 + lane;
       const uint32_t acc = tmem + buf * kAccCols + lanes;
@@ -451,6 +460,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     tc_fence_after();
     acc_free<CG>(tmem);
   }
+  __syncwarp();
+  if constexpr (CG == 2) cluster_sync_all();       // nor before the peer has freed its half
 }
 
 }  // namespace mlp

@@ -665,7 +665,8 @@ cudaError_t fwd(const void* x, const void* w, const void* b, int w_type, float e
   }
   const int W = warps_per_row(N), G = groups_per_block(W), threads = 32 * W * G;
   const int built = threads <= 32 * kBlockWarps ? kBlockWarps : (threads <= 32 * kMidWarps ? kMidWarps : kMaxWarps);
-  const int64_t work = cdiv(M, G), most = int64_t(nsm) * fwd_ctas(built);
+  // what an SM holds at once: 80 registers a thread (128 in the 16-warp build)
+  const int64_t work = cdiv(M, G), most = int64_t(nsm) * std::max(1, (built == kMaxWarps ? 512 : 800) / threads);
   const dim3 grid(unsigned(work < most ? work : most));
   auto go = [&](auto kernel) {
     return launch_pdl(kernel, grid, dim3(threads), fwd_smem<KIND, VEC>(threads), st, x, w, b, w_type, eps, uint32_t(M),

@@ -20,6 +20,7 @@
 #include "../csrc/kernels.h"
 #include "elems.cuh"
 #include "mlp.h"
+#include "waits.cuh"
 
 namespace mlp {
 namespace {
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
       for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
         const int ct = u % P.n_ct, ch = u / P.n_ct, n = steps_of(ch);
         for (int i = 0; i < n; ++i) {
-          if (wait(rempty(r.idx), r.phase ^ 1u, ab, kSiteDa + 1)) {
+          if (wait_for(rempty(r.idx), r.phase ^ 1u, ab, kSiteDa + 1)) {
             const uint32_t st = base + raw_off + r.idx * C::kRawBytes;
             const int m = ch * kWgradChunk + i * C::kRows;
             mbar_expect_tx(rfull(r.idx), C::kRawBytes);
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
       const int n = steps_of(u / P.n_ct);
       for (int i = 0; i < n; ++i) {
         // the stage's copies have landed when it has been expanded
-        bool ok = wait(wfull(i), (wphase >> i) & 1u, ab, kSiteDa + 3);
-        ok = __all_sync(0xffffffffu, ok && wait(tempty(g.idx), g.phase ^ 1u, ab, kSiteDa + 4));
+        bool ok = wait_for(wfull(i), (wphase >> i) & 1u, ab, kSiteDa + 3);
+        ok = __all_sync(0xffffffffu, ok && wait_for(tempty(g.idx), g.phase ^ 1u, ab, kSiteDa + 4));
         if (ok) {
           tc_fence_after();
           const uint32_t d = tmem + g.idx * C::kGroupCols;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
 #pragma unroll
       for (int i = 0; i < C::kSteps; ++i) {
         if (i < n) {
-          const bool ok = __all_sync(0xffffffffu, wait(tfull(g.idx), g.phase, ab, kSiteDa + 6));
+          const bool ok = __all_sync(0xffffffffu, wait_for(tfull(g.idx), g.phase, ab, kSiteDa + 6));
           all = all && ok;
           tc_fence_after();
 #pragma unroll
@@ -278,8 +279,8 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
       for (int k = 0; k < 4; ++k) s[k] = next[k];
       scales_of(u + gridDim.x, next);                   // the next unit's, loaded under this one's work
       if (team >= n) continue;
-      bool ok = wait(rfull(mine % C::kRaw), (mine / C::kRaw) & 1u, ab, kSiteDa + 7);
-      ok = ok && wait(wempty(team), wphase, ab, kSiteDa + 8);
+      bool ok = wait_for(rfull(mine % C::kRaw), (mine / C::kRaw) & 1u, ab, kSiteDa + 7);
+      ok = ok && wait_for(wempty(team), wphase, ab, kSiteDa + 8);
       ok = __all_sync(0xffffffffu, ok);
       wphase ^= 1u;
       if (ok) {

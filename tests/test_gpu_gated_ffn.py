@@ -186,6 +186,18 @@ def test_rows_do_not_depend_on_the_batch(M, K, F):
     assert all(torch.equal(a, b) for a, b in zip(whole + dw, again + dw2))
 
 
+def test_pairs_start_while_the_gpu_is_full():
+    """Backward passes back to back: the pairs of CTAs of the product dx start on SMs that are full of the
+    element-wise step's CTAs, the two of a pair apart from each other. Each pass gives the same bits."""
+    from deterministic_arithmetic_gb300 import gated_ffn as ffn
+
+    t = inputs(4096, 2048, 8192)
+    _, gate, up = ffn.gated_ffn_fwd(t["x"], t["wg"], t["wu"], save="bf16")
+    outs = [ffn.gated_ffn_bwd(t["dh"], None, t["wg"], t["wu"], gate, up, weight_grads=False) for _ in range(30)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o in outs[1:] for a, b in zip(o[:3], outs[0][:3]))
+
+
 def test_extreme_activations():
     """Large and infinite gates: the tails are act's limits, and no NaN comes of 0 times infinity in a slope."""
     from deterministic_arithmetic_gb300 import gated_ffn as ffn
