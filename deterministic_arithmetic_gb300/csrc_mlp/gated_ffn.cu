@@ -135,13 +135,15 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
 // any tile's fixed part takes.
 template <int MODE>
 lora_status launch(FfnArgs& P, const Operands& o, int nsm, cudaStream_t st) {
-  constexpr int most = MODE == kFwd ? 128 : 256, least = MODE == kFwd ? 32 : 64;
+  constexpr int most = MODE == kFwd ? 128 : 256;
+  // narrower tiles go in steps of whole groups of 32 (packed values kept), 8 columns, or 64-column blocks
+  const int step = MODE != kFwd ? 64 : (P.keep_kind == LORA_KEEP_PACKED8 ? 32 : 8), least = MODE == kFwd ? 32 : 64;
   const int64_t products = MODE == kDw ? 2 : 1;
   if (P.m > kBM && products * cdiv(P.m, 2 * kBM) * cdiv(P.n, most) >= g_pairs)
     return launch_as<MODE, 2>(P, o, most, nsm, st);
   int bn = most;
   int64_t best = INT64_MAX;
-  for (int w = most; w >= least; w /= 2) {
+  for (int w = most; w >= least; w -= step) {
     const int64_t cost = cdiv(products * cdiv(P.m, kBM) * cdiv(P.n, w), nsm) * ((MODE == kFwd ? 2 : 1) * w + 64);
     if (cost < best) best = cost, bn = w;
   }

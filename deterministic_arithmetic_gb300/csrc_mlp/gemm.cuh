@@ -159,7 +159,7 @@ __device__ __forceinline__ float act_slope(int act, float y, float p) {
   return fmaf(y * p, q * dz, p);
 }
 
-// 32 consecutive columns from `col` of a row, as bf16 (columns at or past n are left alone; n % 8 == 0).
+// 32 consecutive columns from `col` of a row, as bf16 (columns at or past n, a multiple of 8, are left alone).
 __device__ __forceinline__ void store_row32(__nv_bfloat16* row, int col, int n, const float (&v)[32]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -169,10 +169,11 @@ __device__ __forceinline__ void store_row32(__nv_bfloat16* row, int col, int n, 
                      bf16x2_bits(v[8 * j + 4], v[8 * j + 5]), bf16x2_bits(v[8 * j + 6], v[8 * j + 7]));
 }
 
-// One of the forward's kept values of a row, 32 columns from `col` (a multiple of 32 when packed).
-__device__ __forceinline__ void keep_row32(const FfnArgs& P, int which, int64_t row, int col, float (&v)[32]) {
+// One of the forward's kept values of a row, 32 columns from `col`, those before `end`. Packed: `col` is a
+// multiple of 32, and `end` the row's unless a whole chunk away.
+__device__ __forceinline__ void keep_row32(const FfnArgs& P, int which, int64_t row, int col, int end, float (&v)[32]) {
   if (P.keep_kind == LORA_KEEP_BF16) {
-    store_row32(static_cast<__nv_bfloat16*>(P.keep[which]) + row * P.n, col, P.n, v);
+    store_row32(static_cast<__nv_bfloat16*>(P.keep[which]) + row * P.n, col, end, v);
     return;
   }
   const int G = (P.n + 31) >> 5;
@@ -391,8 +392,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const uint32_t acc = tmem + buf * kAccCols + lanes;
       if (ok) {
         for (int c = 32 * half; c < w.bn; c += 64) {
-          const int col = w.col + c;
-          if (col >= P.n) break;
+          const int col = w.col + c, end = min(P.n, w.col + w.bn);   // (bn need not be whole chunks)
+          if (col >= end) break;
           uint32_t r0[32];
           tmem_ld32(acc + c, r0);
           if constexpr (MODE == kFwd) {
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                 const float* du = P.delta[1] + row * P.n + col;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                  if (col + 4 * j < P.n) {
+                  if (col + 4 * j < end) {
                     const float4 a = __ldcs(reinterpret_cast<const float4*>(dg) + j);
                     const float4 b = __ldcs(reinterpret_cast<const float4*>(du) + j);
                     g[4 * j] += a.x; g[4 * j + 1] += a.y; g[4 * j + 2] += a.z; g[4 * j + 3] += a.w;
@@ -423,10 +424,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               float h[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) h[i] = g[i] * act_p(P.act, g[i]) * v[i];
-              store_row32(P.out[0] + row * P.n, col, P.n, h);
+              store_row32(P.out[0] + row * P.n, col, end, h);
               if (P.keep_kind != LORA_KEEP_NONE) {
-                keep_row32(P, 0, row, col, g);
-                keep_row32(P, 1, row, col, v);
+                keep_row32(P, 0, row, col, end, g);
+                keep_row32(P, 1, row, col, end, v);
               }
             }
           } else {
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r0[i]);
-              store_row32(P.out[w.prod] + row * P.n, col, P.n, v);
+              store_row32(P.out[w.prod] + row * P.n, col, end, v);
             }
           }
         }
