@@ -84,7 +84,7 @@ bool rows_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool bl
   return blocked ? block_map(m, p, rows, cols, kBK, blocks) : tensor_map(m, p, Elem::bf16, rows, cols, cols, 64, kBK, 128);
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, bool SPLIT = false>
 lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream_t st) {
   constexpr int products = MODE == kDw ? 2 : 1;
   P.bn = bn;
@@ -102,7 +102,8 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   const int b_bytes = (MODE == kFwd ? 2 : 1) * bn * 128 / CG;
   P.a_bytes = a_rows * kBK * 2;
   P.stage_bytes = P.a_bytes + b_bytes;
-  P.stages = kRingBytes / P.stage_bytes < kMaxStages ? kRingBytes / P.stage_bytes : kMaxStages;
+  const int ring = kRingBytes - (SPLIT ? bn * kBM * 4 : 0);        // a split's sums arrive behind it
+  P.stages = ring / P.stage_bytes < kMaxStages ? ring / P.stage_bytes : kMaxStages;
   P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, bn));
   const int64_t total = int64_t(products) * P.tiles_m * P.tiles_n;
@@ -113,9 +114,10 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   const bool halves = CG == 2 && 2 * rest <= g_pairs;
   P.whole = int(halves ? total - rest : total);
   P.total = int(halves ? total + rest : total);
-  const int most = CG == 2 ? g_pairs : nsm;
+  constexpr int cluster = SPLIT ? 2 : CG;
+  const int most = SPLIT ? P.total : (CG == 2 ? g_pairs : nsm);    // a split's clusters have a tile each
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(CG * (P.total < most ? P.total : most)));
+  cfg.gridDim = dim3(unsigned(cluster * (P.total < most ? P.total : most)));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = kGemmSmem;
   cfg.stream = st;
@@ -123,10 +125,10 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {unsigned(CG), 1, 1};
+  attr[1].val.clusterDim = {unsigned(cluster), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<MODE, CG>, P, status_block()) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  cfg.numAttrs = cluster == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<MODE, CG, SPLIT>, P, status_block()) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
 // Pairs of CTAs where the output has more rows than one CTA's and the 256 x 256 tiles give every
@@ -146,6 +148,16 @@ lora_status launch(FfnArgs& P, const Operands& o, int nsm, cudaStream_t st) {
   for (int w = most; w >= least; w -= step) {
     const int64_t cost = cdiv(products * cdiv(P.m, kBM) * cdiv(P.n, w), nsm) * ((MODE == kFwd ? 2 : 1) * w + 64);
     if (cost < best) best = cost, bn = w;
+  }
+  if constexpr (MODE == kDx) {
+    // two CTAs a tile, half the reduction each, where that takes less by the same reckoning
+    int split = 0;
+    best *= 2;
+    for (int w = 128; w >= 64; w -= 64) {
+      const int64_t cost = cdiv(2 * cdiv(P.m, kBM) * cdiv(P.n, w), nsm) * (w + 64);
+      if (cost < best) best = cost, split = w;
+    }
+    if (split) return launch_as<kDx, 1, true>(P, o, split, nsm, st);
   }
   return launch_as<MODE, 1>(P, o, bn, nsm, st);
 }
@@ -175,7 +187,8 @@ cudaError_t prepare() {
 }  // namespace
 
 cudaError_t prepare_ffn() {
-  cudaError_t e;
+  cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<kDx, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
+  if (e != cudaSuccess) return e;
   if ((e = prepare<kFwd>()) != cudaSuccess || (e = prepare<kDx>()) != cudaSuccess) return e;
   return prepare<kDw>();
 }

@@ -2,7 +2,7 @@
 // 128-byte-swizzled shared memory, tcgen05 MMAs into FP32 accumulators in TMEM, three products:
 //   kFwd  G = x Wg^T and U = x Wu^T over the same x tile, and in the epilogue h = act(G + Dg) (U + Du),
 //         with G + Dg and U + Du kept in bf16 or in 8 bits when asked for
-//   kDx   dx = dG Wg + dU Wu, one accumulator over both products
+//   kDx   dx = dG Wg + dU Wu, an accumulator a product, added at the end
 //   kDw   dWg = dG^T x and dWu = dU^T x
 //
 // An accumulator takes its whole reduction in order, 16 products at a time, from a cleared start:
@@ -15,6 +15,10 @@
 // operand byte in shared memory feeds twice the products of a CTA alone. The pair's first CTA
 // issues the MMAs of both; copies of both arrive at its barriers. CG = 1 is a CTA alone with 128
 // rows and bn columns, for batches and outputs too small to give every pair a tile.
+//
+// SPLIT (kDx, CG = 1): the two products of a tile by two CTAs of a cluster at once, for outputs of few
+// tiles, whose time is their reductions' length; the second CTA sends its accumulator to the first's
+// shared memory. The same two sums are added, so the bits are those of one CTA doing both.
 //
 // Persistent CTAs (pairs) take tiles in turn. Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 read the
 // accumulator and write the tile (a warp its quarter of the lanes, the two halves of the warps
@@ -44,7 +48,7 @@ constexpr int kRingSlack = kABytes;
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
 constexpr int kAccCols = 256;                      // TMEM columns of an accumulator
-constexpr size_t kGemmSmem = kRingBytes + kRingSlack + 1024 + (2 * kMaxStages + 6) * 8 + 16;
+constexpr size_t kGemmSmem = kRingBytes + kRingSlack + 1024 + (2 * kMaxStages + 7) * 8 + 16;
 static_assert(kGemmSmem < 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -220,7 +224,7 @@ __device__ __forceinline__ Unit unit_at(const FfnArgs& P, int u) {
   return w;
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, bool SPLIT = false>
 __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs P, uint32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -233,11 +237,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
   const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 4);
   const uint32_t never = drain + 8u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
+  const uint32_t sent = drain + 16u;                 // SPLIT: the second CTA's accumulator has arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 7);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const uint32_t warp = warp_id(), lane = lane_id();
-  const int rank = CG == 2 ? int(cluster_rank()) : 0;       // 0 issues the MMAs
+  static_assert(!SPLIT || (MODE == kDx && CG == 1), "a split is dx's");
+  constexpr int kCluster = SPLIT ? 2 : CG;
+  const int peer = kCluster == 2 ? int(cluster_rank()) : 0;
+  const int rank = CG == 2 ? peer : 0;                      // of a pair: 0 issues the MMAs
   const int stages = P.stages, stage_bytes = P.stage_bytes;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -250,6 +258,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     }
     mbar_init(drain, 1);
     mbar_init(never, 1);
+    mbar_init(sent, kEpiWarps);
     *abort_flag = 0u;
     mbar_fence_init();
     for (int i = 0; i < 2; ++i) {
@@ -261,7 +270,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   // known to run (the hardware starts a cluster's CTAs together, but not in the same instant, and an
   // allocation met by no peer does not return). The same meeting shows that the peer's barriers are set up.
   __syncwarp();
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (kCluster == 2) cluster_sync_all();
   if (warp == 1) acc_alloc<CG>(smem_u32(tmem_slot));
   __syncwarp();
   tc_fence_before();
@@ -273,8 +282,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   grid_dependents_launch();
   const Abort ab = make_abort(abort_flag, status);
 
-  const int blocks = MODE == kDx ? 2 * P.nk : P.nk;
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  // A tile's products, each into the next of the two accumulators: both of dx's (of a split, this CTA's)
+  constexpr int kProducts = MODE == kDx && !SPLIT ? 2 : 1;
+  const int blocks = P.nk;
+  const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -291,7 +302,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
         const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
         // the boxes are a whole tile's: half a tile uses half of what it loads
-        for (int kb = 0; kb < blocks; ++kb) {
+        for (int i = 0; i < kProducts * blocks; ++i) {
+          const int h = SPLIT ? peer : (kProducts == 2 && i >= blocks), kb = SPLIT ? i : i - h * blocks;
           if (wait_for(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
             const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + P.a_bytes;
             const uint32_t bar = CG == 2 ? peer_addr(full(idx), 0) : full(idx);
@@ -305,8 +317,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
                 load2d<CG>(sb + P.bn * 128, &P.b[1], bar, kb * kBK, w.col, pb);
               }
             } else {
-              const int h = MODE == kDx && kb >= P.nk;
-              const int k0 = (kb - h * P.nk) * kBK;
+              const int k0 = kb * kBK;
               if constexpr (MODE == kDx) {
                 load2d<CG>(st, &P.a[h], bar, k0, row0, pa);
               } else if (P.blocked) {
@@ -349,30 +360,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       int idx = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       for (int u = first; u < P.total; u += step) {
-        bool ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
-        tc_fence_after();
         const int bn = unit_at<MODE, CG>(P, u).bn;
         const uint32_t idesc = idesc_bf16(CG * kBM, MODE == kFwd ? 2 * bn : bn, MODE == kDw, MODE != kFwd);
-        const uint32_t d = tmem + buf * kAccCols;
-        for (int kb = 0; kb < blocks; ++kb) {
-          ok = __all_sync(0xffffffffu, ok && wait_for(full(idx), phase, ab, kSiteFfn + 5));
-          if (ok) {
-            tc_fence_after();
-            const uint32_t off = uint32_t(idx) * stage_bytes;
-            if (elect_one()) {
+        for (int h = 0; h < kProducts; ++h) {
+          bool ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
+          tc_fence_after();
+          const uint32_t d = tmem + buf * kAccCols;
+          for (int kb = 0; kb < blocks; ++kb) {
+            ok = __all_sync(0xffffffffu, ok && wait_for(full(idx), phase, ab, kSiteFfn + 5));
+            if (ok) {
+              tc_fence_after();
+              const uint32_t off = uint32_t(idx) * stage_bytes;
+              if (elect_one()) {
 #pragma unroll
-              for (int j = 0; j < kBK / 16; ++j)
-                mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
-                        (kb | j) ? 1u : 0u);
-              commit<CG>(empty(idx));
-              if (kb + 1 == blocks) commit<CG>(tfull(buf));
+                for (int j = 0; j < kBK / 16; ++j)
+                  mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
+                          (kb | j) ? 1u : 0u);
+                commit<CG>(empty(idx));
+                if (kb + 1 == blocks) commit<CG>(tfull(buf));
+              }
+              __syncwarp();
             }
-            __syncwarp();
+            if (++idx == stages) idx = 0, phase ^= 1u;
           }
-          if (++idx == stages) idx = 0, phase ^= 1u;
+          buf ^= 1;
+          if (!buf) tphase ^= 1u;
         }
-        buf ^= 1;
-        if (!buf) tphase ^= 1u;
       }
       if (elect_one()) commit_here<CG>(drain);
       __syncwarp();
@@ -384,15 +397,104 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     const uint32_t lanes = uint32_t(q * 32) << 16;
     int buf = 0;
     uint32_t tphase = 0;
-    for (int u = first; u < P.total; u += step) {
-      const Unit w = unit_at<MODE, CG>(P, u);
+    // accumulator `buf` is finished / has been read by this warp
+    auto finished = [&]() {
       const bool ok = __all_sync(0xffffffffu, wait_for(tfull(buf), tphase, ab, kSiteFfn + 7));
       tc_fence_after();
+      return ok;
+    };
+    auto leave = [&](bool ok) {
+      tc_fence_before();
+      __syncwarp();
+      if (ok && lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_peer(peer_addr(tempty(buf), 0));
+        else mbar_arrive(tempty(buf));
+      }
+      buf ^= 1;
+      if (!buf) tphase ^= 1u;
+    };
+    for (int u = first; u < P.total; u += step) {
+      const Unit w = unit_at<MODE, CG>(P, u);
       const int64_t row = int64_t(w.tm * CG + rank) * kBM + q * 32 + lane;
+      const int end = min(P.n, w.col + w.bn);      // (bn need not be whole chunks)
+      if constexpr (MODE == kDx) {
+        // The first product's accumulator is read into registers while the second's is being formed, so
+        // the next tile's first product finds its accumulator free.
+        constexpr int kChunks = SPLIT ? 2 : 4;     // of 32 columns, of this warp: up to 128 (256) columns by two
+        float sum[kChunks][32];
+        bool ok = true;
+        if constexpr (SPLIT) {
+          // places of the second CTA's sums: [4 columns][row]
+          const uint32_t at = base + kRingBytes - P.bn * kBM * 4 + (q * 32 + lane) * 16;
+          ok = peer == 1 ? finished() : __all_sync(0xffffffffu, wait_for(sent, 0u, ab, kSiteFfn + 9));
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = 32 * half + 64 * i;
+            if (!ok || c >= w.bn) continue;
+            if (peer == 1) {
+              uint32_t r[32];
+              tmem_ld32(tmem + lanes + c, r);
+              tmem_ld_wait();
+              reg_fence(r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 peer_addr(at + (c / 4 + j) * kBM * 16, 0)),
+                             "r"(r[4 * j]), "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
+                             : "memory");
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(sum[i][4 * j]), "=f"(sum[i][4 * j + 1]), "=f"(sum[i][4 * j + 2]), "=f"(sum[i][4 * j + 3])
+                             : "r"(at + (c / 4 + j) * kBM * 16)
+                             : "memory");
+            }
+          }
+          if (peer == 1) {
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive_peer(peer_addr(sent, 0));
+            leave(ok);
+            continue;
+          }
+        } else {
+          ok = finished();
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = 32 * half + 64 * i;
+            if (!ok || c >= w.bn) continue;
+            uint32_t r[32];
+            tmem_ld32(tmem + buf * kAccCols + lanes + c, r);
+            tmem_ld_wait();
+            reg_fence(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sum[i][e] = __uint_as_float(r[e]);
+          }
+          leave(ok);
+        }
+        ok = finished() && ok;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = 32 * half + 64 * i, col = w.col + c;
+          if (!ok || c >= w.bn || col >= end) continue;
+          uint32_t r[32];
+          tmem_ld32(tmem + buf * kAccCols + lanes + c, r);
+          tmem_ld_wait();
+          reg_fence(r);
+          if (row < P.m) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sum[i][e] = __fadd_rn(sum[i][e], __uint_as_float(r[e]));
+            store_row32(P.out[0] + row * P.n, col, end, sum[i]);
+          }
+        }
+        leave(ok);
+        continue;
+      }
+      const bool ok = finished();
       const uint32_t acc = tmem + buf * kAccCols + lanes;
       if (ok) {
         for (int c = 32 * half; c < w.bn; c += 64) {
-          const int col = w.col + c, end = min(P.n, w.col + w.bn);   // (bn need not be whole chunks)
+          const int col = w.col + c;
           if (col >= end) break;
           uint32_t r0[32];
           tmem_ld32(acc + c, r0);
@@ -442,20 +544,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (ok && lane == 0) {
-        if constexpr (CG == 2) mbar_arrive_peer(peer_addr(tempty(buf), 0));
-        else mbar_arrive(tempty(buf));
-      }
-      buf ^= 1;
-      if (!buf) tphase ^= 1u;
+      leave(ok);
     }
   }
 
   __syncwarp();
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync_all();       // no CTA leaves while its peer may still signal it
+  if constexpr (kCluster == 2) cluster_sync_all();   // no CTA leaves while its peer may still signal it
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
