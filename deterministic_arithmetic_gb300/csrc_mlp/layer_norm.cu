@@ -7,12 +7,20 @@
 // written once. A row group of W warps owns a row, a thread 16 columns of it (8192
 // columns in 16 warps; longer rows take the looped kernels at the end). CTAs stay
 // and take rows in turn. Every thread copies its own 16 elements of the rows to
-// come into its own part of shared memory (cp.async, three or four rows deep) and reads
+// come into its own part of shared memory (cp.async, three rows deep) and reads
 // back only what it copied itself, so the loads of several rows are in flight with
 // no barrier and no registers spent on them; the row's sums take the loop's only
-// barriers. Measured at 8192 x 4096 bf16: loads straight into registers 43 us
-// forward, 65 us backward; rows brought by bulk copies and mbarriers 31 and 49 us
-// (the copying thread's work a row held up its CTA's barriers).
+// barriers. Measured at 8192 x 4096 bf16: 23 us forward, 49 us backward (45 and the
+// partials' sum); loads straight into registers 43 and 65 us; rows brought by bulk
+// copies and mbarriers 31 and 49 us (the copying thread's work a row held up its CTA's
+// barriers).
+//
+// The forward pass runs at the memory's rate (5.8 TB/s), and so does the backward pass on
+// FP32 rows (6.1). On bf16 rows the backward pass is bound by a warp's chain a row: 361
+// instructions for 512 columns, and the sums' shuffles, of which 16 warps on an SM (128
+// registers a thread, 48 of them the weight and the column sums) issue one every second
+// cycle. Twice the warps with 8 columns a thread took 73 us and two rows to a barrier 56:
+// both add instructions to a row.
 //
 // W and each thread's columns follow from N alone, so a row's sums are added in
 // the same order in any batch. The variance is the sum of squares about the mean,
@@ -43,10 +51,11 @@ constexpr int kBlockWarps = 8;                      // warps of a CTA of short r
 // CTAs on an SM leave a thread (5120 columns, bf16: 34.7 us with the 16-warp build, 27.0 with the 12).
 constexpr int kMidWarps = 12;
 constexpr int fwd_ctas(int warps) { return warps == 8 ? 3 : (warps == 12 ? 2 : 1); }
-// Rows a thread has in hand, the current one and those to come: as many as leave two CTAs of 256
-// threads (or one of 512) their shared memory in the backward pass.
-template <bool F32>
-constexpr int stages_of = F32 ? 3 : 4;
+// Rows a thread has in hand, the current one and those to come. Three leave two CTAs of 256 threads (or
+// one of 512) their shared memory in the backward pass on FP32 rows; more did nothing for bf16 rows either
+// (8192 x 4096, forward and backward: 23.0 and 48.8 us with three, 23.5 and 49.0 with four, 24.7 and 50.0
+// with six).
+constexpr int kStages = 3;
 constexpr int kSMs = 152, kMaxParts = 3 * kSMs;     // partial rows of dw and db (parts_of)
 
 inline int warps_per_row(int64_t n) { return int(cdiv(n, 32 * kPerThread)); }
@@ -119,7 +128,7 @@ __device__ __forceinline__ void vec_at(const uint8_t* p, float* o) {
 
 // The rows of one tensor as a thread sees them. Vectors of 4, 8 or 16 bytes pass through the
 // thread's slots in shared memory, kStages rows deep; smaller ones are read when they are needed.
-template <int KIND, int VEC, int kStages>
+template <int KIND, int VEC>
 struct Feed {
   static constexpr int kBytes = kElemBytes<KIND> * VEC, NV = kPerThread / VEC;
   static constexpr bool kAsync = kBytes >= 4;
@@ -166,7 +175,6 @@ struct Feed {
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest kStages - 1 rows' copies of this thread have landed.
-template <int kStages>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory"); }
 
 // The thread's 16 parameters.
@@ -241,7 +249,6 @@ __global__ void __launch_bounds__(32 * WARPS, fwd_ctas(WARPS))
     ln_fwd_kernel(const void* __restrict__ x, const void* __restrict__ weight, const void* __restrict__ bias, int w_type,
                   float eps, uint32_t M, int N, int W, void* __restrict__ y, float* __restrict__ mean_out,
                   float* __restrict__ rstd_out) {
-  constexpr int kStages = stages_of<KIND == kF32>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kSlots];
   clear_slots(&red[0][0], 2 * kSlots);
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(32 * WARPS, fwd_ctas(WARPS))
   __syncthreads();                   // the cleared slots
   grid_dependency_wait();
   grid_dependents_launch();
-  Feed<KIND, VEC, kStages> feed(x, N, row, stride, W, t, smem);
+  Feed<KIND, VEC> feed(x, N, row, stride, W, t, smem);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s, ahead += stride) {
     feed.copy(s, ahead < M, nv);
@@ -271,7 +278,7 @@ __global__ void __launch_bounds__(32 * WARPS, fwd_ctas(WARPS))
   for (int st = 0; row < M; row += stride, out += out_step, st = (st + 1) % kStages, ahead += stride) {
     feed.copy((st + kStages - 1) % kStages, ahead < M, nv);
     copies_commit();
-    copies_wait<kStages>();
+    copies_wait();
     float v[kPerThread];
     Sum4 s, q;
     feed.get(st, nv, v);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kMaxWarps ? 1 : 2)
                   const void* __restrict__ weight, int w_type, const float* __restrict__ mean_in,
                   const float* __restrict__ rstd_in, uint32_t M, int N, int W, void* __restrict__ dx,
                   float* __restrict__ part, int64_t ld, int with_db) {
-  constexpr int NV = kPerThread / VEC, kStages = stages_of<KIND == kF32>;
+  constexpr int NV = kPerThread / VEC;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][2][kSlots];     // [row parity][sum]
   clear_slots(&red[0][0][0], 4 * kSlots);
@@ -332,8 +339,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kMaxWarps ? 1 : 2)
   grid_dependency_wait();
   grid_dependents_launch();
   const int64_t x_ld = row_ld<XK>(N);
-  Feed<KIND, VEC, kStages> feed_dy(dy, N, row, stride, W, t, smem);
-  Feed<XK, VEC, kStages> feed_x(x, x_ld, row, stride, W, t, smem + Feed<KIND, VEC, kStages>::kSlots * blockDim.x);
+  Feed<KIND, VEC> feed_dy(dy, N, row, stride, W, t, smem);
+  Feed<XK, VEC> feed_x(x, x_ld, row, stride, W, t, smem + Feed<KIND, VEC>::kSlots * blockDim.x);
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s, ahead += stride) {
     feed_dy.copy(s, ahead < M, nv);
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kMaxWarps ? 1 : 2)
       for (int i = 0; i < NV; ++i) step[i] = i < nv ? scale_step(next_scale[i]) : 0.f;
     }
     look_ahead(row + stride);
-    copies_wait<kStages>();
+    copies_wait();
     float g[kPerThread], xh[kPerThread];
     Sum4 s1, s2;
     feed_dy.get(st, nv, g);
@@ -636,11 +643,10 @@ cudaError_t set_smem(K* kernel, int bytes) {
 }
 // Shared memory of the slots of a CTA of `threads`, and (backward) of the row groups' column sums.
 template <int KIND, int VEC>
-int fwd_smem(int threads) { return threads * Feed<KIND, VEC, stages_of<KIND == kF32>>::kSlots; }
+int fwd_smem(int threads) { return threads * Feed<KIND, VEC>::kSlots; }
 template <int KIND, int XK, int VEC>
 int bwd_smem(int threads) {
-  constexpr int stages = stages_of<KIND == kF32>;
-  const int slots = threads * (Feed<KIND, VEC, stages>::kSlots + Feed<XK, VEC, stages>::kSlots);
+  const int slots = threads * (Feed<KIND, VEC>::kSlots + Feed<XK, VEC>::kSlots);
   const int sums = (kBlockWarps - 1) * 2 * 32 * kPerThread * 4;       // at most 7 groups of 512 columns
   return slots > sums ? slots : sums;
 }
