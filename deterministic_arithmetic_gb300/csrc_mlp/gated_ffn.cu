@@ -67,8 +67,9 @@ bool kind_ok(int act, int keep) {
          (keep == LORA_KEEP_NONE || keep == LORA_KEEP_BF16 || keep == LORA_KEEP_PACKED8);
 }
 
-// Pairs of CTAs that fit on the device at once (set when the kernels are prepared).
-int g_pairs = 0;
+// Pairs of CTAs that fit on the device at once, and clusters of two and of eight (set when the kernels are
+// prepared).
+int g_pairs = 0, g_splits[2] = {};
 
 // The operands of a product: a [a_rows][a_cols] and b [b_rows][b_cols], two of each (the second may
 // be the first), bf16.
@@ -84,7 +85,7 @@ bool rows_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool bl
   return blocked ? block_map(m, p, rows, cols, kBK, blocks) : tensor_map(m, p, Elem::bf16, rows, cols, cols, 64, kBK, 128);
 }
 
-template <int MODE, int CG, bool SPLIT = false>
+template <int MODE, int CG, int SPLIT = 0>
 lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream_t st) {
   constexpr int products = MODE == kDw ? 2 : 1;
   P.bn = bn;
@@ -102,7 +103,10 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   const int b_bytes = (MODE == kFwd ? 2 : 1) * bn * 128 / CG;
   P.a_bytes = a_rows * kBK * 2;
   P.stage_bytes = P.a_bytes + b_bytes;
-  const int ring = kRingBytes - (SPLIT ? bn * kBM * 4 : 0);        // a split's sums arrive behind it
+  // what a split's CTAs send one another arrives behind the ring: a tile's sums, or 16 rows of every piece
+  const int ring = kRingBytes + (SPLIT == 2   ? kRingSlack - bn * kBM * 4
+                                 : SPLIT == 8 ? kRingSlack - SPLIT * 16 * (bn * 4 + 16)
+                                              : 0);
   P.stages = ring / P.stage_bytes < kMaxStages ? ring / P.stage_bytes : kMaxStages;
   P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, bn));
@@ -114,7 +118,7 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   const bool halves = CG == 2 && 2 * rest <= g_pairs;
   P.whole = int(halves ? total - rest : total);
   P.total = int(halves ? total + rest : total);
-  constexpr int cluster = SPLIT ? 2 : CG;
+  constexpr int cluster = SPLIT ? SPLIT : CG;
   const int most = SPLIT ? P.total : (CG == 2 ? g_pairs : nsm);    // a split's clusters have a tile each
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(cluster * (P.total < most ? P.total : most)));
@@ -127,39 +131,68 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {unsigned(cluster), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = cluster == 2 ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<MODE, CG, SPLIT>, P, status_block()) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
 
+// What a 64-deep block of a lone CTA's tile of w columns takes, and in a split of dx what a cluster takes
+// besides its blocks (starting, filling its ring, joining the sums), in the same unit of about 0.7 ns.
+// Measured: dx's blocks, whose weights are read across their rows, take 0.29 us at 64 columns, 0.35 at
+// 128 and 0.44 at 256, and the forward's 0.19 at 2 x 32.
+template <int MODE>
+int64_t block_cost(int w) {
+  return MODE == kFwd ? 2 * w + 64 : w + (MODE == kDx ? 256 : 64);
+}
+constexpr int kJoinTwo = 4000, kJoinEight = 4000, kJoinRow = 100;    // (a row of a tile sent to all eight)
+
 // Pairs of CTAs where the output has more rows than one CTA's and the 256 x 256 tiles give every
 // pair one. CTAs alone otherwise, in tiles narrow enough to occupy the SMs: the width whose rounds
-// over all SMs cost least, a k-block of a tile taking its columns plus the 64 columns' worth that
-// any tile's fixed part takes.
+// over all SMs cost least. For dx a cluster a tile where that costs less, a CTA a product or eight with
+// a piece each (us a call, alone / two / eight: 1 x 11392 -> 96 110 / 57 / 19; 64 x 17408 -> 5120
+// 146 / 81 / 90; 512 x 8192 -> 2048 78 / 58 / 91; 300 x 11008 -> 4096 100 / 129 / 145).
 template <int MODE>
 lora_status launch(FfnArgs& P, const Operands& o, int nsm, cudaStream_t st) {
   constexpr int most = MODE == kFwd ? 128 : 256;
   // narrower tiles go in steps of whole groups of 32 (packed values kept), 8 columns, or 64-column blocks
   const int step = MODE != kFwd ? 64 : (P.keep_kind == LORA_KEEP_PACKED8 ? 32 : 8), least = MODE == kFwd ? 32 : 64;
-  const int64_t products = MODE == kDw ? 2 : 1;
+  const int64_t products = MODE == kDw ? 2 : 1, rows = cdiv(P.m, kBM);
   if (P.m > kBM && products * cdiv(P.m, 2 * kBM) * cdiv(P.n, most) >= g_pairs)
     return launch_as<MODE, 2>(P, o, most, nsm, st);
-  int bn = most;
+  const int64_t blocks = int64_t(MODE == kDx ? 2 : 1) * P.nk;
+  int bn = most, split = 0;
   int64_t best = INT64_MAX;
   for (int w = most; w >= least; w -= step) {
-    const int64_t cost = cdiv(products * cdiv(P.m, kBM) * cdiv(P.n, w), nsm) * ((MODE == kFwd ? 2 : 1) * w + 64);
+    const int64_t cost = cdiv(products * rows * cdiv(P.n, w), nsm) * blocks * block_cost<MODE>(w);
     if (cost < best) best = cost, bn = w;
   }
   if constexpr (MODE == kDx) {
-    // two CTAs a tile, half the reduction each, where that takes less by the same reckoning
-    int split = 0;
-    best *= 2;
     for (int w = 128; w >= 64; w -= 64) {
-      const int64_t cost = cdiv(2 * cdiv(P.m, kBM) * cdiv(P.n, w), nsm) * (w + 64);
-      if (cost < best) best = cost, split = w;
+      const int64_t tiles = rows * cdiv(P.n, w), block = block_cost<MODE>(w);
+      const int64_t two = cdiv(tiles, g_splits[0]) * (P.nk * block + kJoinTwo);
+      const int64_t eight = cdiv(tiles, g_splits[1]) * (P.piece * block + kJoinEight + kJoinRow * std::min(P.m, kBM));
+      if (two < best) best = two, split = 2, bn = w;
+      if (eight < best) best = eight, split = 8, bn = w;
     }
-    if (split) return launch_as<kDx, 1, true>(P, o, split, nsm, st);
+    if (split == 2) return launch_as<kDx, 1, 2>(P, o, bn, nsm, st);
+    if (split == 8) return launch_as<kDx, 1, 8>(P, o, bn, nsm, st);
   }
   return launch_as<MODE, 1>(P, o, bn, nsm, st);
+}
+
+// How many of the kernel's clusters the device holds at once.
+template <class K>
+cudaError_t resident(int* n, K* kernel, unsigned cluster) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  return e == cudaSuccess && *n < 1 ? cudaErrorInvalidConfiguration : e;
 }
 
 template <int MODE>
@@ -168,27 +201,21 @@ cudaError_t prepare() {
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(ffn_gemm_kernel<MODE, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kGemmSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {2, 1, 1};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, ffn_gemm_kernel<MODE, 2>, &cfg);
-  if (e == cudaSuccess && n < 1) e = cudaErrorInvalidConfiguration;
-  if (e == cudaSuccess) g_pairs = n;
-  return e;
+  return resident(&g_pairs, ffn_gemm_kernel<MODE, 2>, 2);
+}
+
+template <int SPLIT>
+cudaError_t prepare_split(int* clusters) {
+  const auto kernel = ffn_gemm_kernel<kDx, 1, SPLIT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
+  return e == cudaSuccess ? resident(clusters, kernel, SPLIT) : e;
 }
 
 }  // namespace
 
 cudaError_t prepare_ffn() {
-  cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<kDx, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
-  if (e != cudaSuccess) return e;
+  cudaError_t e = prepare_split<2>(&g_splits[0]);
+  if (e != cudaSuccess || (e = prepare_split<8>(&g_splits[1])) != cudaSuccess) return e;
   if ((e = prepare<kFwd>()) != cudaSuccess || (e = prepare<kDx>()) != cudaSuccess) return e;
   return prepare<kDw>();
 }
@@ -262,6 +289,9 @@ lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate
   P.m = int(M);
   P.n = int(K);
   P.nk = int(cdiv(F, kBK));
+  // (a piece shorter than 4 blocks would keep the large tiles' epilogue from hiding under their MMAs)
+  P.piece = std::max(4, int(cdiv(P.nk, kMaxPieces)));
+  P.pieces = int(cdiv(P.nk, P.piece));
   P.out[0] = static_cast<__nv_bfloat16*>(dx);
   if ((s = launch<kDx>(P, Operands{{dgate, dup}, {w_gate, w_up}, M, F, F, K}, nsm, st)) != LORA_OK || !dw) return s;
   FfnArgs Q{};

@@ -19,6 +19,7 @@ struct FfnArgs {
   int keep_kind, act;
   int m, n;                        // rows and columns of the outputs
   int nk;                          // 64-deep blocks of one product's reduction
+  int piece, pieces;               // kDx: a product is taken in `pieces` of `piece` blocks (the last may be shorter)
   int bn;                          // tile columns (in kFwd of each projection)
   int blocked;                     // kDx, kDw: the maps whose rows lie along the reduction are block_map's
   int stages, stage_bytes, a_bytes;   // of the ring; of a stage (all of it copied); of it A's rows

@@ -2,7 +2,7 @@
 // 128-byte-swizzled shared memory, tcgen05 MMAs into FP32 accumulators in TMEM, three products:
 //   kFwd  G = x Wg^T and U = x Wu^T over the same x tile, and in the epilogue h = act(G + Dg) (U + Du),
 //         with G + Dg and U + Du kept in bf16 or in 8 bits when asked for
-//   kDx   dx = dG Wg + dU Wu, an accumulator a product, added at the end
+//   kDx   dx = dG Wg + dU Wu
 //   kDw   dWg = dG^T x and dWu = dU^T x
 //
 // An accumulator takes its whole reduction in order, 16 products at a time, from a cleared start:
@@ -16,9 +16,13 @@
 // issues the MMAs of both; copies of both arrive at its barriers. CG = 1 is a CTA alone with 128
 // rows and bn columns, for batches and outputs too small to give every pair a tile.
 //
-// SPLIT (kDx, CG = 1): the two products of a tile by two CTAs of a cluster at once, for outputs of few
-// tiles, whose time is their reductions' length; the second CTA sends its accumulator to the first's
-// shared memory. The same two sums are added, so the bits are those of one CTA doing both.
+// dx's reductions are the longest (both of F), and its outputs the smallest. So each product is taken in
+// up to four pieces, an accumulator each, and the pieces are added in order: every variant adds the same
+// ones, so the bits are the same. SPLIT (kDx, CG = 1) is a cluster a tile:
+//   2   a product a CTA: the first sends its pieces' sum to the second, which holds its own pieces in four
+//       accumulators and adds them to that
+//   8   a piece a CTA, for outputs of very few tiles: every CTA sends 16 rows of its accumulator to each of
+//       the others, and adds and stores 16 rows itself
 //
 // Persistent CTAs (pairs) take tiles in turn. Warp 0 loads, warp 1 issues the MMAs, warps 2 to 9 read the
 // accumulator and write the tile (a warp its quarter of the lanes, the two halves of the warps
@@ -47,8 +51,9 @@ constexpr int kRingBytes = 192 * 1024;             // the operand ring
 constexpr int kRingSlack = kABytes;
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
-constexpr int kAccCols = 256;                      // TMEM columns of an accumulator
-constexpr size_t kGemmSmem = kRingBytes + kRingSlack + 1024 + (2 * kMaxStages + 7) * 8 + 16;
+constexpr int kMaxPieces = 4;                      // of a product of dx
+constexpr int kMaxAccs = 4;                        // accumulators in the 512 columns of TMEM
+constexpr size_t kGemmSmem = kRingBytes + kRingSlack + 1024 + (2 * kMaxStages + 2 * kMaxAccs + 3) * 8 + 16;
 static_assert(kGemmSmem < 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -251,7 +256,7 @@ __device__ __forceinline__ Unit unit_at(const FfnArgs& P, int u) {
   return w;
 }
 
-template <int MODE, int CG, bool SPLIT = false>
+template <int MODE, int CG, int SPLIT = 0>
 __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs P, uint32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -261,17 +266,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
   auto tfull = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
-  auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
-  const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 4);
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kMaxAccs + b); };
+  const uint32_t drain = bar0 + 8u * (2 * kMaxStages + 2 * kMaxAccs);
   const uint32_t never = drain + 8u;
-  const uint32_t sent = drain + 16u;                 // SPLIT: the second CTA's accumulator has arrived
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 7);
+  const uint32_t sent = drain + 16u;                 // SPLIT: what the other CTAs send has arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 2 * kMaxAccs + 3);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const uint32_t warp = warp_id(), lane = lane_id();
   static_assert(!SPLIT || (MODE == kDx && CG == 1), "a split is dx's");
-  constexpr int kCluster = SPLIT ? 2 : CG;
-  const int peer = kCluster == 2 ? int(cluster_rank()) : 0;
+  static_assert(SPLIT == 0 || SPLIT == 2 || SPLIT == 8, "by product or by piece");
+  constexpr int kCluster = SPLIT ? SPLIT : CG;
+  constexpr int kAccs = SPLIT == 2 ? 4 : 2, kAccCols = 512 / kAccs;   // accumulators of up to 256 (or 128) columns
+  const int peer = kCluster > 1 ? int(cluster_rank()) : 0;
   const int rank = CG == 2 ? peer : 0;                      // of a pair: 0 issues the MMAs
   const int stages = P.stages, stage_bytes = P.stage_bytes;
   if (threadIdx.x == 0) {
@@ -279,13 +286,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(tfull(b), 1);
       mbar_init(tempty(b), CG * kEpiWarps);
     }
     mbar_init(drain, 1);
     mbar_init(never, 1);
-    mbar_init(sent, kEpiWarps);
+    mbar_init(sent, SPLIT == 8 ? 2 * SPLIT : kEpiWarps);
     *abort_flag = 0u;
     mbar_fence_init();
     for (int i = 0; i < 2; ++i) {
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   // known to run (the hardware starts a cluster's CTAs together, but not in the same instant, and an
   // allocation met by no peer does not return). The same meeting shows that the peer's barriers are set up.
   __syncwarp();
-  if constexpr (kCluster == 2) cluster_sync_all();
+  if constexpr (kCluster > 1) cluster_sync_all();
   if (warp == 1) acc_alloc<CG>(smem_u32(tmem_slot));
   __syncwarp();
   tc_fence_before();
@@ -309,9 +316,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   grid_dependents_launch();
   const Abort ab = make_abort(abort_flag, status);
 
-  // A tile's products, each into the next of the two accumulators: both of dx's (of a split, this CTA's)
-  constexpr int kProducts = MODE == kDx && !SPLIT ? 2 : 1;
-  const int blocks = P.nk;
+  // A tile's pieces of this CTA (pair), each into the next accumulator, and their k-blocks. Of a split by
+  // piece it is piece peer & 3 of product peer >> 2 (of fewer than four, the rest have no blocks).
+  const int pieces = MODE != kDx || SPLIT == 8 ? 1 : (SPLIT ? 1 : 2) * P.pieces;
+  const int piece0 = SPLIT == 8 ? (peer & 3) * P.piece : 0;
+  auto blocks_of = [&](int i) {
+    if constexpr (MODE != kDx) return P.nk;
+    const int k0 = SPLIT == 8 ? piece0 : (i >= P.pieces ? i - P.pieces : i) * P.piece;
+    return min(max(P.nk - k0, 0), P.piece);
+  };
+  const int blocks = MODE != kDx ? P.nk : (SPLIT == 8 ? blocks_of(0) : (SPLIT ? 1 : 2) * P.nk);   // of a tile
   const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
 
   if (warp == 0) {
@@ -329,8 +343,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
         const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
         // the boxes are a whole tile's: half a tile uses half of what it loads
-        for (int i = 0; i < kProducts * blocks; ++i) {
-          const int h = SPLIT ? peer : (kProducts == 2 && i >= blocks), kb = SPLIT ? i : i - h * blocks;
+        for (int i = 0; i < blocks; ++i) {
+          const int h = SPLIT == 8 ? peer >> 2 : (SPLIT ? peer : (MODE == kDx && i >= P.nk));
+          const int kb = SPLIT ? piece0 + i : i - h * P.nk;
           if (wait_for(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
             const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + P.a_bytes;
             const uint32_t bar = CG == 2 ? peer_addr(full(idx), 0) : full(idx);
@@ -389,7 +404,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       for (int u = first; u < P.total; u += step) {
         const int bn = unit_at<MODE, CG>(P, u).bn;
         const uint32_t idesc = idesc_bf16(CG * kBM, MODE == kFwd ? 2 * bn : bn, MODE == kDw, MODE != kFwd);
-        for (int h = 0; h < kProducts; ++h) {
+        for (int i = 0; i < pieces; ++i) {
+          const int blocks = blocks_of(i);
+          if (SPLIT == 8 && blocks == 0) break;
           bool ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
           tc_fence_after();
           const uint32_t d = tmem + buf * kAccCols;
@@ -410,8 +427,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
             }
             if (++idx == stages) idx = 0, phase ^= 1u;
           }
-          buf ^= 1;
-          if (!buf) tphase ^= 1u;
+          if (++buf == kAccs) buf = 0, tphase ^= 1u;
         }
       }
       if (elect_one()) commit_here<CG>(drain);
@@ -437,55 +453,85 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         if constexpr (CG == 2) mbar_arrive_peer(peer_addr(tempty(buf), 0));
         else mbar_arrive(tempty(buf));
       }
-      buf ^= 1;
-      if (!buf) tphase ^= 1u;
+      if (++buf == kAccs) buf = 0, tphase ^= 1u;
     };
     for (int u = first; u < P.total; u += step) {
       const Unit w = unit_at<MODE, CG>(P, u);
       const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32, row = row0 + lane;
       const int end = min(P.n, w.col + w.bn);      // (bn need not be whole chunks)
-      if constexpr (MODE == kDx) {
-        // The first product's accumulator is read into registers while the second's is being formed, so
-        // the next tile's first product finds its accumulator free.
-        constexpr int kChunks = SPLIT ? 2 : 4;     // of 32 columns, of this warp: up to 128 (256) columns by two
+      if constexpr (SPLIT == 8) {
+        // Row r of a piece goes to CTA r / 16: [piece][row][column], rows 16 bytes apart from whole banks.
+        const uint32_t pitch = P.bn * 4 + 16, parts = base + kRingBytes + kRingSlack - SPLIT * 16 * pitch;
+        const bool ok = blocks == 0 || finished();
+        for (int c = 32 * half; c < w.bn; c += 64) {
+          uint32_t r[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;          // a piece of no k-blocks
+          if (ok && blocks > 0) {
+            tmem_ld32(tmem + lanes + c, r);
+            tmem_ld_wait();
+            reg_fence(r);
+          }
+          if (ok && row < P.m) {
+            const uint32_t at = peer_addr(parts + (peer * 16 + (lane & 15)) * pitch + c * 4, 2 * q + (lane >> 4));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16 * j), "r"(r[4 * j]),
+                           "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
+                           : "memory");
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (ok && (lane & 15) == 0) mbar_arrive_peer(peer_addr(sent, 2 * q + (lane >> 4)));
+        if (!__all_sync(0xffffffffu, ok && wait_for(sent, 0u, ab, kSiteFfn + 9))) continue;
+        const int col = w.col + 4 * lane;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int i = 2 * (warp - 2) + k;
+          const int64_t r = int64_t(w.tm) * kBM + peer * 16 + i;
+          if (r >= P.m || 4 * int(lane) >= w.bn || col >= end) continue;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int p = 0; p < SPLIT; ++p) {
+            float v[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                         : "r"(parts + (p * 16 + i) * pitch + 16 * lane)
+                         : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = __fadd_rn(sum[e], v[e]);
+          }
+          *reinterpret_cast<uint2*>(P.out[0] + r * P.n + col) =
+              make_uint2(bf16x2_bits(sum[0], sum[1]), bf16x2_bits(sum[2], sum[3]));
+        }
+        continue;
+      } else if constexpr (MODE == kDx) {
+        constexpr int kChunks = SPLIT ? 2 : 4;     // of 32 columns, of this warp: up to 128 (256) by two
         float sum[kChunks][32];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sum[i][e] = 0.f;
         bool ok = true;
-        if constexpr (SPLIT) {
-          // places of the second CTA's sums: [4 columns][row]
-          const uint32_t at = base + kRingBytes - P.bn * kBM * 4 + (q * 32 + lane) * 16;
-          ok = peer == 1 ? finished() : __all_sync(0xffffffffu, wait_for(sent, 0u, ab, kSiteFfn + 9));
+        // the first product's sums in the second CTA: [4 columns][row]
+        const uint32_t sums = base + kRingBytes + kRingSlack - P.bn * kBM * 4 + (q * 32 + lane) * 16;
+        if (SPLIT && peer == 1) {
+          ok = __all_sync(0xffffffffu, wait_for(sent, 0u, ab, kSiteFfn + 9));
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
             const int c = 32 * half + 64 * i;
             if (!ok || c >= w.bn) continue;
-            if (peer == 1) {
-              uint32_t r[32];
-              tmem_ld32(tmem + lanes + c, r);
-              tmem_ld_wait();
-              reg_fence(r);
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 peer_addr(at + (c / 4 + j) * kBM * 16, 0)),
-                             "r"(r[4 * j]), "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
-                             : "memory");
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(sum[i][4 * j]), "=f"(sum[i][4 * j + 1]), "=f"(sum[i][4 * j + 2]), "=f"(sum[i][4 * j + 3])
-                             : "r"(at + (c / 4 + j) * kBM * 16)
-                             : "memory");
-            }
+            for (int j = 0; j < 8; ++j)
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(sum[i][4 * j]), "=f"(sum[i][4 * j + 1]), "=f"(sum[i][4 * j + 2]), "=f"(sum[i][4 * j + 3])
+                           : "r"(sums + (c / 4 + j) * kBM * 16)
+                           : "memory");
           }
-          if (peer == 1) {
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive_peer(peer_addr(sent, 0));
-            leave(ok);
-            continue;
-          }
-        } else {
-          ok = finished();
+        }
+        for (int p = 0; p < pieces; ++p) {
+          ok = finished() && ok;
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
             const int c = 32 * half + 64 * i;
@@ -495,24 +541,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
             tmem_ld_wait();
             reg_fence(r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) sum[i][e] = __uint_as_float(r[e]);
+            for (int e = 0; e < 32; ++e) sum[i][e] = __fadd_rn(sum[i][e], __uint_as_float(r[e]));
           }
           leave(ok);
         }
-        ok = finished() && ok;
+        if (SPLIT && peer == 0) {
+#pragma unroll
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = 32 * half + 64 * i;
+            if (!ok || c >= w.bn) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               peer_addr(sums + (c / 4 + j) * kBM * 16, 1)),
+                           "f"(sum[i][4 * j]), "f"(sum[i][4 * j + 1]), "f"(sum[i][4 * j + 2]), "f"(sum[i][4 * j + 3])
+                           : "memory");
+          }
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive_peer(peer_addr(sent, 1));
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           const int c = 32 * half + 64 * i, col = w.col + c;
-          if (!ok || c >= w.bn || col >= end) continue;
-          uint32_t r[32];
-          tmem_ld32(tmem + buf * kAccCols + lanes + c, r);
-          tmem_ld_wait();
-          reg_fence(r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) sum[i][e] = __fadd_rn(sum[i][e], __uint_as_float(r[e]));
-          store_rows32(P.out[0], row0, P.m, P.n, col, end, sum[i], lane);
+          if (ok && c < w.bn && col < end) store_rows32(P.out[0], row0, P.m, P.n, col, end, sum[i], lane);
         }
-        leave(ok);
         continue;
       }
       const bool ok = finished();
@@ -571,7 +624,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
 
   __syncwarp();
   tc_fence_before();
-  if constexpr (kCluster == 2) cluster_sync_all();   // no CTA leaves while its peer may still signal it
+  if constexpr (kCluster > 1) cluster_sync_all();   // no CTA leaves while its peer may still signal it
   else __syncthreads();
   if (warp == 1) {
     tc_fence_after();

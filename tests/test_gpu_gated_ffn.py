@@ -186,6 +186,24 @@ def test_rows_do_not_depend_on_the_batch(M, K, F):
     assert all(torch.equal(a, b) for a, b in zip(whole + dw, again + dw2))
 
 
+@pytest.mark.parametrize("F", [72, 520, 1032, 4104])
+def test_every_way_of_taking_dx_gives_the_same_bits(F):
+    """Alone, a cluster a tile (by product, by piece of one) and in pairs: a batch of 19300 rows is enough for
+    pairs at 96 columns, and its parts reach the others. Reductions of one to four pieces, short last ones."""
+    from deterministic_arithmetic_gb300 import gated_ffn as ffn
+
+    t = inputs(19300, 96, F)
+    gate, up = t["dg"].bfloat16(), t["du"].bfloat16()
+
+    def dx(lo, hi):
+        return ffn.gated_ffn_bwd(t["dh"][lo:hi], t["x"][lo:hi], t["wg"], t["wu"], gate[lo:hi], up[lo:hi],
+                                 weight_grads=False)[0]
+
+    whole = dx(0, 19300)
+    for lo, hi in ((0, 1), (8, 72), (64, 192), (0, 1300), (128, 5000), (19040, 19300)):
+        assert torch.equal(dx(lo, hi), whole[lo:hi]), (lo, hi)
+
+
 def test_pairs_start_while_the_gpu_is_full():
     """Backward passes back to back: the pairs of CTAs of the product dx start on SMs that are full of the
     element-wise step's CTAs, the two of a pair apart from each other. Each pass gives the same bits."""
@@ -280,3 +298,25 @@ def test_a_wait_that_runs_out_is_reported(kind, site):
         _capi.device_status_reset()
     assert _capi.device_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(ref, step()))
+
+
+@pytest.mark.parametrize("M,K,F", [(300, 520, 1032), (5, 264, 4104)])      # a CTA a product, a CTA a piece
+def test_a_wait_that_runs_out_in_a_cluster_is_reported(M, K, F):
+    """The same where the CTAs of dx's cluster send one another their sums."""
+    from deterministic_arithmetic_gb300 import _capi, gated_ffn as ffn
+
+    t = inputs(M, K, F)
+    _, gate, up = ffn.gated_ffn_fwd(t["x"], t["wg"], t["wu"], save="bf16")
+
+    def dx():
+        return ffn.gated_ffn_bwd(t["dh"], t["x"], t["wg"], t["wu"], gate, up, weight_grads=False)[0]
+
+    ref = dx()
+    try:
+        _capi.device_status_reset(17, 1000)
+        dx()
+        assert _capi.device_status() == (65 << 8) | 1
+    finally:
+        _capi.device_status_reset()
+    assert _capi.device_status() == 0
+    assert torch.equal(ref, dx())

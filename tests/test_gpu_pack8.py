@@ -175,3 +175,22 @@ def test_streams_and_refusals():
         pack8.pack8_da(t["du"], pack8.pack8(t["x"][:, :100].contiguous()))
     with pytest.raises(ld.LoraDeltaError, match="LORA_ERR_WORKSPACE"):
         pack8.pack8_da(t["du"], p, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [200, 1000])
+def test_a_wait_that_runs_out_is_reported(M):
+    """The copying warp of dA's kernel is made to wait for what never comes (1 ms limit): the kernel returns, the
+    status block names the site, and after a reset the next call gives the same bits as before."""
+    from deterministic_arithmetic_gb300 import _capi, pack8
+
+    t = lora(M, 264, 72, 16, M)
+    p = pack8.pack8(t["x"])
+    ref = pack8.pack8_da(t["du"], p)
+    try:
+        _capi.device_status_reset(13, 1000)
+        pack8.pack8_da(t["du"], p)
+        assert _capi.device_status() == (56 << 8) | 1
+    finally:
+        _capi.device_status_reset()
+    assert _capi.device_status() == 0
+    assert torch.equal(ref, pack8.pack8_da(t["du"], p))
