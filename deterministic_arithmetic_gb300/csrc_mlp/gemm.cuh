@@ -5,10 +5,15 @@
 //   kDx   dx = dG Wg + dU Wu
 //   kDw   dWg = dG^T x and dWu = dU^T x
 //
-// An accumulator takes its whole reduction in order, 16 products at a time, from a cleared start:
-// no split over the reduction, so an output's bits do not depend on the tile it falls into, nor on
-// how many rows the batch has. FP32 accumulation; each output is rounded to bf16 once, in the
+// An accumulator takes its reduction in order, 16 products at a time, from a cleared start, and how a
+// reduction is cut depends on its length alone: an output's bits do not depend on the tile it falls into,
+// nor on how many rows the batch has. FP32 accumulation; each output is rounded to bf16 once, in the
 // epilogue.
+//
+// 4096 x 5120 x 17408: 767 us forward (1.90 PFLOP/s), 856 dx, 760 dW on a cool device. Bound by the tensor
+// pipe (77 to 82 % active at 2048 x 4096 x 8192) and, back to back, by the device's power: the clock falls
+// to some 1.6 GHz, and cuBLAS's products take 830 to 860 us each pair. One token (5120 -> 17408): 57 us, the
+// weights' 356 MB at 6.2 TB/s.
 //
 // CG = 2 works in pairs of CTAs (a cluster of two neighbouring SMs, cta_group::2): a 256 x 256 tile,
 // each CTA holding 128 rows of A, half of B's columns and the accumulator of its rows, so that each

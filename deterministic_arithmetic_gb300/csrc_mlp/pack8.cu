@@ -8,7 +8,8 @@
 // most one bit of the seven and cost a second rounding in every consumer.
 //
 // Packing and unpacking are bound by HBM: x once in, 33 / 32 bytes an element
-// out, and back.
+// out, and back. 8192 x 4096 bf16: 17.6 us (5.8 TB/s) and 11.4 us (codes partly
+// from L2).
 #include "../csrc/common.cuh"
 #include "../csrc/kernels.h"
 #include "elems.cuh"

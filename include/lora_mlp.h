@@ -55,8 +55,9 @@ lora_status lora_layer_norm_bwd(const void *dy, int type, const void *x, const v
  * scale 2^(s - 127), s its scale byte, and 32 codes c (signed 8 bits, |c| <= 127), standing
  * for c * 2^(s - 127): s is the smallest for which the group's largest magnitude is at most
  * 127.5 steps (at most 248, so that no value overflows); c is x / step rounded to nearest
- * even, held to +-127. Every value it stands for is a bf16 value exactly, so a consumer that takes bf16 operands loses nothing more. A
- * group that holds a NaN or an infinity has s = 255, and all its values read NaN.
+ * even, held to +-127. Every value it stands for is a bf16 value exactly, so a consumer that takes
+ * bf16 operands loses nothing more. A group that holds a NaN or an infinity has s = 255, and all its
+ * values read NaN.
  *   x       [M][K] bf16 or fp32; K >= 1, any
  *   codes   [M][32 G] int8, scales [M][G] uint8, G = ceil(K / 32)
  */
