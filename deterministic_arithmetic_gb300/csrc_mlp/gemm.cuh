@@ -335,67 +335,75 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      if (stall_requested(status, kKindFfn + MODE)) stall_wait(never, ab, kSiteFfn + 1);   // test hook
-      // x is read again by every column of tiles (kFwd) or every group of row tiles (kDw): it stays
-      // in L2. The rest is shared by the CTAs at work at one time only.
-      const uint64_t keep = policy_evict_last(), once = policy_normal();
-      const uint64_t pa = MODE == kFwd ? keep : once, pb = MODE == kDw ? keep : once;
-      int idx = 0;
-      uint32_t phase = 0, issued = 0, parities = 0;
-      for (int u = first; u < P.total; u += step) {
-        const Unit w = unit_at<MODE, CG>(P, u);
-        const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
-        const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
-        // the boxes are a whole tile's: half a tile uses half of what it loads
-        for (int i = 0; i < blocks; ++i) {
-          const int h = SPLIT == 8 ? peer >> 2 : (SPLIT ? peer : (MODE == kDx && i >= P.nk));
-          const int kb = SPLIT ? piece0 + i : i - h * P.nk;
-          if (wait_for(empty(idx), phase ^ 1u, ab, kSiteFfn + 2)) {
-            const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + P.a_bytes;
-            const uint32_t bar = CG == 2 ? peer_addr(full(idx), 0) : full(idx);
-            if (rank == 0) mbar_expect_tx(full(idx), uint32_t(CG * stage_bytes));
+    // The whole warp runs this loop and the next (their addresses stay in uniform registers), one lane
+    // issues, and a stage's barrier is tested while the stage before it is issued: a k-block's bookkeeping
+    // took as long as 400 cycles, more than a narrow tile's copies and MMAs.
+    const bool one = elect_one();
+    if (stall_requested(status, kKindFfn + MODE) && one) stall_wait(never, ab, kSiteFfn + 1);   // test hook
+    __syncwarp();
+    // x is read again by every column of tiles (kFwd) or every group of row tiles (kDw): it stays
+    // in L2. The rest is shared by the CTAs at work at one time only.
+    const uint64_t keep = policy_evict_last(), once = policy_normal();
+    const uint64_t pa = MODE == kFwd ? keep : once, pb = MODE == kDw ? keep : once;
+    const uint32_t full0 = CG == 2 ? peer_addr(full(0), 0) : full(0);
+    int idx = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ready = true;                               // stage idx is free (at first all are)
+    for (int u = first; u < P.total; u += step) {
+      const Unit w = unit_at<MODE, CG>(P, u);
+      const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
+      const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
+      // the boxes are a whole tile's: half a tile uses half of what it loads
+      const int h0 = SPLIT == 8 ? peer >> 2 : (SPLIT ? peer : 0), h1 = MODE == kDx && !SPLIT ? 2 : h0 + 1;
+      for (int h = h0; h < h1; ++h) {
+        const CUtensorMap* ma = &P.a[MODE == kDw ? w.prod : h];
+        const CUtensorMap* mb = &P.b[MODE == kFwd && CG == 2 ? rank : h];
+        const int last = piece0 + (SPLIT == 8 ? blocks : P.nk);
+        for (int kb = piece0; kb < last; ++kb) {
+          if (!__all_sync(0xffffffffu, ready || wait_longer(empty(idx), phase ^ 1u, ab, kSiteFfn + 2))) goto given_up;
+          const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + P.a_bytes, bar = full0 + 8u * idx, here = full(idx);
+          if (++idx == stages) idx = 0, phase ^= 1u;
+          ready = completed(empty(idx), phase ^ 1u);
+          ++issued;
+          const int k0 = kb * kBK;
+          if (one) {
+            if (rank == 0) mbar_expect_tx(here, uint32_t(CG * stage_bytes));
             if constexpr (MODE == kFwd) {
-              load2d<CG>(st, &P.a[0], bar, kb * kBK, row0, pa);
-              if constexpr (CG == 2) {             // the pair's columns: 128 of the gate, 128 of up
-                load2d<CG>(sb, &P.b[rank], bar, kb * kBK, w.col, pb);
-              } else {
-                load2d<CG>(sb, &P.b[0], bar, kb * kBK, w.col, pb);
-                load2d<CG>(sb + P.bn * 128, &P.b[1], bar, kb * kBK, w.col, pb);
-              }
+              load2d<CG>(st, ma, bar, k0, row0, pa);
+              load2d<CG>(sb, mb, bar, k0, w.col, pb);      // (of a pair, the columns: 128 of the gate, 128 of up)
+              if constexpr (CG == 1) load2d<CG>(sb + P.bn * 128, &P.b[1], bar, k0, w.col, pb);
             } else {
-              const int k0 = kb * kBK;
               if constexpr (MODE == kDx) {
-                load2d<CG>(st, &P.a[h], bar, k0, row0, pa);
+                load2d<CG>(st, ma, bar, k0, row0, pa);
               } else if (P.blocked) {
-                load3d<CG>(st, &P.a[w.prod], bar, k0, row0 / 64, pa);
+                load3d<CG>(st, ma, bar, k0, row0 / 64, pa);
               } else {
-                load2d<CG>(st, &P.a[w.prod], bar, row0, k0, pa);
-                load2d<CG>(st + 8192, &P.a[w.prod], bar, row0 + 64, k0, pa);
+                load2d<CG>(st, ma, bar, row0, k0, pa);
+                load2d<CG>(st + 8192, ma, bar, row0 + 64, k0, pa);
               }
               if (P.blocked)
-                load3d<CG>(sb, &P.b[h], bar, k0, col0 / 64, pb);
+                load3d<CG>(sb, mb, bar, k0, col0 / 64, pb);
               else
-                for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, &P.b[h], bar, col0 + 64 * j, k0, pb);
+                for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, mb, bar, col0 + 64 * j, k0, pb);
             }
-            issued |= 1u << idx;
-            parities = (parities & ~(1u << idx)) | (phase << idx);
           }
-          if (++idx == stages) idx = 0, phase ^= 1u;
+          __syncwarp();
         }
       }
-      // Nothing may reach this CTA's shared memory once it has gone: neither copies (those of both CTAs
-      // report to the first one) nor the MMAs' last arrivals at `empty`, which come from the other CTA's
-      // tensor core and which no later copy waits for. (A CTA of the next launch may take the place at once.)
-      for (int s = 0; s < stages; ++s) {
-        if (!(issued & (1u << s))) continue;
-        if (rank == 0) wait_drain(full(s), (parities >> s) & 1u, ab, kSiteFfn + 3);
-        if (!*ab.flag) wait_for(empty(s), (parities >> s) & 1u, ab, kSiteFfn + 8);
-      }
-      if (*ab.flag)                                // giving up: what is on its way lands long before this
-        for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainLimitNs;) {
-        }
     }
+  given_up:
+    // Nothing may reach this CTA's shared memory once it has gone: neither copies (those of both CTAs
+    // report to the first one) nor the MMAs' last arrivals at `empty`, which come from the other CTA's
+    // tensor core and which no later copy waits for. (A CTA of the next launch may take the place at once.)
+    for (uint32_t s = 0; s < uint32_t(stages) && s < issued; ++s) {
+      const uint32_t parity = ((issued - 1u - s) / stages) & 1u;       // of the stage's last use
+      if (rank == 0) wait_drain(full(s), parity, ab, kSiteFfn + 3);
+      if (!*ab.flag) wait_for(empty(s), parity, ab, kSiteFfn + 8);
+    }
+    if (*ab.flag)                                  // giving up: what is on its way lands long before this
+      for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainLimitNs;) {
+      }
+    __syncwarp();
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
     if (rank == 0) {
@@ -404,38 +412,42 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       constexpr uint32_t a_step = MODE == kDw ? 2048u : 32u, b_step = MODE == kFwd ? 32u : 2048u;
       const uint64_t a0 = smem_desc(base, MODE == kDw ? 8192u : 16u, 1024u, kLayoutSW128);
       const uint64_t b0 = smem_desc(base + P.a_bytes, MODE == kFwd ? 16u : 8192u, 1024u, kLayoutSW128);
+      const bool one = elect_one();
       int idx = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
-      for (int u = first; u < P.total; u += step) {
+      bool ready = false, ok = true;                 // stage idx has landed; no wait has run out
+      for (int u = first; u < P.total && ok; u += step) {
         const int bn = unit_at<MODE, CG>(P, u).bn;
         const uint32_t idesc = idesc_bf16(CG * kBM, MODE == kFwd ? 2 * bn : bn, MODE == kDw, MODE != kFwd);
         for (int i = 0; i < pieces; ++i) {
           const int blocks = blocks_of(i);
           if (SPLIT == 8 && blocks == 0) break;
-          bool ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
+          ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + buf * kAccCols;
           for (int kb = 0; kb < blocks; ++kb) {
-            ok = __all_sync(0xffffffffu, ok && wait_for(full(idx), phase, ab, kSiteFfn + 5));
-            if (ok) {
-              tc_fence_after();
-              const uint32_t off = uint32_t(idx) * stage_bytes;
-              if (elect_one()) {
-#pragma unroll
-                for (int j = 0; j < kBK / 16; ++j)
-                  mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
-                          (kb | j) ? 1u : 0u);
-                commit<CG>(empty(idx));
-                if (kb + 1 == blocks) commit<CG>(tfull(buf));
-              }
-              __syncwarp();
-            }
+            ok = __all_sync(0xffffffffu, ready || wait_for(full(idx), phase, ab, kSiteFfn + 5));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t off = uint32_t(idx) * stage_bytes, used = empty(idx);
             if (++idx == stages) idx = 0, phase ^= 1u;
+            ready = completed(full(idx), phase);
+            if (one) {
+#pragma unroll
+              for (int j = 0; j < kBK / 16; ++j)
+                mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
+                        (kb | j) ? 1u : 0u);
+              commit<CG>(used);
+              if (kb + 1 == blocks) commit<CG>(tfull(buf));
+            }
+            __syncwarp();
           }
+          if (!ok) break;
           if (++buf == kAccs) buf = 0, tphase ^= 1u;
         }
       }
-      if (elect_one()) commit_here<CG>(drain);
+      if (one) commit_here<CG>(drain);
       __syncwarp();
       wait_drain(drain, 0u, ab, kSiteFfn + 6);
     }
