@@ -102,12 +102,14 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   }
   const int b_bytes = (MODE == kFwd ? 2 : 1) * bn * 128 / CG;
   P.a_bytes = a_rows * kBK * 2;
-  P.stage_bytes = P.a_bytes + b_bytes;
+  P.block_bytes = P.a_bytes + b_bytes;
   // what a split's CTAs send one another arrives behind the ring: a tile's sums, or 16 rows of every piece
   const int ring = kRingBytes + (SPLIT == 2   ? kRingSlack - bn * kBM * 4
                                  : SPLIT == 8 ? kRingSlack - SPLIT * 16 * (bn * 4 + 16)
                                               : 0);
-  P.stages = ring / P.stage_bytes < kMaxStages ? ring / P.stage_bytes : kMaxStages;
+  constexpr bool narrow = CG == 1 && (MODE == kFwd || SPLIT);      // tiles whose blocks may be few bytes
+  const int deep = !narrow ? 1 : (ring >= 16 * P.block_bytes ? 4 : (ring >= 8 * P.block_bytes ? 2 : 1));
+  P.stages = std::min(kMaxStages, ring / (deep * P.block_bytes));
   P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, bn));
   const int64_t total = int64_t(products) * P.tiles_m * P.tiles_n;
@@ -132,7 +134,12 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   attr[1].val.clusterDim = {unsigned(cluster), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<MODE, CG, SPLIT>, P, status_block()) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+  auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, P, status_block()) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA; };
+  if constexpr (narrow) {
+    if (deep == 4) return go(ffn_gemm_kernel<MODE, CG, SPLIT, 4>);
+    if (deep == 2) return go(ffn_gemm_kernel<MODE, CG, SPLIT, 2>);
+  }
+  return go(ffn_gemm_kernel<MODE, CG, SPLIT>);
 }
 
 // What a 64-deep block of a lone CTA's tile of w columns takes, and in a split of dx what a cluster takes
@@ -195,20 +202,27 @@ cudaError_t resident(int* n, K* kernel, unsigned cluster) {
   return e == cudaSuccess && *n < 1 ? cudaErrorInvalidConfiguration : e;
 }
 
+template <int MODE, int CG, int SPLIT, int... DEEP>
+cudaError_t set_smem() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel) {
+    return (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem))) == cudaSuccess;
+  };
+  (void)(set(ffn_gemm_kernel<MODE, CG, SPLIT, DEEP>) && ...);
+  return e;
+}
+
 template <int MODE>
 cudaError_t prepare() {
-  cudaError_t e = cudaFuncSetAttribute(ffn_gemm_kernel<MODE, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(ffn_gemm_kernel<MODE, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
-  if (e != cudaSuccess) return e;
+  cudaError_t e = MODE == kFwd ? set_smem<kFwd, 1, 0, 1, 2, 4>() : set_smem<MODE, 1, 0, 1>();
+  if (e != cudaSuccess || (e = set_smem<MODE, 2, 0, 1>()) != cudaSuccess) return e;
   return resident(&g_pairs, ffn_gemm_kernel<MODE, 2>, 2);
 }
 
 template <int SPLIT>
 cudaError_t prepare_split(int* clusters) {
-  const auto kernel = ffn_gemm_kernel<kDx, 1, SPLIT>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGemmSmem));
-  return e == cudaSuccess ? resident(clusters, kernel, SPLIT) : e;
+  const cudaError_t e = set_smem<kDx, 1, SPLIT, 1, 2, 4>();
+  return e == cudaSuccess ? resident(clusters, ffn_gemm_kernel<kDx, 1, SPLIT>, SPLIT) : e;
 }
 
 }  // namespace

@@ -22,7 +22,8 @@ struct FfnArgs {
   int piece, pieces;               // kDx: a product is taken in `pieces` of `piece` blocks (the last may be shorter)
   int bn;                          // tile columns (in kFwd of each projection)
   int blocked;                     // kDx, kDw: the maps whose rows lie along the reduction are block_map's
-  int stages, stage_bytes, a_bytes;   // of the ring; of a stage (all of it copied); of it A's rows
+  int stages;                      // of the ring
+  int block_bytes, a_bytes;        // of a k-block (all of it copied); of it A's rows
   int tiles_m, tiles_n;            // tiles of one product
   int whole, total;                // units of work: `whole` tiles, then halves of the remaining ones
 };

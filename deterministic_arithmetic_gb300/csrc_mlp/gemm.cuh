@@ -261,7 +261,7 @@ __device__ __forceinline__ Unit unit_at(const FfnArgs& P, int u) {
   return w;
 }
 
-template <int MODE, int CG, int SPLIT = 0>
+template <int MODE, int CG, int SPLIT = 0, int DEEP = 1>
 __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs P, uint32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
   constexpr int kAccs = SPLIT == 2 ? 4 : 2, kAccCols = 512 / kAccs;   // accumulators of up to 256 (or 128) columns
   const int peer = kCluster > 1 ? int(cluster_rank()) : 0;
   const int rank = CG == 2 ? peer : 0;                      // of a pair: 0 issues the MMAs
-  const int stages = P.stages, stage_bytes = P.stage_bytes;
+  const int stages = P.stages, stage_bytes = DEEP * P.block_bytes;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(full(s), 1);
@@ -330,14 +330,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     const int k0 = SPLIT == 8 ? piece0 : (i >= P.pieces ? i - P.pieces : i) * P.piece;
     return min(max(P.nk - k0, 0), P.piece);
   };
-  const int blocks = MODE != kDx ? P.nk : (SPLIT == 8 ? blocks_of(0) : (SPLIT ? 1 : 2) * P.nk);   // of a tile
+  const bool empty_piece = SPLIT == 8 && blocks_of(0) == 0;
   const int first = blockIdx.x / kCluster, step = gridDim.x / kCluster;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     // The whole warp runs this loop and the next (their addresses stay in uniform registers), one lane
-    // issues, and a stage's barrier is tested while the stage before it is issued: a k-block's bookkeeping
-    // took as long as 400 cycles, more than a narrow tile's copies and MMAs.
+    // issues, and a stage's barrier is tested before the stage in front of it is issued. Its bookkeeping
+    // (and the issuer's: tests, commit) takes some 400 cycles, more than the copies and MMAs of a narrow
+    // tile's k-block: so a stage holds DEEP of them, up to four where the ring has room for four such stages.
     const bool one = elect_one();
     if (stall_requested(status, kKindFfn + MODE) && one) stall_wait(never, ab, kSiteFfn + 1);   // test hook
     __syncwarp();
@@ -354,37 +355,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
       const int col0 = w.col + rank * (w.bn / 2);          // kDx, kDw: its columns of B
       // the boxes are a whole tile's: half a tile uses half of what it loads
-      const int h0 = SPLIT == 8 ? peer >> 2 : (SPLIT ? peer : 0), h1 = MODE == kDx && !SPLIT ? 2 : h0 + 1;
-      for (int h = h0; h < h1; ++h) {
+      for (int i = 0; i < pieces; ++i) {
+        const bool second = MODE == kDx && !SPLIT && i >= P.pieces;
+        const int h = SPLIT == 8 ? peer >> 2 : (SPLIT ? peer : int(second));       // dx: the product
         const CUtensorMap* ma = &P.a[MODE == kDw ? w.prod : h];
         const CUtensorMap* mb = &P.b[MODE == kFwd && CG == 2 ? rank : h];
-        const int last = piece0 + (SPLIT == 8 ? blocks : P.nk);
-        for (int kb = piece0; kb < last; ++kb) {
+        const int begin = piece0 + (MODE == kDx ? (i - (second ? P.pieces : 0)) * P.piece : 0), end = begin + blocks_of(i);
+        for (int kb = begin; kb < end; kb += DEEP) {
           if (!__all_sync(0xffffffffu, ready || wait_longer(empty(idx), phase ^ 1u, ab, kSiteFfn + 2))) goto given_up;
-          const uint32_t st = base + uint32_t(idx) * stage_bytes, sb = st + P.a_bytes, bar = full0 + 8u * idx, here = full(idx);
+          const uint32_t st0 = base + uint32_t(idx) * stage_bytes, bar = full0 + 8u * idx, here = full(idx);
           if (++idx == stages) idx = 0, phase ^= 1u;
           ready = completed(empty(idx), phase ^ 1u);
           ++issued;
-          const int k0 = kb * kBK;
           if (one) {
-            if (rank == 0) mbar_expect_tx(here, uint32_t(CG * stage_bytes));
-            if constexpr (MODE == kFwd) {
-              load2d<CG>(st, ma, bar, k0, row0, pa);
-              load2d<CG>(sb, mb, bar, k0, w.col, pb);      // (of a pair, the columns: 128 of the gate, 128 of up)
-              if constexpr (CG == 1) load2d<CG>(sb + P.bn * 128, &P.b[1], bar, k0, w.col, pb);
-            } else {
-              if constexpr (MODE == kDx) {
+            if (rank == 0) mbar_expect_tx(here, uint32_t(CG * (DEEP == 1 ? 1 : min(DEEP, end - kb)) * P.block_bytes));
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) {
+              if (k > 0 && kb + k >= end) break;
+              const uint32_t st = st0 + k * P.block_bytes, sb = st + P.a_bytes;
+              const int k0 = (kb + k) * kBK;
+              if constexpr (MODE == kFwd) {
                 load2d<CG>(st, ma, bar, k0, row0, pa);
-              } else if (P.blocked) {
-                load3d<CG>(st, ma, bar, k0, row0 / 64, pa);
+                load2d<CG>(sb, mb, bar, k0, w.col, pb);    // (of a pair, the columns: 128 of the gate, 128 of up)
+                if constexpr (CG == 1) load2d<CG>(sb + P.bn * 128, &P.b[1], bar, k0, w.col, pb);
               } else {
-                load2d<CG>(st, ma, bar, row0, k0, pa);
-                load2d<CG>(st + 8192, ma, bar, row0 + 64, k0, pa);
+                if constexpr (MODE == kDx) {
+                  load2d<CG>(st, ma, bar, k0, row0, pa);
+                } else if (P.blocked) {
+                  load3d<CG>(st, ma, bar, k0, row0 / 64, pa);
+                } else {
+                  load2d<CG>(st, ma, bar, row0, k0, pa);
+                  load2d<CG>(st + 8192, ma, bar, row0 + 64, k0, pa);
+                }
+                if (P.blocked)
+                  load3d<CG>(sb, mb, bar, k0, col0 / 64, pb);
+                else
+                  for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, mb, bar, col0 + 64 * j, k0, pb);
               }
-              if (P.blocked)
-                load3d<CG>(sb, mb, bar, k0, col0 / 64, pb);
-              else
-                for (int j = 0; j < P.bn / CG / 64; ++j) load2d<CG>(sb + j * 8192, mb, bar, col0 + 64 * j, k0, pb);
             }
           }
           __syncwarp();
@@ -421,25 +428,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
         const uint32_t idesc = idesc_bf16(CG * kBM, MODE == kFwd ? 2 * bn : bn, MODE == kDw, MODE != kFwd);
         for (int i = 0; i < pieces; ++i) {
           const int blocks = blocks_of(i);
-          if (SPLIT == 8 && blocks == 0) break;
+          if (empty_piece) break;
           ok = __all_sync(0xffffffffu, wait_for(tempty(buf), tphase ^ 1u, ab, kSiteFfn + 4));
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + buf * kAccCols;
-          for (int kb = 0; kb < blocks; ++kb) {
+          for (int kb = 0; kb < blocks; kb += DEEP) {
             ok = __all_sync(0xffffffffu, ready || wait_for(full(idx), phase, ab, kSiteFfn + 5));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t off = uint32_t(idx) * stage_bytes, used = empty(idx);
+            const uint32_t off0 = uint32_t(idx) * stage_bytes, used = empty(idx);
             if (++idx == stages) idx = 0, phase ^= 1u;
             ready = completed(full(idx), phase);
             if (one) {
 #pragma unroll
-              for (int j = 0; j < kBK / 16; ++j)
-                mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
-                        (kb | j) ? 1u : 0u);
+              for (int k = 0; k < DEEP; ++k) {
+                if (k > 0 && kb + k >= blocks) break;
+                const uint32_t off = off0 + k * P.block_bytes;
+#pragma unroll
+                for (int j = 0; j < kBK / 16; ++j)
+                  mma<CG>(d, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc,
+                          (kb | k | j) ? 1u : 0u);
+              }
               commit<CG>(used);
-              if (kb + 1 == blocks) commit<CG>(tfull(buf));
+              if (kb + DEEP >= blocks) commit<CG>(tfull(buf));
             }
             __syncwarp();
           }
@@ -479,12 +491,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       if constexpr (SPLIT == 8) {
         // Row r of a piece goes to CTA r / 16: [piece][row][column], rows 16 bytes apart from whole banks.
         const uint32_t pitch = P.bn * 4 + 16, parts = base + kRingBytes + kRingSlack - SPLIT * 16 * pitch;
-        const bool ok = blocks == 0 || finished();
+        const bool ok = empty_piece || finished();
         for (int c = 32 * half; c < w.bn; c += 64) {
           uint32_t r[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) r[e] = 0u;          // a piece of no k-blocks
-          if (ok && blocks > 0) {
+          if (ok && !empty_piece) {
             tmem_ld32(tmem + lanes + c, r);
             tmem_ld_wait();
             reg_fence(r);
