@@ -143,20 +143,20 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
 }
 
 // What a 64-deep block of a lone CTA's tile of w columns takes, and in a split of dx what a cluster takes
-// besides its blocks (starting, filling its ring, joining the sums), in the same unit of about 0.7 ns.
-// Measured: dx's blocks, whose weights are read across their rows, take 0.29 us at 64 columns, 0.35 at
-// 128 and 0.44 at 256, and the forward's 0.19 at 2 x 32.
+// besides its blocks (starting, filling its ring, joining the sums), in units of 0.5 to 0.8 ns, by the rows.
+// Fitted to the times of 27 shapes of dx from 1 x 96 to 2048 x 8192, taken in each way: the way and width
+// of least cost are the fastest there, or within 2 % of it.
 template <int MODE>
 int64_t block_cost(int w) {
   return MODE == kFwd ? 2 * w + 64 : w + (MODE == kDx ? 256 : 64);
 }
-constexpr int kJoinTwo = 4000, kJoinEight = 4000, kJoinRow = 100;    // (a row of a tile sent to all eight)
+constexpr int kJoinTwo = 4000, kJoinEight = 10000, kJoinRow = 50;    // (a row of a tile, sent by all eight)
 
 // Pairs of CTAs where the output has more rows than one CTA's and the 256 x 256 tiles give every
 // pair one. CTAs alone otherwise, in tiles narrow enough to occupy the SMs: the width whose rounds
 // over all SMs cost least. For dx a cluster a tile where that costs less, a CTA a product or eight with
-// a piece each (us a call, alone / two / eight: 1 x 11392 -> 96 110 / 57 / 19; 64 x 17408 -> 5120
-// 146 / 81 / 90; 512 x 8192 -> 2048 78 / 58 / 91; 300 x 11008 -> 4096 100 / 129 / 145).
+// a piece each (us a call, alone / two / eight: 1 x 11392 -> 96 78 / 31 / 12; 64 x 17408 -> 5120
+// 116 / 83 / 91; 512 x 8192 -> 2048 67 / 60 / 93; 300 x 11008 -> 4096 98 / 133 / 148).
 template <int MODE>
 lora_status launch(FfnArgs& P, const Operands& o, int nsm, cudaStream_t st) {
   constexpr int most = MODE == kFwd ? 128 : 256;
