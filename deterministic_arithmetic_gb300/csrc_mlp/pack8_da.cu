@@ -49,9 +49,10 @@ struct DaCfg {
   static constexpr int kSteps = kWgradChunk / kRows;            // stages of a chunk; a team and a place for each
   static constexpr int kCPT = RP / 2;                           // accumulator columns of an epilogue thread
   static constexpr int kCH = kCPT < 16 ? kCPT : 16;             // of them, at a time
-  static constexpr int kBars = 2 * kRaw + 2 * kWide + 2 * kAcc + 2;
+  static constexpr int kBars = 2 * kRaw + kWide + kAcc + 2;
   static constexpr size_t kSmem = size_t(kWide) * kWideBytes + size_t(kRaw) * kRawBytes + 1024 + kBars * 8 + 16;
   static_assert(kSteps == 4 && kWide == kSteps && kTeam * 32 == kRows && kRawBytes % 1024 == 0 && kSmem < 227 * 1024, "layout");
+  static_assert(kAcc <= kRaw && kWide <= kRaw, "a stage's barrier is met by all before its next use");
 };
 
 // 4 codes of a group with step 2^(s - 127), 1 <= s <= 246, as 4 bf16 values. With b the code's byte,
@@ -87,20 +88,20 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
   uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + raw_off + C::kRaw * C::kRawBytes);
   const uint32_t bar0 = smem_u32(bars);
   auto rfull = [&](int s) { return bar0 + 8u * s; };                                   // codes and du landed
-  auto rempty = [&](int s) { return bar0 + 8u * (C::kRaw + s); };
+  // A stage's MMAs are done: its places may be filled again and its leaves read. One barrier tells all
+  // three (a commit each took the issuing warp longer than the MMAs).
+  auto done = [&](int s) { return bar0 + 8u * (C::kRaw + s); };
   auto wfull = [&](int s) { return bar0 + 8u * (2 * C::kRaw + s); };                   // expanded
-  auto wempty = [&](int s) { return bar0 + 8u * (2 * C::kRaw + C::kWide + s); };
-  auto tfull = [&](int g) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kWide + g); };    // leaves done
-  auto tempty = [&](int g) { return bar0 + 8u * (2 * C::kRaw + 2 * C::kWide + C::kAcc + g); };
+  auto tempty = [&](int g) { return bar0 + 8u * (2 * C::kRaw + C::kWide + g); };       // leaves read
   const uint32_t drain = bar0 + 8u * (C::kBars - 2), never = drain + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kBars);
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   const uint32_t warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kRaw; ++s) mbar_init(rfull(s), 1), mbar_init(rempty(s), 1);
-    for (int s = 0; s < C::kWide; ++s) mbar_init(wfull(s), C::kTeam), mbar_init(wempty(s), 1);
-    for (int g = 0; g < C::kAcc; ++g) mbar_init(tfull(g), 1), mbar_init(tempty(g), C::kEpi);
+    for (int s = 0; s < C::kRaw; ++s) mbar_init(rfull(s), 1), mbar_init(done(s), 1);
+    for (int s = 0; s < C::kWide; ++s) mbar_init(wfull(s), C::kTeam);
+    for (int g = 0; g < C::kAcc; ++g) mbar_init(tempty(g), C::kEpi);
     mbar_init(drain, 1);
     mbar_init(never, 1);
     *abort_flag = 0u;
@@ -125,29 +126,34 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
 
   if (warp == 0) {
     // -------------------------------------------------------------- copies
-    if (lane == 0) {
-      if (stall_requested(status, kKindDa)) stall_wait(never, ab, kSiteDa);   // test hook: a wait that runs out
-      const uint64_t once = policy_evict_first(), keep = policy_evict_last();
-      Ring r;
-      uint32_t issued = 0, parities = 0;
-      for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
-        const int ct = u % P.n_ct, ch = u / P.n_ct, n = steps_of(ch);
-        for (int i = 0; i < n; ++i) {
-          if (wait_for(rempty(r.idx), r.phase ^ 1u, ab, kSiteDa + 1)) {
-            const uint32_t st = base + raw_off + r.idx * C::kRawBytes;
-            const int m = ch * kWgradChunk + i * C::kRows;
-            mbar_expect_tx(rfull(r.idx), C::kRawBytes);
-            tma_load(st, &P.codes, rfull(r.idx), ct * C::kCols, m, once);
-            tma_load(st + C::kCodeBytes, &P.du, rfull(r.idx), 0, m, keep);
-            issued |= 1u << r.idx;
-            parities = (parities & ~(1u << r.idx)) | (r.phase << r.idx);
-          }
-          r.next<C::kRaw>();
+    // (the whole warp, one lane issuing: the addresses stay in uniform registers)
+    const bool one = elect_one();
+    if (stall_requested(status, kKindDa) && one) stall_wait(never, ab, kSiteDa);   // test hook: a wait that runs out
+    __syncwarp();
+    const uint64_t once = policy_evict_first(), keep = policy_evict_last();
+    Ring r;
+    uint32_t issued = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < P.total && ok; u += gridDim.x) {
+      const int ct = u % P.n_ct, ch = u / P.n_ct, n = steps_of(ch);
+      for (int i = 0; i < n; ++i) {
+        ok = __all_sync(0xffffffffu, wait_for(done(r.idx), r.phase ^ 1u, ab, kSiteDa + 1));
+        if (!ok) break;
+        const uint32_t st = base + raw_off + r.idx * C::kRawBytes, bar = rfull(r.idx);
+        const int m = ch * kWgradChunk + i * C::kRows;
+        if (one) {
+          mbar_expect_tx(bar, C::kRawBytes);
+          tma_load(st, &P.codes, bar, ct * C::kCols, m, once);
+          tma_load(st + C::kCodeBytes, &P.du, bar, 0, m, keep);
         }
+        __syncwarp();
+        ++issued;
+        r.next<C::kRaw>();
       }
-      for (int s = 0; s < C::kRaw; ++s)
-        if (issued & (1u << s)) wait_drain(rfull(s), (parities >> s) & 1u, ab, kSiteDa + 2);
     }
+    for (uint32_t s = 0; s < C::kRaw && s < issued; ++s)
+      wait_drain(rfull(s), ((issued - 1u - s) / C::kRaw) & 1u, ab, kSiteDa + 2);
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc = idesc_bf16(128, RP, 1, 1);
@@ -175,9 +181,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
             for (int j = 0; j < C::kLeaves; ++j)
               mma_bf16(d + j * RP, desc_advance(xdesc[j], i * C::kWideBytes), desc_advance(gdesc[j], r.idx * C::kRawBytes),
                        idesc, 0u);
-            mma_commit(wempty(i));
-            mma_commit(rempty(r.idx));
-            mma_commit(tfull(g.idx));
+            mma_commit(done(r.idx));
           }
           __syncwarp();
         }
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
     // ---------------------------------------------------- leaves to partials
     const int q = warp & 3, h = (warp - 2) >> 2;        // a quarter of the columns of x, a half of the rank
     const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + h * C::kCPT;
-    Ring g;
+    Ring r, g;
     for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
       const int ct = u % P.n_ct, ch = u / P.n_ct, n = steps_of(ch);
       float sum[C::kCPT], left[2][C::kCPT];
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
 #pragma unroll
       for (int i = 0; i < C::kSteps; ++i) {
         if (i < n) {
-          const bool ok = __all_sync(0xffffffffu, wait_for(tfull(g.idx), g.phase, ab, kSiteDa + 6));
+          const bool ok = __all_sync(0xffffffffu, wait_for(done(r.idx), r.phase, ab, kSiteDa + 6));
           all = all && ok;
           tc_fence_after();
 #pragma unroll
@@ -226,6 +230,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
           tc_fence_before();
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(tempty(g.idx));
+          r.next<C::kRaw>();
           g.next<C::kAcc>();
         } else {
 #pragma unroll
@@ -268,7 +273,7 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
       for (int k = 0; k < 4; ++k)
         s[k] = u < P.total && m < P.M && grp + k < P.G ? uint32_t(__ldg(P.scales + size_t(m) * P.G + grp + k)) : 127u;
     };
-    uint32_t stage = 0, wphase = 1u;                    // stages of this CTA so far
+    uint32_t stage = 0, before = ~0u;                   // stages of this CTA so far; the last one in this place
     uint32_t next[4];
     scales_of(blockIdx.x, next);
     for (int u = blockIdx.x; u < P.total; u += gridDim.x) {
@@ -281,9 +286,9 @@ __global__ void __launch_bounds__(DaCfg<RP>::kThreads, 1) pack8_da_kernel(const 
       scales_of(u + gridDim.x, next);                   // the next unit's, loaded under this one's work
       if (team >= n) continue;
       bool ok = wait_for(rfull(mine % C::kRaw), (mine / C::kRaw) & 1u, ab, kSiteDa + 7);
-      ok = ok && wait_for(wempty(team), wphase, ab, kSiteDa + 8);
+      ok = ok && (before == ~0u || wait_for(done(before % C::kRaw), (before / C::kRaw) & 1u, ab, kSiteDa + 8));
       ok = __all_sync(0xffffffffu, ok);
-      wphase ^= 1u;
+      before = mine;
       if (ok) {
         const uint8_t* in = gbase + raw_off + mine % C::kRaw * C::kRawBytes + row * 128;
 #pragma unroll
