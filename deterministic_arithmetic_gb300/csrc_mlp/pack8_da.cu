@@ -48,7 +48,6 @@ struct DaCfg {
   static constexpr int kEpi = 8, kTeam = 2, kXf = kTeam * kWide, kThreads = 32 * (2 + kEpi + kXf);
   static constexpr int kSteps = kWgradChunk / kRows;            // stages of a chunk; a team and a place for each
   static constexpr int kCPT = RP / 2;                           // accumulator columns of an epilogue thread
-  static constexpr int kCH = kCPT < 16 ? kCPT : 16;             // of them, at a time
   static constexpr int kBars = 2 * kRaw + kWide + kAcc + 2;
   static constexpr size_t kSmem = size_t(kWide) * kWideBytes + size_t(kRaw) * kRawBytes + 1024 + kBars * 8 + 16;
   static_assert(kSteps == 4 && kWide == kSteps && kTeam * 32 == kRows && kRawBytes % 1024 == 0 && kSmem < 227 * 1024, "layout");
