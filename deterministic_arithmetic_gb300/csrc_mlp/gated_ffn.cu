@@ -98,7 +98,8 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
                                : tensor_map(&P.a[i], o.a[i], Elem::bf16, o.a_rows, o.a_cols, o.a_cols, kBK, a_rows, 128);
     const bool b = MODE == kFwd ? tensor_map(&P.b[i], o.b[i], Elem::bf16, o.b_rows, o.b_cols, o.b_cols, kBK, bn, 128)
                                 : rows_map(&P.b[i], o.b[i], o.b_rows, o.b_cols, P.blocked, bn / CG / 64);
-    if (!a || !b) return LORA_ERR_CUDA;
+    const bool out = MODE != kDw || tensor_map(&P.o[i], P.out[i], Elem::bf16, P.m, P.n, P.n, 32, 32, 64);
+    if (!a || !b || !out) return LORA_ERR_CUDA;
   }
   const int b_bytes = (MODE == kFwd ? 2 : 1) * bn * 128 / CG;
   P.a_bytes = a_rows * kBK * 2;

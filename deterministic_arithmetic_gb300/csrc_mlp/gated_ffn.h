@@ -12,6 +12,7 @@ constexpr uint32_t kKindFfn = 16, kSiteFfn = 64;   // status block: kind kKindFf
 
 struct FfnArgs {
   CUtensorMap a[2], b[2];          // kFwd: x | Wg, Wu.  kDx: dG, dU | Wg, Wu.  kDw: dG, dU | x
+  CUtensorMap o[2];                // kDw: of the outputs, boxes 32 rows x 32 columns
   __nv_bfloat16* out[2];           // [m][n]: h | dx | dWg, dWu
   const float* delta[2];           // kFwd: Dg, Du [m][n], or null
   void* keep[2];                   // kFwd: G and U, kept as keep_kind says

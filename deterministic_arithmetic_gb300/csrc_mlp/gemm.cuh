@@ -53,8 +53,11 @@ constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 192 * 1024;             // the operand ring
 // Behind it: a stage of a small batch holds fewer than 128 rows of A, and the MMAs' reads of the other
 // rows (whose products nobody reads) run on into what follows, in the last stage to here.
-constexpr int kRingSlack = kABytes;
+// The same place holds the boxes that dW's epilogue writes out (two of 2 KB a warp), and ends with what a
+// split's CTAs send one another.
 constexpr int kEpiWarps = 8;
+constexpr int kBoxBytes = 32 * 32 * 2, kRingSlack = kEpiWarps * 2 * kBoxBytes;
+static_assert(kRingSlack >= kABytes, "the reads past a short A stay inside");
 constexpr int kGemmThreads = 32 * (2 + kEpiWarps);
 constexpr int kMaxPieces = 4;                      // of a product of dx
 constexpr int kMaxAccs = 4;                        // accumulators in the 512 columns of TMEM
@@ -176,7 +179,7 @@ __device__ __forceinline__ float act_slope(int act, float y, float p) {
 // 32 rows by 32 columns of the warp, as bf16: lane l holds row row0 + l's columns from `col` on. Rows at or
 // past m and columns at or past n (a multiple of 8) are left alone. Lanes of a quad first trade 8-column
 // pieces, so that a store writes 64 bytes of each of 8 rows: 16 bytes of each of 32 rows took four times
-// the accesses (weight gradients of one token 5120 x 17408: 208 -> 109 us).
+// the accesses (dW of one token 5120 x 17408, which went this way then: 208 -> 109 us).
 __device__ __forceinline__ void store_rows32(__nv_bfloat16* out, int64_t row0, int64_t m, int64_t ld, int col, int n,
                                              const float (&v)[32], uint32_t lane) {
   uint32_t p[4][4];                                // [piece][word]
@@ -468,7 +471,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = uint32_t(q * 32) << 16;
     int buf = 0;
-    uint32_t tphase = 0;
+    uint32_t tphase = 0, turn = 0;
     // accumulator `buf` is finished / has been read by this warp
     auto finished = [&]() {
       const bool ok = __all_sync(0xffffffffu, wait_for(tfull(buf), tphase, ab, kSiteFfn + 7));
@@ -600,12 +603,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
       const bool ok = finished();
       const uint32_t acc = tmem + buf * kAccCols + lanes;
       if (ok) {
-        for (int c = 32 * half; c < w.bn; c += 64) {
-          const int col = w.col + c;
-          if (col >= end) break;
-          uint32_t r0[32];
-          tmem_ld32(acc + c, r0);
-          if constexpr (MODE == kFwd) {
+        if constexpr (MODE == kFwd) {
+          for (int c = 32 * half; c < w.bn; c += 64) {
+            const int col = w.col + c;
+            if (col >= end) break;
+            uint32_t r0[32];
+            tmem_ld32(acc + c, r0);
             uint32_t r1[32];
             tmem_ld32(acc + w.bn + c, r1);
             tmem_ld_wait();
@@ -637,18 +640,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               keep_rows32(P, 0, row0, col, end, g, lane);
               keep_rows32(P, 1, row0, col, end, v, lane);
             }
-          } else {
+          }
+        } else {
+          // By boxes of 32 rows x 32 columns through shared memory (rows of 64 bytes, 16-byte pieces permuted
+          // by the row's bits 1 and 2), two of a warp on their way: where the reduction is short, the stores
+          // are the tile's time (64 tokens 5120 x 17408: 100 us in 64-byte stores from registers, 94 so; boxes
+          // of 64 columns 90, but the stage of the ring that they cost slows the longer reductions by 3 to 8 %).
+          for (int c = 32 * half; c < w.bn; c += 64) {
+            const int col = w.col + c;
+            if (col >= end) break;
+            uint32_t r[32];
+            tmem_ld32(acc + c, r);
             tmem_ld_wait();
-            reg_fence(r0);
-            float v[32];
+            reg_fence(r);
+            const uint32_t box = base + kRingBytes + ((warp - 2) * 2 + turn) * kBoxBytes;
+            turn ^= 1u;
+            if (lane == 0) tma_store_wait_read<1>();
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r0[i]);
-            store_rows32(P.out[w.prod], row0, P.m, P.n, col, end, v, lane);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = bf16x2_bits(__uint_as_float(r[8 * j + 2 * e]), __uint_as_float(r[8 * j + 2 * e + 1]));
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)),
+                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (row0 < P.m) tma_store(&P.o[w.prod], box, col, int(row0), policy_normal());
+              tma_store_commit();
+            }
           }
         }
       }
       leave(ok);
     }
+    if (MODE == kDw && lane == 0) tma_store_wait_all<0>();
   }
 
   __syncwarp();
