@@ -354,16 +354,24 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kMaxWarps ? 1 : 2)
   for (int i = 0; i < kPerThread; ++i) dw[i] = db[i] = 0.f;
   // what a row needs besides its elements is loaded a row ahead
   float next_mean = 0.f, next_rstd = 0.f;
-  uint8_t next_scale[NV];
+  // The scale bytes of a warp's vectors: a thread's own of each, or, where a vector is 1 or 2 elements and
+  // the warp's 16 groups therefore more than its loads are worth, a group a lane.
+  constexpr bool kShared = XK == kPacked && VEC <= 2;
+  const int lane = threadIdx.x & 31, group0 = (lane / VEC * W + (t >> 5)) * VEC + lane % VEC;
+  uint8_t next_scale[kShared ? 1 : NV];
   auto look_ahead = [&](uint32_t r) {
     if (r >= M) return;
     next_mean = mean_in[r];
     next_rstd = rstd_in[r];
     if constexpr (XK == kPacked) {
       const uint8_t* sc = static_cast<const uint8_t*>(x_scales) + int64_t(r) * (x_ld >> 5);
+      if constexpr (kShared) {
+        next_scale[0] = lane < kPerThread && group0 < int(x_ld >> 5) ? sc[group0] : uint8_t(0);
+      } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i < nv) next_scale[i] = sc[((i * 32 * W + t) * VEC) >> 5];
+        for (int i = 0; i < NV; ++i)
+          if (i < nv) next_scale[i] = sc[((i * 32 * W + t) * VEC) >> 5];
+      }
     }
   };
   look_ahead(row);
@@ -377,7 +385,14 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == kMaxWarps ? 1 : 2)
     copies_commit();
     const float mean = next_mean, rstd = next_rstd;
     float step[NV];
-    if constexpr (XK == kPacked) {
+    if constexpr (kShared) {
+      const float own = scale_step(next_scale[0]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float s = __shfl_sync(0xffffffffu, own, i * VEC + lane * VEC / 32);
+        step[i] = i < nv ? s : 0.f;
+      }
+    } else if constexpr (XK == kPacked) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) step[i] = i < nv ? scale_step(next_scale[i]) : 0.f;
     }
