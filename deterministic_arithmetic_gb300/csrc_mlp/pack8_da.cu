@@ -13,7 +13,7 @@
 // work on the four stages of a unit at once (all eight warps on one stage at a time waited out every
 // stage's latencies in turn: 25 us). The tensor core takes both operands transposed (M = 128 columns,
 // N = padded rank, K = 16 rows). At 8192 x 4096, rank 16: 38 us for unpacking x and running the delta's
-// own kernels on it, 20 us here with the combine launch; 17 without the expansion, 18 without the MMAs,
+// own kernels on it, 19.8 us here with the combine launch; 17 without the expansion, 18 without the MMAs,
 // 12 with the copies and launches alone.
 //
 // Warps: 0 copies, 1 issues the MMAs, 2..9 add the leaves, 10..17 expand.
