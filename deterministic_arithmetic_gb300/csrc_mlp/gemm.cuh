@@ -12,7 +12,7 @@
 //
 // 4096 x 5120 x 17408: 767 us forward (1.90 PFLOP/s), 856 dx, 760 dW on a cool device. Bound by the tensor
 // pipe (77 to 82 % active at 2048 x 4096 x 8192) and, back to back, by the device's power: the clock falls
-// to some 1.6 GHz, and cuBLAS's products take 830 to 860 us each pair. One token (5120 -> 17408): 57 us, the
+// to some 1.6 GHz, and plain library products of the sizes take 830 to 860 us. One token (5120 -> 17408): 57 us, the
 // weights' 356 MB at 6.2 TB/s.
 //
 // CG = 2 works in pairs of CTAs (a cluster of two neighbouring SMs, cta_group::2): a 256 x 256 tile,
