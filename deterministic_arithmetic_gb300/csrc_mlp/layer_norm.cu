@@ -10,7 +10,7 @@
 // come into its own part of shared memory (cp.async, three rows deep) and reads
 // back only what it copied itself, so the loads of several rows are in flight with
 // no barrier and no registers spent on them; the row's sums take the loop's only
-// barriers. Measured at 8192 x 4096 bf16: 23 us forward, 49 us backward (45 and the
+// barriers. Measured at 8192 x 4096 bf16: 23 us forward, 41 us backward (37 and the
 // partials' sum); loads straight into registers 43 and 65 us; rows brought by bulk
 // copies and mbarriers 31 and 49 us (the copying thread's work a row held up its CTA's
 // barriers).
@@ -19,8 +19,8 @@
 // FP32 rows (6.1). On bf16 rows the backward pass is bound by a warp's chain a row: 361
 // instructions for 512 columns, and the sums' shuffles, of which 16 warps on an SM (128
 // registers a thread, 48 of them the weight and the column sums) issue one every second
-// cycle. Twice the warps with 8 columns a thread took 73 us and two rows to a barrier 56:
-// both add instructions to a row.
+// cycle. Twice the warps with 8 columns a thread took 24 us more and two rows to a barrier 7
+// more: both add instructions to a row.
 //
 // W and each thread's columns follow from N alone, so a row's sums are added in
 // the same order in any batch. The variance is the sum of squares about the mean,
@@ -204,18 +204,33 @@ __device__ __forceinline__ void store16(uint8_t* row, int nv, int W, int t, cons
   }
 }
 
-// The thread's 16 column sums to and from a row of floats.
+// The thread's 16 column sums to and from a row of floats (16-byte aligned), four at a time where its
+// columns lie so (8192 x 4096 bf16 backward: 49 us one at a time, a sector a lane and store; 41 so).
 template <int VEC>
 __device__ __forceinline__ void put_sums16(float* row, int nv, int W, int t, const float (&v)[kPerThread]) {
+  constexpr int S = VEC >= 4 ? 4 : 1;
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k)
-    if (k / VEC < nv) row[(k / VEC * 32 * W + t) * VEC + k % VEC] = v[k];
+  for (int k = 0; k < kPerThread; k += S)
+    if (k / VEC < nv) {
+      float* at = row + (k / VEC * 32 * W + t) * VEC + k % VEC;
+      if constexpr (S == 4) *reinterpret_cast<float4*>(at) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      else *at = v[k];
+    }
 }
 template <int VEC>
 __device__ __forceinline__ void add_sums16(const float* row, int nv, int W, int t, float (&v)[kPerThread]) {
+  constexpr int S = VEC >= 4 ? 4 : 1;
 #pragma unroll
-  for (int k = 0; k < kPerThread; ++k)
-    if (k / VEC < nv) v[k] += row[(k / VEC * 32 * W + t) * VEC + k % VEC];
+  for (int k = 0; k < kPerThread; k += S)
+    if (k / VEC < nv) {
+      const float* at = row + (k / VEC * 32 * W + t) * VEC + k % VEC;
+      if constexpr (S == 4) {
+        const float4 a = *reinterpret_cast<const float4*>(at);
+        v[k] += a.x; v[k + 1] += a.y; v[k + 2] += a.z; v[k + 3] += a.w;
+      } else {
+        v[k] += *at;
+      }
+    }
 }
 
 // Four partial sums in step, then their tree.
