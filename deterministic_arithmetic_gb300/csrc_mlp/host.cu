@@ -62,6 +62,18 @@ lora_status device_ready(int* nsm) {
   return LORA_OK;
 }
 
+bool any_device() {
+  int n = 0;
+  const cudaError_t e = cudaGetDeviceCount(&n);
+  return e != cudaErrorNoDevice && e != cudaErrorInsufficientDriver && (e != cudaSuccess || n > 0);
+}
+
+bool in_device_memory(const void* p) {
+  cudaPointerAttributes a{};
+  return cudaPointerGetAttributes(&a, p) == cudaSuccess &&
+         (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged);
+}
+
 uint32_t* status_block() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;

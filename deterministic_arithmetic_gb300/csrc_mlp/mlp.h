@@ -33,6 +33,10 @@ lora_status check_ptrs(const P*... p) {
 
 // LORA_OK on an sm_103 device (with every kernel of the operators prepared on it); *nsm its SMs.
 lora_status device_ready(int* nsm);
+// Whether the machine has a CUDA device (and a driver for it) at all.
+bool any_device();
+// Whether p is device (or managed) memory.
+bool in_device_memory(const void* p);
 
 // Raise the shared-memory limits of the kernels (on the current device).
 cudaError_t prepare_ffn();

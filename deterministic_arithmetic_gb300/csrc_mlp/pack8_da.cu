@@ -435,14 +435,26 @@ lora_status lora_delta_bwd_packed8(const void* dy, const void* codes, const void
                                    void* stream) {
   if (!rank_ok(R)) return shape_ok(M, K) && shape_ok(M, N) ? LORA_ERR_RANK : LORA_ERR_SHAPE;
   if (!shape_ok(M, K) || !shape_ok(M, N)) return LORA_ERR_SHAPE;
-  if (M == 0) return LORA_OK;                       // as lora_delta_bwd
-  lora_status s = check_ptrs(dy, codes, scales, a, b, u, dx, da, db, du, workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  lora_status s;
+  int nsm = 0;
+  if (M == 0) {                                     // sums over no rows
+    // (where there is no device there is no tensor to write either: the no-op of lora_delta_bwd)
+    if ((s = check_ptrs(da, db)) != LORA_OK || !any_device()) return s;
+    if ((s = device_ready(&nsm)) != LORA_OK) return s;
+    // lora_delta_bwd does not look at the pointers of a call on no rows: what a caller of it got away with
+    // becomes an error here and not a stray write
+    if (!in_device_memory(da) || !in_device_memory(db)) return LORA_ERR_CUDA;
+    return cudaMemsetAsync(da, 0, size_t(R) * size_t(K) * 4, st) == cudaSuccess &&
+                   cudaMemsetAsync(db, 0, size_t(N) * size_t(R) * 4, st) == cudaSuccess
+               ? LORA_OK
+               : LORA_ERR_CUDA;
+  }
+  s = check_ptrs(dy, codes, scales, a, b, u, dx, da, db, du, workspace);
   if (s != LORA_OK) return s;
   const BwdLayout L = bwd_layout(M, K, N, R);
   if (workspace_bytes < L.bytes) return LORA_ERR_WORKSPACE;
-  int nsm = 0;
   if ((s = device_ready(&nsm)) != LORA_OK) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   float *du_part = reinterpret_cast<float*>(ws + L.du), *db_part = reinterpret_cast<float*>(ws + L.db);

@@ -61,6 +61,6 @@ def lora_delta_bwd_packed8_workspace_size(M: int, K: int, N: int, R: int) -> int
 def lora_delta_bwd_packed8(dy, p: Packed8, a, b, u, alpha: float, *, dx=None, da=None, db=None, du=None,
                            workspace=None):
     """``lora_delta.lora_delta_bwd(dy, x, a, b, u, alpha)`` with x given as its 8-bit checkpoint:
-    ``(dx, da, db, du)``, bit for bit those of the unpacked x. ``workspace`` (optional):
-    ``lora_delta.new_workspace`` of the size above."""
+    ``(dx, da, db, du)``, bit for bit those of the unpacked x; of no rows, ``da`` and ``db`` are zeros.
+    ``workspace`` (optional): ``lora_delta.new_workspace`` of the size above."""
     return c.mlp.lora_delta_bwd_packed8(dy, p, a, b, u, alpha, dx, da, db, du, workspace)

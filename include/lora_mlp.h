@@ -72,7 +72,8 @@ lora_status lora_pack8_da(const void *du, const void *codes, const void *scales,
                           float *da, void *workspace, size_t workspace_bytes, void *stream);
 
 /* lora_delta_bwd with x given packed: same outputs, bit for bit those of lora_delta_bwd for
- * the unpacked x, which is nowhere formed. The workspace starts with lora_delta_bwd's control block
+ * the unpacked x, which is nowhere formed (M = 0, where that call writes nothing: da and db are
+ * written as zeros, as everywhere here). The workspace starts with lora_delta_bwd's control block
  * (zero before its first use), whose status block its kernels report to. */
 size_t lora_delta_bwd_packed8_workspace_size(int64_t M, int64_t K, int64_t N, int64_t R);
 lora_status lora_delta_bwd_packed8(const void *dy, const void *codes, const void *scales, const void *a, const void *b,

@@ -1,0 +1,44 @@
+"""Edges of the MLP-block operators on the GPU: batches of no rows, kernels whose CTAs take several units of
+work, streams and devices, status, against 64-bit forms or the unpacked tensor's bits."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import mlp_ref as R  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from deterministic_arithmetic_gb300 import build_lib
+
+    build_lib.build()
+
+
+def rnd(*shape, c=1.0, dtype=torch.bfloat16, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + sum(shape))
+    return (torch.randn(*shape, generator=g, device="cuda") * c).to(dtype)
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("r", [8, 40])
+def test_packed_backward_of_no_rows_gives_zero_gradients(r, given):
+    """da and db are sums over no rows: zeros, whatever the outputs held before."""
+    from deterministic_arithmetic_gb300 import pack8
+
+    K, N = 200, 136
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    p = pack8.pack8(torch.empty(0, K, **bf))
+    nan = {k: torch.full(s, float("nan"), device="cuda") for k, s in (("da", (r, K)), ("db", (N, r)))}
+    trash = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]       # what new outputs may get
+    del trash
+    dx, da, db, du = pack8.lora_delta_bwd_packed8(torch.empty(0, N, **bf), p, rnd(r, K), rnd(N, r),
+                                                  torch.empty(0, r, **bf), 2.0, **(nan if given else {}))
+    assert dx.shape == (0, K) and du.shape == (0, r)
+    assert torch.equal(da, torch.zeros(r, K, device="cuda")) and torch.equal(db, torch.zeros(N, r, device="cuda"))
+    if given:
+        assert da.data_ptr() == nan["da"].data_ptr() and db.data_ptr() == nan["db"].data_ptr()
