@@ -10,6 +10,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <sstream>
@@ -79,12 +80,18 @@ void* check_either(const Tensor& t, const char* name, c10::IntArrayRef shape, in
   *code = t.scalar_type() == BF16 ? LORA_BF16 : LORA_F32;
   return check(t, name, shape, t.scalar_type(), dev);
 }
-// The device an operator runs on, that of its first tensor, and that tensor's two sizes.
+// The device an operator runs on, that of its first tensor, and that tensor's two sizes. The library
+// launches on the current device, where another device's addresses are not to be used: they are refused.
 int first(const Tensor& t, const char* name, int64_t* rows, int64_t* cols) {
   if (t.dim() != 2 || !t.is_cuda()) refuse(t, name, "2-D tensor", t.sizes(), t.is_cuda() ? int(t.get_device()) : -1);
+  const int dev = int(t.get_device());
+  c10::DeviceIndex current = -1;
+  if (c10::cuda::GetDevice(&current) != cudaSuccess || current != dev)
+    raise(PyExc_ValueError, std::string(name) + " is on cuda:" + std::to_string(dev) + ", which is not the current device" +
+                                (current < 0 ? "" : " (cuda:" + std::to_string(int(current)) + ")"));
   *rows = t.size(0);
   *cols = t.size(1);
-  return int(t.get_device());
+  return dev;
 }
 Tensor empty(c10::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, c10::DeviceIndex(dev)), std::nullopt);

@@ -3,8 +3,8 @@
  * (GB300 / sm_103a): layer norm, activation checkpoints in 8 bits and their use
  * in the backward pass, and the gated feed-forward block. Same library, status
  * codes and conventions as lora_delta.h:
- *   - Tensors are dense, row-major, contiguous, in device memory, 16-byte
- *     aligned. The caller owns every buffer and the stream; no entry point
+ *   - Tensors are dense, row-major, contiguous, in the current device's memory
+ *     (the Python functions refuse those of another one), 16-byte aligned. The caller owns every buffer and the stream; no entry point
  *     allocates or synchronises (the status calls at the end excepted). A
  *     workspace needs no initial value (lora_delta_bwd_packed8's excepted).
  *   - Sizes below 2^31, M >= 0. M = 0 returns LORA_OK; gradients that are sums

@@ -26,3 +26,34 @@ def test_packed_backward_of_no_rows_wants_its_gradients():
 
     assert call(da=None) == call(db=None) == NULL
     assert call(da=F + 4) == call(db=F + 8) == ALIGN
+
+
+def calls_on(device, monkeypatch):
+    """A call of every operator with tensors that claim to be on ``device`` (fake ones: they have no memory)."""
+    import torch
+    from torch._subclasses import fake_tensor
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from deterministic_arithmetic_gb300 import gated_ffn as ffn, layer_norm as ln, pack8
+
+    # on a machine with a GPU the mode would first touch the device, which is not there
+    monkeypatch.setattr(fake_tensor, "init_gpu_context", lambda *_: None, raising=False)
+    with FakeTensorMode():
+        def t(*shape, dtype=torch.bfloat16):
+            return torch.empty(*shape, dtype=dtype, device=device)
+
+        x, row, w, f32 = t(4, 64), t(64), t(32, 64), t(4, dtype=torch.float32)
+        p = pack8.Packed8(t(4, 64, dtype=torch.int8), t(4, 2, dtype=torch.uint8), 64)
+        h, du, a, b = t(4, 32), t(4, 8), t(8, 64), t(32, 8)
+    return [lambda: ln.layer_norm_fwd(x, row, row), lambda: ln.layer_norm_bwd(x, x, row, f32, f32),
+            lambda: ln.layer_norm_bwd(x, p, row, f32, f32), lambda: pack8.pack8(x), lambda: pack8.unpack8(p),
+            lambda: pack8.pack8_da(du, p), lambda: pack8.lora_delta_bwd_packed8(h, p, a, b, du, 1.0),
+            lambda: ffn.gated_ffn_fwd(x, w, w), lambda: ffn.gated_ffn_bwd(h, x, w, w, h, h)]
+
+
+@pytest.mark.parametrize("i", range(9))
+def test_tensors_on_another_device_than_the_current_one_are_refused(i, monkeypatch):
+    """The library launches on the current device, so tensors of another one must not reach it. Device 5 is
+    current nowhere here; the refusal comes before any address is taken."""
+    with pytest.raises(ValueError, match="cuda:5, which is not the current device"):
+        calls_on("cuda:5", monkeypatch)[i]()
