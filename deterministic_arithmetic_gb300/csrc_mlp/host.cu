@@ -121,6 +121,8 @@ lora_status lora_mlp_device_status(int* code) {
   const lora_status s = mlp::device_ready(&nsm);
   if (s != LORA_OK) return s;
   uint32_t word = 0;
+  // (the copy alone would not wait for streams that do not block on the default one, as torch's own do not)
+  if (cudaDeviceSynchronize() != cudaSuccess) return LORA_ERR_CUDA;
   if (cudaMemcpy(&word, mlp::status_block(), sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return LORA_ERR_CUDA;
   *code = int(word);
   return word ? LORA_ERR_TIMEOUT : LORA_OK;
@@ -130,6 +132,7 @@ lora_status lora_mlp_device_status_reset(int stall_kind, int wait_limit_us) {
   int nsm = 0;
   const lora_status s = mlp::device_ready(&nsm);
   if (s != LORA_OK) return s;
+  if (cudaDeviceSynchronize() != cudaSuccess) return LORA_ERR_CUDA;
   const uint32_t words[4] = {0u, 0u, uint32_t(stall_kind), uint32_t(wait_limit_us)};
   return cudaMemcpy(mlp::status_block(), words, sizeof(words), cudaMemcpyHostToDevice) == cudaSuccess ? LORA_OK
                                                                                                   : LORA_ERR_CUDA;

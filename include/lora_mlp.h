@@ -4,9 +4,10 @@
  * in the backward pass, and the gated feed-forward block. Same library, status
  * codes and conventions as lora_delta.h:
  *   - Tensors are dense, row-major, contiguous, in the current device's memory
- *     (the Python functions refuse those of another one), 16-byte aligned. The caller owns every buffer and the stream; no entry point
- *     allocates or synchronises (the status calls at the end excepted). A
- *     workspace needs no initial value (lora_delta_bwd_packed8's excepted).
+ *     (the Python functions refuse those of another one), 16-byte aligned. The
+ *     caller owns every buffer and the stream; no entry point allocates or
+ *     synchronises (the status calls at the end excepted). A workspace needs no
+ *     initial value (lora_delta_bwd_packed8's excepted).
  *   - Sizes below 2^31, M >= 0. M = 0 returns LORA_OK; gradients that are sums
  *     over the rows are then written as zeros, nothing else is.
  *   - Every sum is FP32 in a fixed order that does not depend on the device. A
@@ -107,7 +108,7 @@ lora_status lora_gated_ffn_bwd(const void *dh, const void *x, const void *w_gate
  * The tensor-core kernels of these operators bound every wait. One that runs out ends its kernel
  * early and leaves a code, (site << 8) | 1, in the library's status block of the device (the
  * first code stays): the outputs of that call, and of calls since, are then not to be used.
- *   lora_mlp_device_status        waits for the device; *code = the block's code, 0 when no kernel
+ *   lora_mlp_device_status        waits for the device (every stream of it); *code = the block's code, 0 when no kernel
  *                                 reported a problem. Returns LORA_OK, or LORA_ERR_TIMEOUT.
  *   lora_mlp_device_status_reset  waits for the device and clears the code. For tests: stall_kind
  *                                 != 0 makes the producer of that kind of kernel wait for what

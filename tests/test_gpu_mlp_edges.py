@@ -42,3 +42,28 @@ def test_packed_backward_of_no_rows_gives_zero_gradients(r, given):
     assert torch.equal(da, torch.zeros(r, K, device="cuda")) and torch.equal(db, torch.zeros(N, r, device="cuda"))
     if given:
         assert da.data_ptr() == nan["da"].data_ptr() and db.data_ptr() == nan["db"].data_ptr()
+
+
+def test_status_calls_wait_for_every_stream():
+    """A wait that runs out (1 ms) in a call queued on another stream behind 50 ms of idling: the status call comes
+    back with its code, and a reset behind such a call leaves nothing of it."""
+    from deterministic_arithmetic_gb300 import _capi, pack8
+
+    du, p = rnd(200, 16), pack8.pack8(rnd(200, 264))
+    s = torch.cuda.Stream()
+
+    def stalled_call():
+        _capi.device_status_reset(13, 1000)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)                # cycles, at up to 2.1 GHz
+            pack8.pack8_da(du, p)
+
+    try:
+        stalled_call()
+        assert _capi.device_status() == (56 << 8) | 1
+        stalled_call()
+    finally:
+        _capi.device_status_reset()
+    torch.cuda.synchronize()
+    assert _capi.device_status() == 0
