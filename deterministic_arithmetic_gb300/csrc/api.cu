@@ -833,6 +833,7 @@ lora_status lora_delta_exact_finalize(const int64_t* digits, int64_t n, float* o
 lora_status lora_delta_device_status(const void* workspace, int* code) {
   if (!workspace || !code) return LORA_ERR_NULL;
   uint32_t v = 0;
+  if (cudaDeviceSynchronize() != cudaSuccess) return LORA_ERR_CUDA;   // the copy alone waits for blocking streams only
   if (cudaMemcpy(&v, workspace, sizeof v, cudaMemcpyDeviceToHost) != cudaSuccess) return LORA_ERR_CUDA;
   *code = int(v);
   return v == 0 ? LORA_OK : LORA_ERR_TIMEOUT;

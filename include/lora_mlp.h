@@ -108,8 +108,9 @@ lora_status lora_gated_ffn_bwd(const void *dh, const void *x, const void *w_gate
  * The tensor-core kernels of these operators bound every wait. One that runs out ends its kernel
  * early and leaves a code, (site << 8) | 1, in the library's status block of the device (the
  * first code stays): the outputs of that call, and of calls since, are then not to be used.
- *   lora_mlp_device_status        waits for the device (every stream of it); *code = the block's code, 0 when no kernel
- *                                 reported a problem. Returns LORA_OK, or LORA_ERR_TIMEOUT.
+ *   lora_mlp_device_status        waits for the device (every stream of it); *code = the block's
+ *                                 code, 0 when no kernel reported a problem. Returns LORA_OK, or
+ *                                 LORA_ERR_TIMEOUT.
  *   lora_mlp_device_status_reset  waits for the device and clears the code. For tests: stall_kind
  *                                 != 0 makes the producer of that kind of kernel wait for what
  *                                 never comes; wait_limit_us != 0 sets the waits' limit.

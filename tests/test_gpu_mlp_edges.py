@@ -67,3 +67,19 @@ def test_status_calls_wait_for_every_stream():
         _capi.device_status_reset()
     torch.cuda.synchronize()
     assert _capi.device_status() == 0
+
+
+def test_workspace_status_waits_for_every_stream():
+    """The same of the status block of a workspace, which the packed backward's kernels report to."""
+    from deterministic_arithmetic_gb300 import lora_delta as ld, pack8
+
+    M, K, N, r = 200, 264, 136, 16
+    ws = ld.new_workspace(pack8.lora_delta_bwd_packed8_workspace_size(M, K, N, r), "cuda")
+    ws[:16].view(torch.int32).copy_(torch.tensor([0, 0, 13, 1000]))       # dA's copying warp stalls; 1 ms
+    args = rnd(M, N), pack8.pack8(rnd(M, K)), rnd(r, K), rnd(N, r), rnd(M, r), 2.0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+        pack8.lora_delta_bwd_packed8(*args, workspace=ws)
+    assert ld.lora_delta_device_status(ws) == (56 << 8) | 1
