@@ -83,3 +83,28 @@ def test_workspace_status_waits_for_every_stream():
         torch.cuda._sleep(100_000_000)
         pack8.lora_delta_bwd_packed8(*args, workspace=ws)
     assert ld.lora_delta_device_status(ws) == (56 << 8) | 1
+
+
+def test_the_readme_step_is_the_examples_step():
+    """README.md's lines, run as they stand: the output and every gradient of examples/mlp_block_step.py."""
+    import os
+    import re
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, os.path.join(root, "examples"))
+    import mlp_block_step as ex
+
+    from deterministic_arithmetic_gb300 import lora_delta as ld
+
+    text = open(os.path.join(root, "README.md"), encoding="utf-8").read()
+    step, = [b for b in re.findall(r"```python\n(.*?)```", text, flags=re.S) if "gated_ffn_bwd" in b]
+    p, x, dh = ex.make(300, 256, 520, 16)
+    names = dict(torch=torch, ld=ld, x=x, dh=dh, weight=p.ln_weight, bias=p.ln_bias, w_gate=p.w_gate, w_up=p.w_up,
+                 a_g=p.a_gate, b_g=p.b_gate, a_u=p.a_up, b_u=p.b_up, alpha=p.alpha)
+    exec(step, names)
+    h, kept = ex.forward(p, x)
+    dx, grads = ex.backward(p, dh, kept)
+    mine = dict(ln_weight="dw", ln_bias="db", a_gate="da_g", b_gate="db_g", a_up="da_u", b_up="db_u")
+    assert torch.equal(names["h"], h) and torch.equal(names["dx"], dx)
+    assert all(torch.equal(names[mine[k]], grads[k]) for k in grads)
