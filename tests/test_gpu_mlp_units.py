@@ -112,3 +112,80 @@ def test_norm_of_equal_elements():
     rstd = R.f64(ln.layer_norm_fwd(x, w, eps=1e-5)[2])
     ref = 1 / np.sqrt(np.float64(np.float32(1e-5)))
     assert (np.abs(rstd - ref) <= 4 * R.U32 * ref).all()
+
+
+# -------------------------------------------------------------- gated block
+def check_products(M, K, F, act, delta):
+    """Forward and backward against 64 bits, the products with torch's 64-bit ones (the sizes are large)."""
+    from deterministic_arithmetic_gb300 import gated_ffn as ffn, pack8
+
+    t = ffn_inputs(M, K, F, M + K + F)
+    kw = dict(delta_gate=t["dg"], delta_up=t["du"]) if delta else {}
+    h, gate, up = ffn.gated_ffn_fwd(t["x"], t["wg"], t["wu"], activation=act, save="bf16", **kw)
+    h8, gate8, up8 = ffn.gated_ffn_fwd(t["x"], t["wg"], t["wu"], activation=act, save="packed8", **kw)
+    assert torch.equal(h, h8)
+
+    def prod(p, q):                                       # 64-bit, and the sum of the products' magnitudes
+        return (p @ q).cpu().numpy(), (p.abs() @ q.abs()).cpu().numpy()
+
+    x, wg, wu = t["x"].double(), t["wg"].double(), t["wu"].double()
+    n = (K / 16 + 16) * A22
+    pre, err = [], []
+    for w, d in ((wg, "dg"), (wu, "du")):
+        v, s = prod(x, w.t())
+        v = v + (R.f64(t[d]) if delta else 0.0)
+        pre.append(v)
+        err.append(n * s + R.U32 * np.abs(v))
+    (g, u), (eg, eu) = pre, err
+    a = np.abs(R.act(act, g)[0])
+    rh = R.act(act, g)[0] * u
+    bound = (1.2 * eg + 2.0 ** -18 * a) * np.abs(u) + (a + 1.2 * eg) * eu
+    within("h", h, rh, bound + R.U16 * (np.abs(rh) + bound) + 1e-38)
+    for name, b16, p8, v, e in (("gate", gate, gate8, g, eg), ("up", up, up8, u, eu)):
+        within(name, b16, v, e + R.U16 * (np.abs(v) + e))
+        top = np.pad(np.abs(v) + e, ((0, 0), (0, -F % 32))).reshape(M, -1, 32).max(2)
+        within(name + " in 8 bits", pack8.unpack8(p8), v, e + np.repeat(top, 32, 1)[:, :F] / 127.5)
+    del h8, gate8, up8
+    dx, dgate, dup, dwg, dwu = ffn.gated_ffn_bwd(t["dh"], t["x"], t["wg"], t["wu"], gate, up, activation=act)
+    DG, DU = dgate.double(), dup.double()
+    (p, sp), (q, sq) = prod(DG, wg), prod(DU, wu)
+    e = (2 * F / 16 + 16) * A22 * (sp + sq)
+    within("dx", dx, p + q, e + R.U16 * (np.abs(p + q) + e) + 1e-38)
+    for name, got, d in (("dw_gate", dwg, DG), ("dw_up", dwu, DU)):
+        rd, s = prod(d.t(), x)
+        e = (M / 16 + 16) * A22 * s
+        within(name, got, rd, e + R.U16 * (np.abs(rd) + e) + 1e-38)
+
+
+# With 76 pairs of CTAs (256 x 256 tiles of dx and dW, 256 x 128 of the forward): tiles, and what is left for a last
+# round in half tiles where it is at most 38.
+#   1300 x 4160 -> 576   dx 102 (26 halved), operands in whole 64-column blocks
+#   2100 x 2560 -> 1088  forward 81 (5), dx 90 (14), dW 100 (24), blocks
+#   2600 x 1792 -> 896   forward 77 (1), dx 77 (1), blocks
+#   2600 x 1792 -> 1408  forward 121, dx 77 (1), dW 84 (8), blocks
+#   5000 x 2048 -> 2048  forward 320 (16), dx 160 (8), dW 128, blocks: several tiles a pair
+#   2300 x 2312 -> 1096  forward 81 (5), dx 90 (14), dW 100 (24), rows that are not whole blocks
+@pytest.mark.parametrize("M,K,F,act,delta", [
+    (1300, 4160, 576, "silu", True), (2100, 2560, 1088, "gelu", False), (2600, 1792, 896, "silu", True),
+    (2600, 1792, 1408, "gelu", True), (5000, 2048, 2048, "silu", False), (2300, 2312, 1096, "silu", True)])
+def test_products_on_pairs(M, K, F, act, delta):
+    check_products(M, K, F, act, delta)
+
+
+@pytest.mark.parametrize("M,K,F", [(2600, 1792, 1408), (4096, 1536, 2112)])
+def test_rows_of_pairs_with_blocked_operands_do_not_depend_on_the_batch(M, K, F):
+    """The whole batch goes to pairs of CTAs, its parts to lone CTAs and to clusters, all with blocked operands."""
+    from deterministic_arithmetic_gb300 import gated_ffn as ffn
+
+    t = ffn_inputs(M, K, F)
+
+    def step(lo, hi):
+        x, dh, dg, du = (t[k][lo:hi].clone() for k in ("x", "dh", "dg", "du"))
+        h, gate, up = ffn.gated_ffn_fwd(x, t["wg"], t["wu"], delta_gate=dg, delta_up=du, save="bf16")
+        return (h, gate, up) + ffn.gated_ffn_bwd(dh, x, t["wg"], t["wu"], gate, up)
+
+    whole = step(0, M)
+    for lo, hi in ((0, 1), (M - 1, M), (8, 72), (100, 228), (0, 300), (64, 1100), (300, M)):
+        for a, b in zip(whole[:6], step(lo, hi)[:6]):
+            assert torch.equal(a[lo:hi], b), (lo, hi)
+    assert all(torch.equal(a, b) for a, b in zip(whole, step(0, M)))
