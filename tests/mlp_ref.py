@@ -67,3 +67,15 @@ def act(name, y):
 def ffn(name, x, wg, wu, dg=0.0, du=0.0):
     g, u = x @ wg.T + dg, x @ wu.T + du
     return act(name, g)[0] * u, g, u
+
+
+def ffn_off_along(name, x, wg, wu, dh, i, grad, h=2.0 ** -12):
+    """How far |grad|, the slope that a gradient of sum(dh * h) by argument i (x, wg, wu) claims along itself, is from
+    the central difference along it, in units of |grad|. A gradient off by an error e shows it as (e . grad) / |grad|^2."""
+    size = np.linalg.norm(grad)
+    ends = []
+    for s in (h, -h):
+        args = [x, wg, wu]
+        args[i] = args[i] + s * grad / size
+        ends.append((ffn(name, *args)[0] * dh).sum())
+    return abs((ends[0] - ends[1]) / (2 * h) / size - 1)

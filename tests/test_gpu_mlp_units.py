@@ -189,3 +189,20 @@ def test_rows_of_pairs_with_blocked_operands_do_not_depend_on_the_batch(M, K, F)
         for a, b in zip(whole[:6], step(lo, hi)[:6]):
             assert torch.equal(a[lo:hi], b), (lo, hi)
     assert all(torch.equal(a, b) for a, b in zip(whole, step(0, M)))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gradients_against_differences_along_themselves(act):
+    """The slope of the 64-bit forward along each gradient is that gradient's length. Tolerance: gate, up, dgate (dup)
+    and the result are each rounded to bf16, 2^-9 of a value at most; the errors of one gradient's terms are
+    independent in sign, so its error's length stays below 2^-9 sqrt(4) = 2^-8 of its own, and 2^-7 allows twice that.
+    Truncation (h^2, h = 2^-12) and 64-bit rounding are below 1e-6. A missing or halved term is off by several times
+    the tolerance (test_mlp_host.py shows it on planted ones)."""
+    from deterministic_arithmetic_gb300 import gated_ffn as ffn
+
+    t = ffn_inputs(24, 40, 56, 3)
+    _, gate, up = ffn.gated_ffn_fwd(t["x"], t["wg"], t["wu"], activation=act, save="bf16")
+    dx, _, _, dwg, dwu = ffn.gated_ffn_bwd(t["dh"], t["x"], t["wg"], t["wu"], gate, up, activation=act)
+    args = [R.f64(t[k]) for k in ("x", "wg", "wu", "dh")]
+    for i, grad in enumerate((dx, dwg, dwu)):
+        assert R.ffn_off_along(act, *args, i, R.f64(grad)) <= 2.0 ** -7, i

@@ -57,3 +57,30 @@ def test_tensors_on_another_device_than_the_current_one_are_refused(i, monkeypat
     current nowhere here; the refusal comes before any address is taken."""
     with pytest.raises(ValueError, match="cuda:5, which is not the current device"):
         calls_on("cuda:5", monkeypatch)[i]()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_differences_along_a_gradient_tell_wrong_ones(act):
+    """ffn_off_along on the formulas' own gradients and on planted mistakes, at the GPU test's sizes and tolerance."""
+    import numpy as np
+
+    import mlp_ref as R
+
+    rng = np.random.RandomState(3)
+    M, K, F = 24, 40, 56
+    x, wg, wu = rng.standard_normal((M, K)), rng.standard_normal((F, K)) / K ** 0.5, rng.standard_normal((F, K)) / K ** 0.5
+    dh = 0.1 * rng.standard_normal((M, F))
+    _, g, u = R.ffn(act, x, wg, wu)
+    a, slope = R.act(act, g)
+    p = a / g                                             # act(g) = g p: the slope without its second term
+    dg, du, short = dh * u * slope, dh * a, dh * u * p
+
+    def off(i, grad):
+        return R.ffn_off_along(act, x, wg, wu, dh, i, grad)
+
+    right = (dg @ wg + du @ wu, dg.T @ x, du.T @ x)
+    assert all(off(i, v) < 1e-6 for i, v in enumerate(right))
+    for i, v in ((0, dg @ wg), (0, du @ wu), (0, short @ wg + du @ wu), (0, -dg @ wg + du @ wu), (1, short.T @ x),
+                 (1, 0.5 * right[1]), (1, (dh * slope).T @ x), (2, 0.5 * right[2]), (2, (dh * p).T @ x), (2, (dh * g).T @ x)):
+        print(act, i, off(i, v))
+        assert off(i, v) > 2 * 2.0 ** -7, i
