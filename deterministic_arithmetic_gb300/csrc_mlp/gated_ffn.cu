@@ -67,10 +67,6 @@ bool kind_ok(int act, int keep) {
          (keep == LORA_KEEP_NONE || keep == LORA_KEEP_BF16 || keep == LORA_KEEP_PACKED8);
 }
 
-// Pairs of CTAs that fit on the device at once, and clusters of two and of eight (set when the kernels are
-// prepared).
-int g_pairs = 0, g_splits[2] = {};
-
 // The operands of a product: a [a_rows][a_cols] and b [b_rows][b_cols], two of each (the second may
 // be the first), bf16.
 struct Operands {
@@ -86,7 +82,7 @@ bool rows_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, bool bl
 }
 
 template <int MODE, int CG, int SPLIT = 0>
-lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream_t st) {
+lora_status launch_as(FfnArgs& P, const Operands& o, int bn, const FfnFit& fit, cudaStream_t st) {
   constexpr int products = MODE == kDw ? 2 : 1;
   P.bn = bn;
   // a batch smaller than a tile: only its rows are copied, and the ring holds more stages (the other
@@ -117,12 +113,12 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   if (total >= int64_t(1) << 30) return LORA_ERR_SHAPE;
   // The pairs take the tiles in rounds. A last round that would keep at most half of them at work is
   // dealt out as half tiles instead: it then takes half a tile's time.
-  const int rest = int(total % g_pairs);
-  const bool halves = CG == 2 && 2 * rest <= g_pairs;
+  const int rest = CG == 2 ? int(total % fit.pairs) : 0;
+  const bool halves = CG == 2 && 2 * rest <= fit.pairs;
   P.whole = int(halves ? total - rest : total);
   P.total = int(halves ? total + rest : total);
   constexpr int cluster = SPLIT ? SPLIT : CG;
-  const int most = SPLIT ? P.total : (CG == 2 ? g_pairs : nsm);    // a split's clusters have a tile each
+  const int most = SPLIT ? P.total : (CG == 2 ? fit.pairs : fit.nsm);    // a split's clusters have a tile each
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(cluster * (P.total < most ? P.total : most)));
   cfg.blockDim = dim3(kGemmThreads);
@@ -143,53 +139,20 @@ lora_status launch_as(FfnArgs& P, const Operands& o, int bn, int nsm, cudaStream
   return go(ffn_gemm_kernel<MODE, CG, SPLIT>);
 }
 
-// What a 64-deep block of a lone CTA's tile of w columns takes, and in a split of dx what a cluster takes
-// besides its blocks (starting, filling its ring, joining the sums), in units of 0.5 to 0.8 ns, by the rows.
-// Fitted to the times of 27 shapes of dx from 1 x 96 to 2048 x 8192, taken in each way: the way and width
-// of least cost are the fastest there, or within 2 % of it.
 template <int MODE>
-int64_t block_cost(int w) {
-  return MODE == kFwd ? 2 * w + 64 : w + (MODE == kDx ? 256 : 64);
-}
-constexpr int kJoinTwo = 4000, kJoinEight = 10000, kJoinRow = 50;    // (a row of a tile, sent by all eight)
-
-// Pairs of CTAs where the output has more rows than one CTA's and the 256 x 256 tiles give every
-// pair one. CTAs alone otherwise, in tiles narrow enough to occupy the SMs: the width whose rounds
-// over all SMs cost least. For dx a cluster a tile where that costs less, a CTA a product or eight with
-// a piece each (us a call, alone / two / eight: 1 x 11392 -> 96 78 / 31 / 12; 64 x 17408 -> 5120
-// 116 / 83 / 91; 512 x 8192 -> 2048 67 / 60 / 93; 300 x 11008 -> 4096 98 / 133 / 148).
-template <int MODE>
-lora_status launch(FfnArgs& P, const Operands& o, int nsm, cudaStream_t st) {
-  constexpr int most = MODE == kFwd ? 128 : 256;
-  // narrower tiles go in steps of whole groups of 32 (packed values kept), 8 columns, or 64-column blocks
-  const int step = MODE != kFwd ? 64 : (P.keep_kind == LORA_KEEP_PACKED8 ? 32 : 8), least = MODE == kFwd ? 32 : 64;
-  const int64_t products = MODE == kDw ? 2 : 1, rows = cdiv(P.m, kBM);
-  if (P.m > kBM && products * cdiv(P.m, 2 * kBM) * cdiv(P.n, most) >= g_pairs)
-    return launch_as<MODE, 2>(P, o, most, nsm, st);
-  const int64_t blocks = int64_t(MODE == kDx ? 2 : 1) * P.nk;
-  int bn = most, split = 0;
-  int64_t best = INT64_MAX;
-  for (int w = most; w >= least; w -= step) {
-    const int64_t cost = cdiv(products * rows * cdiv(P.n, w), nsm) * blocks * block_cost<MODE>(w);
-    if (cost < best) best = cost, bn = w;
-  }
+lora_status launch(FfnArgs& P, const Operands& o, const FfnFit& fit, cudaStream_t st) {
+  const FfnPlan plan = ffn_plan(MODE, P.m, P.n, P.nk, P.piece, P.keep_kind == LORA_KEEP_PACKED8, fit);
+  if (plan.cg == 2) return launch_as<MODE, 2>(P, o, plan.bn, fit, st);
   if constexpr (MODE == kDx) {
-    for (int w = 128; w >= 64; w -= 64) {
-      const int64_t tiles = rows * cdiv(P.n, w), block = block_cost<MODE>(w);
-      const int64_t two = cdiv(tiles, g_splits[0]) * (P.nk * block + kJoinTwo);
-      const int64_t eight = cdiv(tiles, g_splits[1]) * (P.piece * block + kJoinEight + kJoinRow * std::min(P.m, kBM));
-      if (two < best) best = two, split = 2, bn = w;
-      if (eight < best) best = eight, split = 8, bn = w;
-    }
-    if (split == 2) return launch_as<kDx, 1, 2>(P, o, bn, nsm, st);
-    if (split == 8) return launch_as<kDx, 1, 8>(P, o, bn, nsm, st);
+    if (plan.split == 2) return launch_as<kDx, 1, 2>(P, o, plan.bn, fit, st);
+    if (plan.split == 8) return launch_as<kDx, 1, 8>(P, o, plan.bn, fit, st);
   }
-  return launch_as<MODE, 1>(P, o, bn, nsm, st);
+  return launch_as<MODE, 1>(P, o, plan.bn, fit, st);
 }
 
-// How many of the kernel's clusters the device holds at once.
+// How many of the kernel's clusters the device holds at once (0 where it can form none).
 template <class K>
-cudaError_t resident(int* n, K* kernel, unsigned cluster) {
+int resident(K* kernel, unsigned cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster);
   cfg.blockDim = dim3(kGemmThreads);
@@ -199,8 +162,10 @@ cudaError_t resident(int* n, K* kernel, unsigned cluster) {
   attr[0].val.clusterDim = {cluster, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
-  return e == cudaSuccess && *n < 1 ? cudaErrorInvalidConfiguration : e;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
+  cudaGetLastError();                              // (an answer, not an error of a later call)
+  return 0;
 }
 
 template <int MODE, int CG, int SPLIT, int... DEEP>
@@ -213,26 +178,20 @@ cudaError_t set_smem() {
   return e;
 }
 
-template <int MODE>
-cudaError_t prepare() {
-  cudaError_t e = MODE == kFwd ? set_smem<kFwd, 1, 0, 1, 2, 4>() : set_smem<MODE, 1, 0, 1>();
-  if (e != cudaSuccess || (e = set_smem<MODE, 2, 0, 1>()) != cudaSuccess) return e;
-  return resident(&g_pairs, ffn_gemm_kernel<MODE, 2>, 2);
-}
-
-template <int SPLIT>
-cudaError_t prepare_split(int* clusters) {
-  const cudaError_t e = set_smem<kDx, 1, SPLIT, 1, 2, 4>();
-  return e == cudaSuccess ? resident(clusters, ffn_gemm_kernel<kDx, 1, SPLIT>, SPLIT) : e;
-}
-
 }  // namespace
 
-cudaError_t prepare_ffn() {
-  cudaError_t e = prepare_split<2>(&g_splits[0]);
-  if (e != cudaSuccess || (e = prepare_split<8>(&g_splits[1])) != cudaSuccess) return e;
-  if ((e = prepare<kFwd>()) != cudaSuccess || (e = prepare<kDx>()) != cudaSuccess) return e;
-  return prepare<kDw>();
+cudaError_t prepare_ffn(FfnFit* fit) {
+  cudaError_t e;
+  if ((e = set_smem<kFwd, 1, 0, 1, 2, 4>()) != cudaSuccess || (e = set_smem<kDx, 1, 0, 1>()) != cudaSuccess ||
+      (e = set_smem<kDw, 1, 0, 1>()) != cudaSuccess || (e = set_smem<kDx, 1, 2, 1, 2, 4>()) != cudaSuccess ||
+      (e = set_smem<kDx, 1, 8, 1, 2, 4>()) != cudaSuccess || (e = set_smem<kFwd, 2, 0, 1>()) != cudaSuccess ||
+      (e = set_smem<kDx, 2, 0, 1>()) != cudaSuccess || (e = set_smem<kDw, 2, 0, 1>()) != cudaSuccess)
+    return e;
+  fit->pairs = std::min({resident(ffn_gemm_kernel<kFwd, 2>, 2), resident(ffn_gemm_kernel<kDx, 2>, 2),
+                         resident(ffn_gemm_kernel<kDw, 2>, 2)});
+  fit->two = resident(ffn_gemm_kernel<kDx, 1, 2>, 2);
+  fit->eight = resident(ffn_gemm_kernel<kDx, 1, 8>, 8);
+  return cudaSuccess;
 }
 
 }  // namespace mlp
@@ -267,7 +226,7 @@ lora_status lora_gated_ffn_fwd(const void* x, const void* w_gate, const void* w_
   P.keep_kind = keep;
   P.act = act;
   const Operands o{{x, x}, {w_gate, w_up}, M, K, F, K};
-  return launch<kFwd>(P, o, nsm, static_cast<cudaStream_t>(stream));
+  return launch<kFwd>(P, o, ffn_fit(), static_cast<cudaStream_t>(stream));
 }
 
 lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate, const void* w_up, int keep,
@@ -291,6 +250,7 @@ lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate
                ? LORA_OK
                : LORA_ERR_CUDA;
   }
+  const FfnFit fit = ffn_fit();
   const int64_t items = M * (F / 8);
   const dim3 grid(unsigned(cdiv(items, 256 * kDeep)));
   auto grad = [&](auto kernel) {
@@ -308,14 +268,14 @@ lora_status lora_gated_ffn_bwd(const void* dh, const void* x, const void* w_gate
   P.piece = std::max(4, int(cdiv(P.nk, kMaxPieces)));
   P.pieces = int(cdiv(P.nk, P.piece));
   P.out[0] = static_cast<__nv_bfloat16*>(dx);
-  if ((s = launch<kDx>(P, Operands{{dgate, dup}, {w_gate, w_up}, M, F, F, K}, nsm, st)) != LORA_OK || !dw) return s;
+  if ((s = launch<kDx>(P, Operands{{dgate, dup}, {w_gate, w_up}, M, F, F, K}, fit, st)) != LORA_OK || !dw) return s;
   FfnArgs Q{};
   Q.m = int(F);
   Q.n = int(K);
   Q.nk = int(cdiv(M, kBK));
   Q.out[0] = static_cast<__nv_bfloat16*>(dw_gate);
   Q.out[1] = static_cast<__nv_bfloat16*>(dw_up);
-  return launch<kDw>(Q, Operands{{dgate, dup}, {x, x}, M, F, M, K}, nsm, st);
+  return launch<kDw>(Q, Operands{{dgate, dup}, {x, x}, M, F, M, K}, fit, st);
 }
 
 }  // extern "C"

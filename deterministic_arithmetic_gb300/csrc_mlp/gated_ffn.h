@@ -5,9 +5,10 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "ffn_plan.h"
+
 namespace mlp {
 
-constexpr int kFwd = 0, kDx = 1, kDw = 2;          // the kernel's products (gemm.cuh)
 constexpr uint32_t kKindFfn = 16, kSiteFfn = 64;   // status block: kind kKindFfn + product, sites from kSiteFfn
 
 struct FfnArgs {

@@ -47,7 +47,6 @@ namespace mlp {
 
 using namespace lora;
 
-constexpr int kBM = 128, kBK = 64;                 // rows of A and depth of a k-block
 constexpr int kABytes = kBM * kBK * 2;             // 16 KB
 constexpr int kMaxStages = 16;
 constexpr int kRingBytes = 192 * 1024;             // the operand ring

@@ -14,6 +14,7 @@ struct Device {
   bool probed = false, usable = false;
   int nsm = 0;
   uint32_t* status = nullptr;
+  FfnFit fit;
 };
 Device g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -51,7 +52,8 @@ lora_status device_ready(int* nsm) {
       void* p = nullptr;
       if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess || !p) return LORA_ERR_CUDA;
       d.status = static_cast<uint32_t*>(p);
-      if (prepare_pack8_da() != cudaSuccess || prepare_ffn() != cudaSuccess ||
+      d.fit.nsm = n;
+      if (prepare_pack8_da() != cudaSuccess || prepare_ffn(&d.fit) != cudaSuccess ||
           prepare_layer_norm() != cudaSuccess)
         return LORA_ERR_CUDA;
     }
@@ -79,6 +81,13 @@ uint32_t* status_block() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lock(g_mu);
   return g_dev[dev].status;
+}
+
+FfnFit ffn_fit() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FfnFit{};
+  std::lock_guard<std::mutex> lock(g_mu);
+  return g_dev[dev].fit;
 }
 
 bool tensor_map(CUtensorMap* m, const void* ptr, Elem e, int64_t rows, int64_t cols, int64_t ld, int box_cols,

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "../../include/lora_mlp.h"
+#include "ffn_plan.h"
 
 namespace mlp {
 
@@ -38,14 +39,16 @@ bool any_device();
 // Whether p is device (or managed) memory.
 bool in_device_memory(const void* p);
 
-// Raise the shared-memory limits of the kernels (on the current device).
-cudaError_t prepare_ffn();
+// Raise the shared-memory limits of the kernels (on the current device), and find what clusters it holds.
+cudaError_t prepare_ffn(FfnFit* fit);
 cudaError_t prepare_layer_norm();
 cudaError_t prepare_pack8_da();
 
 // The status block of the current device (common.cuh's layout): the operators of this folder run
 // without a workspace of their own to hold one. Valid after device_ready; zero when loaded.
 uint32_t* status_block();
+// What the current device holds of the gated block's clusters. Valid after device_ready.
+FfnFit ffn_fit();
 
 // 2-D row-major map of a tensor [rows][cols] whose rows are `ld` elements apart; `swizzle` bytes
 // (128, 64, 32; 0: none). False: the driver refused it.

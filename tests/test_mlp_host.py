@@ -84,3 +84,42 @@ def test_differences_along_a_gradient_tell_wrong_ones(act):
                  (1, 0.5 * right[1]), (1, (dh * slope).T @ x), (2, 0.5 * right[2]), (2, (dh * p).T @ x), (2, (dh * g).T @ x)):
         print(act, i, off(i, v))
         assert off(i, v) > 2 * 2.0 ** -7, i
+
+
+def ffn_plans(tmp_path, cases):
+    """(CTAs of a pair, CTAs of a split, tile columns) that the library's rule gives for (mode, m, n, nk, piece,
+    whole groups, SMs, pairs, clusters of two, of eight): its header, compiled on the host."""
+    import os
+    import subprocess
+
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "deterministic_arithmetic_gb300", "csrc_mlp")
+    rows = ",".join("{" + ",".join(map(str, c)) + "}" for c in cases)
+    src, exe = tmp_path / "plan.cpp", tmp_path / "plan"
+    src.write_text('#include <cstdio>\n#include "ffn_plan.h"\nint main() { static const int c[][10] = {%s};\n'
+                   'for (auto& v : c) { const mlp::FfnPlan p = mlp::ffn_plan(v[0], v[1], v[2], v[3], v[4], v[5], '
+                   '{v[6], v[7], v[8], v[9]});\nstd::printf("%%d %%d %%d\\n", p.cg, p.split, p.bn); } }\n' % rows)
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    return [tuple(map(int, line.split())) for line in out.splitlines()]
+
+
+def test_products_are_taken_without_clusters_that_the_device_cannot_hold(tmp_path):
+    """A device (or the part of one that a process has) that can form no cluster of eight, of two, or no pair takes
+    the products another way; nothing but the way changes. One that holds them all uses all of them."""
+    sizes = (1, 8, 16, 64, 128, 129, 300, 512, 1300, 4096, 17408)
+    cols = (8, 96, 520, 2048, 5120, 17408)
+    shapes = [(mode, m, n, nk, max(4, -(-nk // 4)), packed) for mode in (0, 1, 2) for m in sizes for n in cols
+              for nk in (1, 8, 80, 272) for packed in ((0, 1) if mode == 0 else (0,))]
+    seen = set()
+    for nsm, pairs, two, eight in ((152, 76, 76, 16), (152, 76, 76, 0), (152, 76, 0, 0), (152, 0, 0, 0), (7, 3, 3, 0), (1, 0, 0, 0)):
+        for (mode, m, n, nk, piece, packed), (cg, split, bn) in zip(
+                shapes, ffn_plans(tmp_path, [s + (nsm, pairs, two, eight) for s in shapes])):
+            assert cg in (1, 2) and split in (0, 2, 8) and (cg == 1 or split == 0) and (mode == 1 or split == 0)
+            assert cg == 1 or pairs
+            assert split != 2 or two
+            assert split != 8 or eight
+            most, step = (128, 32 if packed else 8) if mode == 0 else (256, 64)
+            assert 0 < bn <= most and bn % step == 0 and (cg == 1 or bn == most) and (split == 0 or bn <= 128)
+            if eight:
+                seen.add((mode, cg, split))
+    assert seen == {(0, 1, 0), (0, 2, 0), (1, 1, 0), (1, 2, 0), (1, 1, 2), (1, 1, 8), (2, 1, 0), (2, 2, 0)}
