@@ -164,6 +164,8 @@ __device__ __forceinline__ void acc_free(uint32_t taddr) {
 
 // act(y) = y p and its slope p + y p (1 - p) z', with p = 1 / (1 + exp(-z)): z = y for silu; for gelu in
 // its tanh form 0.5 y (1 + tanh(s)) = y / (1 + exp(-2 s)), z = 2 s = sqrt(8 / pi) (y + 0.044715 y^3).
+// The fast exponential and division, a few units of FP32's last place (the exponential's grow with |z|):
+// every result is rounded to bf16 or to a step of 8 bits, some 2^-9 of it, right after.
 __device__ __forceinline__ float act_p(int act, float y) {
   const float z = act == LORA_ACT_SILU ? y : 1.5957691216057308f * fmaf(0.044715f * y * y, y, y);
   return __fdividef(1.f, 1.f + __expf(-z));        // exp overflowing to infinity gives 0
@@ -619,6 +621,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ffn_gemm_kernel(const __grid_
               g[i] = __uint_as_float(r0[i]);
               v[i] = __uint_as_float(r1[i]);
             }
+            // (A lane reads its own row, 16 bytes at a time: four times the accesses of 64-byte pieces. Their
+            // time does not hide under the MMAs: 4096 x 5120 x 17408 1110 us with deltas, 740 to 795 without.)
             if (P.delta[0] && row < P.m) {
               const float* dg = P.delta[0] + row * P.n + col;
               const float* du = P.delta[1] + row * P.n + col;

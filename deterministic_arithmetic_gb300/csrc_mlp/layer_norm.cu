@@ -11,9 +11,10 @@
 // back only what it copied itself, so the loads of several rows are in flight with
 // no barrier and no registers spent on them; the row's sums take the loop's only
 // barriers. Measured at 8192 x 4096 bf16: 23 us forward, 41 us backward (37 and the
-// partials' sum); loads straight into registers 43 and 65 us; rows brought by bulk
-// copies and mbarriers 31 and 49 us (the copying thread's work a row held up its CTA's
-// barriers).
+// partials' sum). Before the column sums were stored four at a time (8 us of the backward
+// pass) the ways to bring the rows were compared: loads straight into registers 43 and
+// 65 us, bulk copies and mbarriers 31 and 49 (the copying thread's work a row held up its
+// CTA's barriers), this one 23 and 49.
 //
 // The forward pass runs at the memory's rate (5.8 TB/s), and so does the backward pass on
 // FP32 rows (6.1). On bf16 rows the backward pass is bound by a warp's chain a row: 361
@@ -53,7 +54,7 @@ constexpr int kMidWarps = 12;
 constexpr int fwd_ctas(int warps) { return warps == 8 ? 3 : (warps == 12 ? 2 : 1); }
 // Rows a thread has in hand, the current one and those to come. Three leave two CTAs of 256 threads (or
 // one of 512) their shared memory in the backward pass on FP32 rows; more did nothing for bf16 rows either
-// (8192 x 4096, forward and backward: 23.0 and 48.8 us with three, 23.5 and 49.0 with four, 24.7 and 50.0
+// (8192 x 4096, forward and backward: 22.5 and 40.9 us with three, 23.0 and 41.3 with four, 24.2 and 42.5
 // with six).
 constexpr int kStages = 3;
 constexpr int kSMs = 152, kMaxParts = 3 * kSMs;     // partial rows of dw and db (parts_of)
@@ -708,7 +709,8 @@ cudaError_t fwd(const void* x, const void* w, const void* b, int w_type, float e
     return launch_pdl(kernel, grid, dim3(threads), fwd_smem<KIND, VEC>(threads), st, x, w, b, w_type, eps, uint32_t(M),
                       int(N), W, y, mean, rstd);
   };
-  // rows that fill their threads exactly take kernels without the tests of the row's end (31 against 38 us at 8192 x 4096)
+  // rows that fill their threads exactly take kernels without tests of the row's end (8192 x 4096 bf16: 22.5
+  // against 24.1 us, backward 40.6 against 43.9)
   constexpr bool vec = VEC > 2;
   const bool full = vec && N == 32 * kPerThread * W;
   if (built == kBlockWarps)

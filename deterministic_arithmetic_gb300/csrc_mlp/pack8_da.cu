@@ -6,15 +6,16 @@
 // pairwise tree in 256-row chunks, and the chunks' partials by the canonical tree (combine). The values
 // the codes stand for are bf16 values, so the leaves are those of the unpacked x, bit for bit.
 //
-// Bound by HBM in principle (33 / 32 bytes an element of x and little else); in practice by the
-// expansion of the codes, 2.5 instructions each. Work unit = (128 columns, 256 rows); a stage brings 64
+// Bound by HBM in principle (33 / 32 bytes an element of x and little else: 5.2 us at 8192 x 4096, rank 16);
+// in practice by a unit's steps in turn. Of 19.8 us there, 12 are spent with the copies and launches alone
+// (3.5 of it the combine launch, which reads the partials of every unit); the expansion of the codes, 2.5
+// instructions each, adds 3, the MMAs 2. Work unit = (128 columns, 256 rows); a stage brings 64
 // rows of codes (one box, 128-byte swizzle) and of du. Two warps expand a stage, a thread a row of 128
 // codes, into two 64-column bf16 blocks in the layout a TMA copy of x would have left; four such teams
 // work on the four stages of a unit at once (all eight warps on one stage at a time waited out every
 // stage's latencies in turn: 25 us). The tensor core takes both operands transposed (M = 128 columns,
 // N = padded rank, K = 16 rows). At 8192 x 4096, rank 16: 38 us for unpacking x and running the delta's
-// own kernels on it, 19.8 us here with the combine launch; 17 without the expansion, 18 without the MMAs,
-// 12 with the copies and launches alone.
+// own kernels on it, 19.8 us here with the combine launch (rank 32: 23, rank 64: 35).
 //
 // Warps: 0 copies, 1 issues the MMAs, 2..9 add the leaves, 10..17 expand.
 #include "../csrc/common.cuh"

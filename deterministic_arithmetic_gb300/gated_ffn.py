@@ -5,7 +5,7 @@ projections, the activation and the product in one kernel; the LoRA deltas of th
 enter inside the activation (``delta_gate``, ``delta_up``: the outputs of ``lora_delta_fwd``).
 ``gated_ffn_bwd`` returns ``(dx, dgate, dup, dw_gate, dw_up)``; ``dgate`` and ``dup`` are also the
 ``dy`` of the two deltas' backward passes. Every call takes ``stream=`` (default: the current stream).
-There is no fallback.
+No autograd graph records them. There is no fallback.
 """
 from __future__ import annotations
 

@@ -3,8 +3,8 @@
 ``layer_norm_fwd(x, weight, bias)`` returns ``(y, mean, rstd)``; ``layer_norm_bwd(dy, x, weight,
 mean, rstd)`` returns ``(dx, dw, db)`` and takes ``x`` as a tensor or as its 8-bit checkpoint
 (``pack8.Packed8``). A row's results are the same bits in any batch; dw and db are the same bits
-in every rerun. Every call takes ``stream=`` (default: the current stream). There is no fallback:
-without the library or off a GB300 the calls raise.
+in every rerun. Every call takes ``stream=`` (default: the current stream). No autograd graph records
+them. There is no fallback: without the library or off a GB300 the calls raise.
 """
 from __future__ import annotations
 

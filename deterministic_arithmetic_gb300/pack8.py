@@ -4,7 +4,7 @@ packed activations of ``include/lora_mlp.h``).
 A ``Packed8`` holds int8 codes and one scale byte per group of 32 elements of a row; a code times
 its power-of-two step is a bf16 value exactly, so a backward pass from the checkpoint gives bit for
 bit what it gives for the unpacked tensor. Every call takes ``stream=`` (default: the current
-stream). There is no fallback.
+stream). No autograd graph records them. There is no fallback.
 """
 from __future__ import annotations
 
