@@ -1,4 +1,4 @@
-"""What the Python modules over include/lora_mlp.h share: the compiled binding ``_mlp``, entry points of
+"""What the Python modules over include/lora_mlp.h and include/lora_base8.h share: the compiled binding ``_mlp``, entry points of
 the C ABI for what needs no tensors, and the choice of stream."""
 from __future__ import annotations
 
@@ -30,9 +30,10 @@ class _Binding:
     def __getattr__(self, name):
         _ld.library()
         from . import _mlp
+        from .block8 import Block8
         from .pack8 import Packed8
 
-        _mlp.setup(Packed8, _ld.LoraDeltaError)
+        _mlp.setup(Packed8, Block8, _ld.LoraDeltaError)
         for f in dir(_mlp):
             if not f.startswith("_"):
                 setattr(self, f, getattr(_mlp, f))

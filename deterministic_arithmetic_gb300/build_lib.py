@@ -1,5 +1,5 @@
 """Builds ``liblora_delta.so`` (the C ABI + sm_103a kernels) in-tree with nvcc, and ``_mlp.so``, the
-compiled Python binding of include/lora_mlp.h, with the host compiler.
+compiled Python binding of include/lora_mlp.h and include/lora_base8.h, with the host compiler.
 
 Each translation unit compiles in its own nvcc process (in parallel), then
 they are linked into one shared library next to this file. Only sm_103a code
@@ -16,6 +16,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 CSRC_MLP = os.path.join(HERE, "csrc_mlp")     # the MLP-block operators (include/lora_mlp.h)
+CSRC_BASE8 = os.path.join(HERE, "csrc_base8") # 8-bit base and distillation (include/lora_base8.h)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "liblora_delta.so")
 BINDING = os.path.join(HERE, "_mlp.so")
@@ -23,6 +24,7 @@ BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["api.cu", "down.cu", "up.cu", "fwd_fused.cu", "fwd_cluster.cu", "bwd_cluster.cu", "dxda.cu", "wgrad.cu", "dy.cu", "rows.cu", "combine.cu", "noalloc.cu",
            "dvf32.cu", "exact.cu"]
 SOURCES_MLP = ["host.cu", "layer_norm.cu", "pack8.cu", "pack8_da.cu", "gated_ffn.cu"]
+SOURCES_BASE8 = ["block8.cu", "linear.cu", "distill.cu"]
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", *GENCODE]
 
@@ -33,7 +35,7 @@ def nvcc() -> str:
 
 
 def _deps() -> list[str]:
-    return [os.path.join(d, f) for d in (CSRC, CSRC_MLP, INCLUDE) for f in os.listdir(d)]
+    return [os.path.join(d, f) for d in (CSRC, CSRC_MLP, CSRC_BASE8, INCLUDE) for f in os.listdir(d)]
 
 
 def up_to_date(lib: str = LIB) -> bool:
@@ -95,6 +97,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple = (), l
         return obj
 
     sources = [os.path.join(CSRC, f) for f in SOURCES] + [os.path.join(CSRC_MLP, f) for f in SOURCES_MLP]
+    sources += [os.path.join(CSRC_BASE8, f) for f in SOURCES_BASE8]
     bind = lib == LIB                  # a library built elsewhere (other flags) has no binding of its own
     with ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         binding = ex.submit(_binding_object) if bind else None

@@ -1,0 +1,407 @@
+// linear.cuh -- the tensor-core kernel of the products with weights in 8-bit blocks: e4m3 operands by TMA
+// into swizzled shared memory, tcgen05 MMAs (kind::f8f6f4) into FP32 accumulators in TMEM.
+//   kLinFwd  y = x w^T     both operands lie along the reduction (K-major)
+//   kLinBwd  dx = dy w     the weight's rows lie across it (MN-major): one copy of the codes serves both passes
+//
+// A block of 128 of the reduction has a scale of its own for each row and each 128 columns, so its sum is
+// an accumulator of its own: four MMAs of depth 32 from a cleared start, which the epilogue warps then
+// multiply by the scales' product and add to the output's FP32 sum in registers, one fma an element, blocks in
+// order. An output's bits depend on its row, its column and the reduction's length only: not on the
+// tile it falls into, nor on the batch.
+#pragma once
+
+#include "../csrc_mlp/gemm.cuh"
+#include "linear.h"
+
+namespace mlp {
+
+constexpr int kLinBK = 128;                        // depth of a k-block: a block of the scales
+constexpr int kLinSmemRing = 200 * 1024;           // the operand ring
+constexpr int kLinStages = 16;
+constexpr int kLinSlots = 4;                       // accumulator slots at most
+// Behind the ring, 2 KB of each epilogue warp; the MMAs' reads past a short batch's rows of A (whose products nobody
+// reads) stay inside.
+constexpr int kLinSlack = 16 * 1024;
+constexpr size_t kLinSmem = kLinSmemRing + kLinSlack + 1024 + (2 * kLinStages + 2 * kLinSlots + 2) * 8 + 16;
+static_assert(kLinSmem < 227 * 1024, "shared memory of a CTA");
+
+// Four warps to load, issue and idle, eight for the epilogue. Of 256-column tiles an epilogue thread holds 128 sums:
+// it takes registers that the first four warps give up (shares of 56 and 224 of the launch's 168 a thread).
+constexpr int kLinThreads = 384, kLinRegs = 168, kLinRegsFew = 56, kLinRegsMany = 224;
+static_assert(128 * kLinRegsFew + 256 * kLinRegsMany <= kLinThreads * kLinRegs, "the shares fit the launch's registers");
+
+// The bounded waits of waits.cuh, without a call: a kernel that shares out its registers can hold none.
+__device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, Abort ab, uint32_t site, uint64_t limit,
+                                                bool honour_abort) {
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (honour_abort && *ab.flag) return false;
+    if (mbar_test_cluster(bar, parity)) return true;
+    if (global_ns() - t0 > limit) {
+      *ab.flag = 1u;
+      if (ab.status) atomicCAS(ab.status, 0u, (site << 8) | kDevTimeout);   // the first code stays
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
+  return completed(bar, parity) || lin_wait_longer(bar, parity, ab, site, ab.limit_ns, true);
+}
+__device__ __forceinline__ void lin_drain(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
+  if (!completed(bar, parity)) lin_wait_longer(bar, parity, ab, site, kDrainLimitNs, false);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: e4m3 A and B (0), FP32 D, A K-major, B K-major or (b_mn) MN-major.
+__device__ __forceinline__ uint32_t idesc_f8(int M, int N, int b_mn) {
+  return (1u << 4) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 16 || N == 32, "");
+  if constexpr (N == 32) tmem_ld32(taddr, r);
+  else tmem_ld16(taddr, r);
+}
+
+// The tile of a unit (gemm.cuh's order: groups of up to 16 row tiles, row tiles fastest).
+struct LinUnit {
+  int tm, col, bn;
+};
+template <int CG>
+__device__ __forceinline__ LinUnit lin_unit(const LinArgs& P, int u) {
+  int tile = u, half = -1;
+  if (CG == 2 && u >= P.whole) {
+    tile = P.whole + (u - P.whole) / 2;
+    half = (u - P.whole) & 1;
+  }
+  LinUnit w;
+  const int group = tile / (16 * P.tiles_n), m0 = 16 * group;
+  const int gm = min(16, P.tiles_m - m0);
+  const int r = tile - 16 * group * P.tiles_n;
+  w.tm = m0 + r % gm;
+  w.bn = half < 0 ? P.bn : P.bn / 2;
+  w.col = (r / gm) * P.bn + (half == 1 ? w.bn : 0);
+  return w;
+}
+
+// 32 rows by 16 columns of the warp (lane l holds row row0 + l's), plus delta, to the output, by way of the warp's
+// 2 KB of shared memory: 4 lanes a row then read and write whole sectors. 16-byte pieces of a row are permuted by the
+// row's bits 1 and 2, so that neither way meets a bank twice. Rows past m and columns past `end` are left alone.
+__device__ __forceinline__ void lin_store16(const LinArgs& P, uint32_t box, int64_t row0, int col, int end, const float* acc,
+                                            uint32_t lane) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)),
+                 "f"(acc[4 * j]), "f"(acc[4 * j + 1]), "f"(acc[4 * j + 2]), "f"(acc[4 * j + 3])
+                 : "memory");
+  __syncwarp();
+  const int c = col + 4 * int(lane & 3);
+#pragma unroll 4
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + int(lane >> 2);
+    const int64_t row = row0 + r;
+    float v[4];
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(box + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4))
+                 : "memory");
+    if (row >= P.m || c >= end) continue;
+    const int64_t at = row * P.n + c;
+    if (P.vec) {                                   // the row's columns are whole vectors: so is c's
+      if (P.delta) {
+        const float4 d = __ldcs(reinterpret_cast<const float4*>(P.delta + at));
+        v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
+      }
+      if (P.out_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(P.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(P.out) + at) =
+            make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < end) {
+          const float y = P.delta ? v[e] + P.delta[at + e] : v[e];
+          if (P.out_f32) static_cast<float*>(P.out)[at + e] = y;
+          else static_cast<__nv_bfloat16*>(P.out)[at + e] = __float2bfloat16_rn(y);
+        }
+    }
+  }
+}
+
+// W: columns of an accumulator (bn rounded up to a power of two); DEEP: k-blocks of a stage, each with an
+// accumulator of its own in the slot.
+template <int MODE, int CG, int W, int DEEP>
+__global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_constant__ LinArgs P, uint32_t* status) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kLinSmemRing + kLinSlack);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (kLinStages + s); };
+  auto tfull = [&](int b) { return bar0 + 8u * (2 * kLinStages + b); };
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * kLinStages + kLinSlots + b); };
+  const uint32_t drain = bar0 + 8u * (2 * kLinStages + 2 * kLinSlots);
+  const uint32_t never = drain + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kLinStages + 2 * kLinSlots + 2);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  constexpr int kSlots = 512 / (W * DEEP) < kLinSlots ? 512 / (W * DEEP) : kLinSlots;
+  static_assert(kSlots >= 2 && (W >= 32 && W <= 256), "TMEM columns");
+  static_assert(CG == 1 || W == 256, "pairs take tiles of 256 columns");
+
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int rank = CG == 2 ? int(cluster_rank()) : 0;       // of a pair: 0 issues the MMAs
+  const int stages = P.stages, stage_bytes = DEEP * P.block_bytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kLinStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < kSlots; ++b) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), CG * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(never, 1);
+    *abort_flag = 0u;
+    mbar_fence_init();
+    prefetch_map(&P.a);
+    prefetch_map(&P.b);
+  }
+  // (a pair meets before its joint TMEM allocation and after its freeing, as in gemm.cuh)
+  __syncwarp();
+  if constexpr (CG == 2) cluster_sync_all();
+  if (warp == 1) acc_alloc<CG>(smem_u32(tmem_slot));
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync_all();
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const Abort ab = make_abort(abort_flag, status);
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  // a copied piece of MN-major B: kChunk columns of 128 rows of the weight, its swizzle span
+  constexpr int kChunk = W < 128 ? W : 128;
+
+  if (warp < 4) {
+  if constexpr (W == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLinRegsFew));
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer (gemm.cuh's)
+    const bool one = elect_one();
+    if (stall_requested(status, kKindLinear + MODE) && one) lin_wait_longer(never, 0u, ab, kSiteLinear + 1, ab.limit_ns / 4, true);   // test hook
+    __syncwarp();
+    const uint64_t pa = P.tiles_n > 1 ? policy_evict_last() : policy_normal(), pb = policy_normal();
+    const uint32_t full0 = CG == 2 ? peer_addr(full(0), 0) : full(0);
+    int idx = 0;
+    uint32_t phase = 0, issued = 0;
+    bool ready = true;
+    for (int u = first; u < P.total; u += step) {
+      const LinUnit w = lin_unit<CG>(P, u);
+      const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
+      const int col0 = w.col + rank * (w.bn / 2);          // and columns (of a pair, half of the tile's)
+      for (int kb = 0; kb < P.nk; kb += DEEP) {
+        if (!__all_sync(0xffffffffu, ready || lin_wait(empty(idx), phase ^ 1u, ab, kSiteLinear + 2))) goto given_up;
+        const uint32_t st0 = base + uint32_t(idx) * stage_bytes, bar = full0 + 8u * idx, here = full(idx);
+        if (++idx == stages) idx = 0, phase ^= 1u;
+        ready = completed(empty(idx), phase ^ 1u);
+        ++issued;
+        if (one) {
+          if (rank == 0) mbar_expect_tx(here, uint32_t(CG * (DEEP == 1 ? 1 : min(DEEP, P.nk - kb)) * P.block_bytes));
+#pragma unroll
+          for (int k = 0; k < DEEP; ++k) {
+            if (k > 0 && kb + k >= P.nk) break;
+            const uint32_t st = st0 + k * P.block_bytes, sb = st + P.a_bytes;
+            const int k0 = (kb + k) * kLinBK;
+            load2d<CG>(st, &P.a, bar, k0, row0, pa);
+            if constexpr (MODE == kLinFwd) {
+              load2d<CG>(sb, &P.b, bar, k0, col0, pb);
+            } else {
+#pragma unroll 1
+              for (int j = 0; j < P.bn / CG; j += kChunk) load2d<CG>(sb + j * kLinBK, &P.b, bar, col0 + j, k0, pb);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  given_up:
+    // nothing may reach this CTA's shared memory once it has gone (gemm.cuh)
+    for (uint32_t s = 0; s < uint32_t(stages) && s < issued; ++s) {
+      const uint32_t parity = ((issued - 1u - s) / stages) & 1u;       // of the stage's last use
+      if (rank == 0) lin_drain(full(s), parity, ab, kSiteLinear + 3);
+      if (!*ab.flag) lin_wait(empty(s), parity, ab, kSiteLinear + 8);
+    }
+    if (*ab.flag)
+      for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainLimitNs;) {
+      }
+    __syncwarp();
+  } else if (warp == 1) {
+    // --------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      // K-major operands step 32 bytes inside the swizzle span per 32 of the reduction; MN-major ones 32 rows.
+      constexpr uint32_t kSpan = MODE == kLinFwd ? 128 : kChunk, a_step = 32u, b_step = MODE == kLinFwd ? 32u : 32u * kSpan;
+      const uint64_t a0 = smem_desc(base, 16u, 1024u, kLayoutSW128);
+      const uint64_t b0 = smem_desc(base + P.a_bytes, MODE == kLinFwd ? 16u : kLinBK * kSpan, 8u * kSpan, layout_for_span(kSpan));
+      const bool one = elect_one();
+      int idx = 0, buf = 0;
+      uint32_t phase = 0, tphase = 0;
+      bool ready = false, ok = true;
+      for (int u = first; u < P.total && ok; u += step) {
+        const uint32_t idesc = idesc_f8(CG * kBM, lin_unit<CG>(P, u).bn, MODE == kLinBwd);
+        for (int kb = 0; kb < P.nk; kb += DEEP) {
+          ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4) &&
+                                           (ready || lin_wait(full(idx), phase, ab, kSiteLinear + 5)));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + buf * (W * DEEP), off0 = uint32_t(idx) * stage_bytes, used = empty(idx), done = tfull(buf);
+          if (++idx == stages) idx = 0, phase ^= 1u;
+          if (++buf == kSlots) buf = 0, tphase ^= 1u;
+          ready = completed(full(idx), phase);
+          if (one) {
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) {
+              if (k > 0 && kb + k >= P.nk) break;
+              const uint32_t off = off0 + k * P.block_bytes;
+#pragma unroll
+              for (int j = 0; j < kLinBK / 32; ++j)
+                mma_f8<CG>(d + k * W, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc, j ? 1u : 0u);
+            }
+            commit<CG>(used);
+            commit<CG>(done);
+          }
+          __syncwarp();
+        }
+      }
+      if (one) commit_here<CG>(drain);
+      __syncwarp();
+      lin_drain(drain, 0u, ab, kSiteLinear + 6);
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    if constexpr (W == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLinRegsMany));
+    // A warp has its quarter of the rows and half of the tile's columns, in chunks of C.
+    constexpr int C = W >= 64 ? 32 : 16, kChunks = W / 2 / C;
+    constexpr int kScales = W == 256 ? 1 : (W == 64 ? 2 : kChunks);    // the weight's scales of a warp's columns and k-block
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lanes = uint32_t(q * 32) << 16;
+    int buf = 0;
+    uint32_t tphase = 0;
+    for (int u = first; u < P.total; u += step) {
+      const LinUnit w = lin_unit<CG>(P, u);
+      const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32, row = row0 + lane;
+      const int off = half * (W == 256 ? w.bn / 2 : W / 2);          // its first column in the tile
+      const bool rows = row0 < P.m;
+      const float* sa = P.sa + min(row, int64_t(P.m) - 1) * P.nk;
+      // scale e of a block: of columns 32 e (or, of 64-column tiles, whose width need not be whole chunks, 16 e) on
+      const float* sb[kScales];
+#pragma unroll
+      for (int e = 0; e < kScales; ++e) sb[e] = P.sb + min(w.col + off + e * (W == 64 ? 16 : C), P.n - 1) / 128 * P.sb_out;
+      float acc[kChunks * C];
+#pragma unroll
+      for (int i = 0; i < kChunks * C; ++i) acc[i] = 0.f;
+      bool ok = true;
+      // the scales of the next four blocks
+      float na[4], nb[4][kScales];
+      auto fetch = [&](int kb) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (kb + k < P.nk) {
+            na[k] = __ldg(sa + kb + k);
+#pragma unroll
+            for (int e = 0; e < kScales; ++e) nb[k][e] = __ldg(sb[e] + (kb + k) * P.sb_red);
+          }
+      };
+      fetch(0);
+      for (int kb0 = 0; kb0 < P.nk; kb0 += 4) {
+        float s[4][kScales];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < kScales; ++e) s[k][e] = na[k] * nb[k][e];
+        if (kb0 + 4 < P.nk) fetch(kb0 + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (kb0 + k >= P.nk) break;
+          if (k % DEEP == 0) {
+            ok = __all_sync(0xffffffffu, lin_wait(tfull(buf), tphase, ab, kSiteLinear + 7)) && ok;
+            tc_fence_after();
+          }
+          if (ok && rows) {
+            const uint32_t at = tmem + buf * (W * DEEP) + (k % DEEP) * W + lanes + off;
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+              if (W == 256 && i * C >= w.bn / 2) break;      // half a tile
+              uint32_t r[C];
+              tmem_ldn(at + i * C, r);
+              tmem_ld_wait();
+              reg_fence(r);
+#pragma unroll
+              for (int e = 0; e < C; ++e) {
+                const float f = s[k][W == 256 ? 0 : (W == 64 ? e / 16 : i)];
+                acc[i * C + e] = fmaf(f, __uint_as_float(r[e]), acc[i * C + e]);
+              }
+            }
+          }
+          if (k % DEEP == DEEP - 1 || kb0 + k == P.nk - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (ok && lane == 0) {
+              if constexpr (CG == 2) mbar_arrive_peer(peer_addr(tempty(buf), 0));
+              else mbar_arrive(tempty(buf));
+            }
+            if (++buf == kSlots) buf = 0, tphase ^= 1u;
+          }
+        }
+      }
+      if (ok && rows) {
+        const int end = min(P.n, w.col + w.bn);
+        const uint32_t box = base + kLinSmemRing + (warp - 4) * 2048;
+#pragma unroll
+        for (int i = 0; i < kChunks * C; i += 16)
+          if (off + i < w.bn && (W != 256 || i < w.bn / 2)) lin_store16(P, box, row0, w.col + off + i, end, acc + i, lane);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync_all();
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    acc_free<CG>(tmem);
+  }
+  __syncwarp();
+  if constexpr (CG == 2) cluster_sync_all();
+}
+
+}  // namespace mlp

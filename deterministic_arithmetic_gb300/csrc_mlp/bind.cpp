@@ -1,4 +1,4 @@
-// bind.cpp -- the Python binding of include/lora_mlp.h: argument checks, outputs and workspaces as
+// bind.cpp -- the Python binding of include/lora_mlp.h and include/lora_base8.h: argument checks, outputs and workspaces as
 // torch tensors, the call on the current stream. Argument marshalling only; the kernels do the work.
 //
 // A compiled module rather than ctypes, because the small calls of these operators are bound by the
@@ -15,16 +15,16 @@
 
 #include <sstream>
 
-#include "../../include/lora_mlp.h"
+#include "../../include/lora_base8.h"
 
 namespace {
 
 using at::Tensor;
 using Shape = std::vector<int64_t>;
-constexpr auto BF16 = at::kBFloat16, F32 = at::kFloat, U8 = at::kByte, I8 = at::kChar;
+constexpr auto BF16 = at::kBFloat16, F32 = at::kFloat, U8 = at::kByte, I8 = at::kChar, F8 = at::kFloat8_e4m3fn, I64 = at::kLong, I32 = at::kInt;
 
-PyObject *packed_type = nullptr, *error_type = nullptr;      // Packed8 and LoraDeltaError, given by setup()
-PyObject *codes_name = nullptr, *scales_name = nullptr, *cols_name = nullptr;
+PyObject *packed_type = nullptr, *block_type = nullptr, *error_type = nullptr;   // Packed8, Block8 and LoraDeltaError, given by setup()
+PyObject *codes_name = nullptr, *scales_name = nullptr, *cols_name = nullptr, *tile_name = nullptr;
 
 struct Raised {};                                             // a Python error is set
 
@@ -53,7 +53,7 @@ const Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
-const char* dtype_name(at::ScalarType t) { return t == BF16 ? "torch.bfloat16" : t == F32 ? "torch.float32" : t == U8 ? "torch.uint8" : t == I8 ? "torch.int8" : c10::toString(t); }
+const char* dtype_name(at::ScalarType t) { return t == BF16 ? "torch.bfloat16" : t == F32 ? "torch.float32" : t == U8 ? "torch.uint8" : t == I8 ? "torch.int8" : t == F8 ? "torch.float8_e4m3fn" : t == I64 ? "torch.int64" : t == I32 ? "torch.int32" : c10::toString(t); }
 
 [[noreturn]] void refuse(const Tensor& t, const char* name, const char* want, c10::IntArrayRef shape, int dev) {
   std::ostringstream s;
@@ -375,12 +375,152 @@ PyObject* gated_ffn_bwd(PyObject* const* a) {
   return tuple(wrap(dx), wrap(dg), wrap(du), grads ? wrap(dwg) : none(), grads ? wrap(dwu) : none());
 }
 
-// setup(Packed8, LoraDeltaError)
+// ------------------------------------------ 8-bit blocks, their products, distillation
+
+// A Block8: its codes and scales, its sizes, the rows of a block and its device.
+struct Block {
+  void* codes;
+  float* scales;
+  int64_t rows, cols, tile;
+  int dev;
+};
+int64_t int_attr(PyObject* o, PyObject* name) {
+  Ref v(PyObject_GetAttr(o, name));
+  return integer(v.p);
+}
+int64_t code_ld(int64_t cols) { return (cols + 15) / 16 * 16; }
+int64_t blocks(int64_t n, int64_t of) { return (n + of - 1) / of; }
+// The parts of a Block8, checked against its own sizes; of device `dev` and of the given size and tile where those are not -1.
+Block check_block(PyObject* o, const char* name, int64_t rows, int64_t cols, int64_t tile, int dev) {
+  if (Py_TYPE(o) != reinterpret_cast<PyTypeObject*>(block_type)) raise(PyExc_TypeError, std::string(name) + " must be a Block8");
+  Block b;
+  b.cols = int_attr(o, cols_name);
+  b.tile = int_attr(o, tile_name);
+  if (b.tile != 1 && b.tile != 128) raise(PyExc_ValueError, std::string(name) + ": expected blocks of 1 or 128 rows, got " + std::to_string(b.tile));
+  if (tile >= 0 && b.tile != tile) raise(PyExc_ValueError, std::string(name) + ": expected blocks of " + std::to_string(tile) + (tile == 1 ? " row, got " : " rows, got ") + std::to_string(b.tile));
+  if (b.cols < 1 || (cols >= 0 && b.cols != cols)) raise(PyExc_ValueError, std::string(name) + ": expected " + (cols >= 0 ? std::to_string(cols) : "1 or more") + " columns, got " + std::to_string(b.cols));
+  Ref c(PyObject_GetAttr(o, codes_name)), s(PyObject_GetAttr(o, scales_name));
+  const std::string cn = std::string(name) + ".codes";
+  const Tensor& ct = tensor(c.p, cn.c_str());
+  int64_t ld;
+  if (dev < 0) dev = first(ct, cn.c_str(), &b.rows, &ld);
+  else b.rows = ct.dim() ? ct.size(0) : 0;
+  if (rows >= 0) b.rows = rows;
+  b.dev = dev;
+  b.codes = check(ct, cn.c_str(), {b.rows, code_ld(b.cols)}, F8, dev);
+  b.scales = static_cast<float*>(check(s.p, (std::string(name) + ".scales").c_str(), {blocks(b.rows, b.tile), blocks(b.cols, 128)}, F32, dev));
+  return b;
+}
+// A new Block8; *b its parts.
+PyObject* new_block(int64_t rows, int64_t cols, int64_t tile, int dev, Block* b) {
+  const Tensor c = empty({rows, code_ld(cols)}, F8, dev), s = empty({blocks(rows, tile), blocks(cols, 128)}, F32, dev);
+  *b = {c.data_ptr(), s.data_ptr<float>(), rows, cols, tile, dev};
+  Ref a(wrap(c)), t(wrap(s)), n(PyLong_FromLongLong(cols)), r(PyLong_FromLongLong(tile));
+  PyObject* args[] = {a.p, t.p, n.p, r.p};
+  PyObject* made = PyObject_Vectorcall(block_type, args, 4, nullptr);
+  if (!made) throw Raised{};
+  return made;
+}
+
+PyObject* block8(PyObject* const* a) {                        // x, tile, out
+  const Tensor& x = tensor(a[0], "x");
+  int64_t M, K;
+  int xt;
+  const int dev = first(x, "x", &M, &K);
+  const void* xp = check_either(x, "x", x.sizes(), dev, &xt);
+  const int64_t tile = integer(a[1]);
+  if (tile != 1 && tile != 128) raise(PyExc_ValueError, "tile: expected 1 or 128, got " + std::to_string(tile));
+  Block b;
+  if (a[2] != Py_None) b = check_block(a[2], "out", M, K, tile, dev), Py_INCREF(a[2]);
+  Ref o(a[2] == Py_None ? new_block(M, K, tile, dev, &b) : a[2]);
+  done(lora_block8(xp, xt, int(tile), M, K, b.codes, b.scales, stream(dev)), "lora_block8");
+  return o.release();
+}
+
+PyObject* unblock8(PyObject* const* a) {                      // p, dtype code, out
+  const Block b = check_block(a[0], "p", -1, -1, -1, -1);
+  const int code = int(integer(a[1]));
+  const Tensor o = out(a[2], "out", {b.rows, b.cols}, code == LORA_BF16 ? BF16 : F32, b.dev);
+  done(lora_unblock8(b.codes, b.scales, int(b.tile), b.rows, b.cols, o.data_ptr(), code, stream(b.dev)), "lora_unblock8");
+  return wrap(o);
+}
+
+// x or dy, w, delta, dtype code, y or dx. The weight is [N][K]: x has K columns and y N, dy N and dx K.
+template <bool BWD>
+PyObject* block8_linear(PyObject* const* a) {
+  const char *in = BWD ? "dy" : "x", *res = BWD ? "dx" : "y";
+  const Block x = check_block(a[0], in, -1, -1, 1, -1), w = check_block(a[1], "w", -1, -1, 128, x.dev);
+  const int64_t M = x.rows, N = w.rows, K = w.cols, cols = BWD ? K : N;
+  if (x.cols != (BWD ? N : K))
+    raise(PyExc_ValueError, std::string(in) + ": expected " + std::to_string(BWD ? N : K) + " columns, as w has " + (BWD ? "rows" : "columns") + ", got " + std::to_string(x.cols));
+  const float* delta = a[2] == Py_None ? nullptr : static_cast<const float*>(check(a[2], "delta", {M, cols}, F32, x.dev));
+  const int code = int(integer(a[3]));
+  const Tensor y = out(a[4], res, {M, cols}, code == LORA_BF16 ? BF16 : F32, x.dev);
+  done((BWD ? lora_block8_linear_bwd : lora_block8_linear_fwd)(x.codes, x.scales, w.codes, w.scales, delta, M, K, N, y.data_ptr(), code, stream(x.dev)),
+       BWD ? "lora_block8_linear_bwd" : "lora_block8_linear_fwd");
+  return wrap(y);
+}
+
+// ids [M][top], int64 or int32; *bytes an element's.
+const void* check_ids(const Tensor& t, c10::IntArrayRef shape, int dev, int* bytes) {
+  if (t.scalar_type() != I64 && t.scalar_type() != I32) refuse(t, "ids", "torch.int64 or torch.int32", shape, dev);
+  *bytes = t.scalar_type() == I64 ? 8 : 4;
+  return check(t, "ids", shape, t.scalar_type(), dev);
+}
+
+PyObject* distill_topk_fwd(PyObject* const* a) {  // logits, ids, teacher, temperature, teacher_lse, weight, loss, probs, stats
+  const Tensor &z = tensor(a[0], "logits"), &ids = tensor(a[1], "ids"), &teacher = tensor(a[2], "teacher");
+  int64_t M, V;
+  int type, tt, bytes;
+  const int dev = first(z, "logits", &M, &V);
+  const void* zp = check_either(z, "logits", z.sizes(), dev, &type);
+  const int64_t top = ids.dim() == 2 ? ids.size(1) : 0;
+  const void* ip = check_ids(ids, {M, top}, dev, &bytes);
+  const void* tp = check_either(teacher, "teacher", {M, top}, dev, &tt);
+  const float temperature = float(number(a[3]));
+  const float* lse = a[4] == Py_None ? nullptr : static_cast<const float*>(check(a[4], "teacher_lse", {M}, F32, dev));
+  const float* w = a[5] == Py_None ? nullptr : static_cast<const float*>(check(a[5], "weight", {M}, F32, dev));
+  const Tensor loss = out(a[6], "loss", {M}, F32, dev), probs = out(a[7], "probs", {M, top}, F32, dev);
+  const Tensor stats = out(a[8], "stats", {M, 4}, F32, dev);
+  done(lora_distill_topk_fwd(zp, type, ip, bytes, tp, tt, lse, w, temperature, M, V, top, loss.data_ptr<float>(),
+                             probs.data_ptr<float>(), stats.data_ptr<float>(), stream(dev)), "lora_distill_topk_fwd");
+  return tuple(wrap(loss), wrap(probs), wrap(stats));
+}
+
+PyObject* distill_topk_bwd(PyObject* const* a) {  // dloss, logits, ids, probs, stats, temperature, block8, dlogits
+  const Tensor &z = tensor(a[1], "logits"), &ids = tensor(a[2], "ids");
+  int64_t M, V;
+  int type, bytes;
+  const int dev = first(z, "logits", &M, &V);
+  const void* zp = check_either(z, "logits", z.sizes(), dev, &type);
+  const float* dl = static_cast<const float*>(check(a[0], "dloss", {M}, F32, dev));
+  const int64_t top = ids.dim() == 2 ? ids.size(1) : 0;
+  const void* ip = check_ids(ids, {M, top}, dev, &bytes);
+  const float* pp = static_cast<const float*>(check(a[3], "probs", {M, top}, F32, dev));
+  const float* sp = static_cast<const float*>(check(a[4], "stats", {M, 4}, F32, dev));
+  const float temperature = float(number(a[5]));
+  const int as_blocks = PyObject_IsTrue(a[6]);
+  if (as_blocks < 0) throw Raised{};
+  Block b{};
+  if (!as_blocks) {
+    const Tensor dz = out(a[7], "dlogits", z.sizes(), z.scalar_type(), dev);
+    done(lora_distill_topk_bwd(dl, zp, type, ip, bytes, pp, sp, temperature, M, V, top, dz.data_ptr(), nullptr, stream(dev)),
+         "lora_distill_topk_bwd");
+    return wrap(dz);
+  }
+  if (a[7] != Py_None) b = check_block(a[7], "dlogits", M, V, 1, dev), Py_INCREF(a[7]);
+  Ref o(a[7] == Py_None ? new_block(M, V, 1, dev, &b) : a[7]);
+  done(lora_distill_topk_bwd(dl, zp, type, ip, bytes, pp, sp, temperature, M, V, top, b.codes, b.scales, stream(dev)),
+       "lora_distill_topk_bwd");
+  return o.release();
+}
+
+// setup(Packed8, Block8, LoraDeltaError)
 PyObject* setup(PyObject* const* a) {
-  Py_INCREF(a[0]);
-  Py_INCREF(a[1]);
+  for (int i = 0; i < 3; ++i) Py_INCREF(a[i]);
   Py_XSETREF(packed_type, a[0]);
-  Py_XSETREF(error_type, a[1]);
+  Py_XSETREF(block_type, a[1]);
+  Py_XSETREF(error_type, a[2]);
   return none();
 }
 
@@ -407,7 +547,9 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {
     method<layer_norm_fwd, 7>("layer_norm_fwd"), method<layer_norm_bwd, 10>("layer_norm_bwd"), method<pack8, 2>("pack8"),
     method<unpack8, 3>("unpack8"), method<pack8_da, 4>("pack8_da"), method<lora_delta_bwd_packed8, 11>("lora_delta_bwd_packed8"),
-    method<gated_ffn_fwd, 10>("gated_ffn_fwd"), method<gated_ffn_bwd, 13>("gated_ffn_bwd"), method<setup, 2>("setup"),
+    method<gated_ffn_fwd, 10>("gated_ffn_fwd"), method<gated_ffn_bwd, 13>("gated_ffn_bwd"), method<block8, 3>("block8"),
+    method<unblock8, 3>("unblock8"), method<block8_linear<false>, 5>("block8_linear_fwd"), method<block8_linear<true>, 5>("block8_linear_bwd"),
+    method<distill_topk_fwd, 9>("distill_topk_fwd"), method<distill_topk_bwd, 8>("distill_topk_bwd"), method<setup, 3>("setup"),
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mlp", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
@@ -417,5 +559,6 @@ PyMODINIT_FUNC PyInit__mlp() {
   codes_name = PyUnicode_InternFromString("codes");
   scales_name = PyUnicode_InternFromString("scales");
   cols_name = PyUnicode_InternFromString("cols");
-  return codes_name && scales_name && cols_name ? PyModule_Create(&module) : nullptr;
+  tile_name = PyUnicode_InternFromString("tile");
+  return codes_name && scales_name && cols_name && tile_name ? PyModule_Create(&module) : nullptr;
 }

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "../csrc_base8/base8.h"
 #include "mlp.h"
 
 namespace mlp {
@@ -54,7 +55,7 @@ lora_status device_ready(int* nsm) {
       d.status = static_cast<uint32_t*>(p);
       d.fit.nsm = n;
       if (prepare_pack8_da() != cudaSuccess || prepare_ffn(&d.fit) != cudaSuccess ||
-          prepare_layer_norm() != cudaSuccess)
+          prepare_layer_norm() != cudaSuccess || prepare_linear(dev) != cudaSuccess || prepare_distill() != cudaSuccess)
         return LORA_ERR_CUDA;
     }
     d.probed = true;
