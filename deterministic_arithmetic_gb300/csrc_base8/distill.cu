@@ -144,12 +144,7 @@ struct Lists {
   int *head, *next, *id;           // shared memory: groups, top, top
 };
 
-// The sum of a double over a warp, in a fixed order; every lane has it.
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+// The sum (maximum) over a warp, in a fixed order; every lane has it.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -331,19 +326,23 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
   s_top = warp_sum(s_top);
   s_teacher = warp_sum(s_teacher);
   const float s_rest = rescale(rest.s, rest.m, m, c), s = s_rest + s_top;
-  // log p and log q in 64 bits: the terms of a small divergence cancel
-  const double inv = 1.0 / double(P.temperature);
-  const double log_s = double(logf(s)), lse = double(m) * inv + log_s;
-  const double norm = P.teacher_lse ? double(__ldg(P.teacher_lse + row)) : double(tm) * inv + double(logf(s_teacher));
-  double sum_p = 0.0, loss = 0.0;
+  // log p - log q = (t - z) / T - (norm - log sum exp(z / T)): a difference of an entry's own two logits, and one of the
+  // row's, taken in 64 bits. The terms of a small divergence cancel, and so keep their digits.
+  const float inv_t = 1.f / P.temperature, log_s = logf(s);
+  const float lse = P.teacher_lse ? __ldg(P.teacher_lse + row) : 0.f, log_t = logf(s_teacher);
+  const double it = 1.0 / double(P.temperature);
+  const float gap = float((P.teacher_lse ? double(lse) : double(tm) * it + double(log_t)) - (double(m) * it + double(log_s)));
+  const float it_lo = float(it - double(inv_t));
+  float sum_p = 0.f, loss = 0.f;
   for (int i = lane; i < P.top; i += 32) {
     const float ti = tl[i];
     float p = -1.f;
     if (ti != -kInf) {
-      const double log_p = double(ti) * inv - norm;
-      p = expf(float(log_p));
-      sum_p += double(p);
-      if (p != 0.f) loss += double(p) * (log_p - (double(zl[i]) * inv - lse));
+      // t / T - lse by an exact product and its rest; (t - the largest t) / T - log of the sum
+      const float h = ti * inv_t, rest_h = fmaf(ti, inv_t, -h) + ti * it_lo;
+      p = expf(P.teacher_lse ? (h - lse) + rest_h : (ti - tm) * inv_t - log_t);
+      sum_p += p;
+      if (p != 0.f) loss += p * ((ti - zl[i]) * inv_t - gap);
     }
     P.probs[row * P.top + i] = p;
   }
@@ -352,14 +351,11 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
   if (lane == 0) {
     float keep = 1.f;
     if (P.teacher_lse) {
-      const double r = fmax(1.0 - sum_p, 0.0);
-      if (r != 0.0) {                              // (NaN too)
-        const float ratio = s_top / s_rest;        // log rho = -log(1 + ratio)
-        loss += r * (log(r) + double(log1pf(ratio)));
-      }
-      if (s_rest != 0.f) keep = float(1.0 - r * (1.0 + double(s_top) / double(s_rest)));
+      const float r = sum_p >= 1.f ? 0.f : 1.f - sum_p, ratio = s_top / s_rest;   // log rho = -log(1 + ratio)
+      if (r != 0.f) loss += r * (log1pf(-sum_p) + log1pf(ratio));                 // (NaN too)
+      if (s_rest != 0.f) keep = 1.f - r * (1.f + ratio);
     }
-    P.loss[row] = any ? float(double(weight) * loss) : 0.f;
+    P.loss[row] = any ? weight * loss : 0.f;
     *reinterpret_cast<float4*>(P.stats + row * 4) =
         any ? make_float4(m, log2f(s), keep, weight) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
@@ -380,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_ke
   grid_dependency_wait();
   grid_dependents_launch();
   const float4 st = __ldg(reinterpret_cast<const float4*>(P.stats + row * 4));
-  const double g = double(__ldg(P.dloss + row)) * double(st.w) / double(P.temperature);
-  const bool zero = g == 0.0;
+  const float g = __ldg(P.dloss + row) * st.w / P.temperature;
+  const bool zero = g == 0.f;
   for (int i = tid; i < g1 - g0; i += kThreads) L.head[i] = -1;
   __syncthreads();
   for (int i = tid; i < P.top && !zero; i += kThreads) {
@@ -395,11 +391,8 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_ke
     }
   }
   __syncthreads();
-  // q g = 2^(x c + hi) 2^lo g, hi + lo = -(m c) - log2 sum; the part lo that hi's rounding leaves joins g
-  const float c = kLog2e / P.temperature;
-  const double shift = -(double(st.x) * double(c)) - double(st.y);
-  const float hi = float(shift);
-  const float ga = float(g * exp2(shift - double(hi))), gr = float(double(ga) * double(st.z)), gp = -float(g);
+  // q = 2^((x - m) c - log2 sum): the difference first, which is exact where q is large
+  const float c = kLog2e / P.temperature, m = st.x, log_s = -st.y, gr = g * st.z;
   const int64_t base = row * P.V, ld = code_ld(P.V);
   const int cblocks = (P.V + kBlock - 1) / kBlock;
   for (int gb = g0 + warp; gb < g1; gb += kWarps * kLoads) {
@@ -422,16 +415,16 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_ke
         held[k].get(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[e] = ex2(fmaf(x[e], c, hi));
+          x[e] = ex2(fmaf(x[e] - m, c, log_s));
           v[e] = x[e] * gr;
         }
         for (int i = L.head[gi - g0]; i >= 0; i = L.next[i]) {
           const int o = L.id[i] - gi * kGroupElems, e0 = Held<KIND, VEC>::elem_of(o);
           if (Held<KIND, VEC>::lane_of(o) == lane) {
-            const float pg = pl[i] * gp;
+            const float pg = pl[i] * g;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (e == e0) v[e] = fmaf(x[e], ga, pg);
+              if (e == e0) v[e] = fmaf(x[e], g, -pg);
           }
         }
       }

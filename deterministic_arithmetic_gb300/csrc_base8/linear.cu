@@ -22,7 +22,7 @@ lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void
   P.bn = plan.bn;
   // a batch smaller than a tile: only its rows are copied, and the ring holds more stages
   const int a_rows = P.m < kBM ? int((P.m + 7) & ~7) : kBM;
-  constexpr int chunk = W < 128 ? W : 128;
+  constexpr int chunk = lin_chunk(W, CG);
   if (!tensor_map(&P.a, a, Elem::u8, P.m, red, code_ld(red), kLinBK, a_rows, 128)) return LORA_ERR_CUDA;
   const bool b = MODE == kLinFwd
                      ? tensor_map(&P.b, w, Elem::u8, w_rows, w_cols, code_ld(w_cols), kLinBK, P.bn / CG, 128)
@@ -35,11 +35,7 @@ lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void
   P.tiles_n = int(cdiv(P.n, P.bn));
   const int64_t total = int64_t(P.tiles_m) * P.tiles_n;
   if (total >= int64_t(1) << 30) return LORA_ERR_SHAPE;
-  // a last round of at most half the pairs is dealt out as half tiles (whole swizzle spans only)
-  const int rest = CG == 2 && MODE == kLinFwd ? int(total % pairs) : 0;
-  const bool halves = rest > 0 && 2 * rest <= pairs;
-  P.whole = int(halves ? total - rest : total);
-  P.total = int(halves ? total + rest : total);
+  P.total = int(total);
   const int most = CG == 2 ? pairs : nsm;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(CG * (P.total < most ? P.total : most)));

@@ -30,13 +30,33 @@ static_assert(kLinSmem < 227 * 1024, "shared memory of a CTA");
 constexpr int kLinThreads = 384, kLinRegs = 168, kLinRegsFew = 56, kLinRegsMany = 224;
 static_assert(128 * kLinRegsFew + 256 * kLinRegsMany <= kLinThreads * kLinRegs, "the shares fit the launch's registers");
 
-// The bounded waits of waits.cuh, without a call: a kernel that shares out its registers can hold none.
+// The bounded waits of waits.cuh, without a call: a kernel that shares out its registers can hold none. And without
+// ordering at cluster scope: what the barriers of this kernel stand for is written by copies and tensor cores, never
+// by a peer's stores. (Acquiring at that scope throws the SM's L1 away, and a release waits for the thread's loads: of a
+// pair's 4096 x 17408 -> 5120, 943 us with both, 411 with neither.)
+__device__ __forceinline__ bool lin_done(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0u;
+}
+__device__ __forceinline__ void lin_arrive_peer(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, Abort ab, uint32_t site, uint64_t limit,
                                                 bool honour_abort) {
+  // (the clock takes longer to read than most waits last: not before some tries)
+  for (uint32_t it = 0; it < 1024u; ++it)
+    if (mbar_test(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (true) {
     if (honour_abort && *ab.flag) return false;
-    if (mbar_test_cluster(bar, parity)) return true;
+    if (mbar_test(bar, parity)) return true;
     if (global_ns() - t0 > limit) {
       *ab.flag = 1u;
       if (ab.status) atomicCAS(ab.status, 0u, (site << 8) | kDevTimeout);   // the first code stays
@@ -45,10 +65,10 @@ __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, A
   }
 }
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
-  return completed(bar, parity) || lin_wait_longer(bar, parity, ab, site, ab.limit_ns, true);
+  return lin_done(bar, parity) || lin_wait_longer(bar, parity, ab, site, ab.limit_ns, true);
 }
 __device__ __forceinline__ void lin_drain(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
-  if (!completed(bar, parity)) lin_wait_longer(bar, parity, ab, site, kDrainLimitNs, false);
+  if (!lin_done(bar, parity)) lin_wait_longer(bar, parity, ab, site, kDrainLimitNs, false);
 }
 
 template <int CG>
@@ -80,6 +100,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// a += s * (x, y), each one fma, as a pair.
+__device__ __forceinline__ void add_scaled(float2& a, float s, uint32_t x, uint32_t y) {
+  asm("{\n\t.reg .b64 a, v, s;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 v, {%2, %3};\n\t"
+      "mov.b64 s, {%4, %4};\n\t"
+      "fma.rn.f32x2 a, s, v, a;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(x), "r"(y), "f"(s));
+}
 template <int N>
 __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
   static_assert(N == 16 || N == 32, "");
@@ -87,41 +118,43 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
   else tmem_ld16(taddr, r);
 }
 
-// The tile of a unit (gemm.cuh's order: groups of up to 16 row tiles, row tiles fastest).
+// Columns of a copied piece of MN-major B, which is its swizzle span; an MMA takes whole pieces.
+constexpr int lin_chunk(int W, int CG) { return CG == 2 ? 64 : (W < 128 ? W : 128); }
+
+// The tile of a unit: groups of up to 16 row tiles, row tiles fastest (gemm.cuh).
 struct LinUnit {
   int tm, col, bn;
 };
 template <int CG>
 __device__ __forceinline__ LinUnit lin_unit(const LinArgs& P, int u) {
-  int tile = u, half = -1;
-  if (CG == 2 && u >= P.whole) {
-    tile = P.whole + (u - P.whole) / 2;
-    half = (u - P.whole) & 1;
-  }
-  LinUnit w;
-  const int group = tile / (16 * P.tiles_n), m0 = 16 * group;
+  const int group = u / (16 * P.tiles_n), m0 = 16 * group;
   const int gm = min(16, P.tiles_m - m0);
-  const int r = tile - 16 * group * P.tiles_n;
-  w.tm = m0 + r % gm;
-  w.bn = half < 0 ? P.bn : P.bn / 2;
-  w.col = (r / gm) * P.bn + (half == 1 ? w.bn : 0);
-  return w;
+  const int r = u - 16 * group * P.tiles_n;
+  return {m0 + r % gm, (r / gm) * P.bn, P.bn};
 }
 
 // 32 rows by 16 columns of the warp (lane l holds row row0 + l's), plus delta, to the output, by way of the warp's
 // 2 KB of shared memory: 4 lanes a row then read and write whole sectors. 16-byte pieces of a row are permuted by the
 // row's bits 1 and 2, so that neither way meets a bank twice. Rows past m and columns past `end` are left alone.
-__device__ __forceinline__ void lin_store16(const LinArgs& P, uint32_t box, int64_t row0, int col, int end, const float* acc,
+__device__ __forceinline__ void lin_store16(const LinArgs& P, uint32_t box, int64_t row0, int col, int end, const float2* acc,
                                             uint32_t lane) {
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)),
-                 "f"(acc[4 * j]), "f"(acc[4 * j + 1]), "f"(acc[4 * j + 2]), "f"(acc[4 * j + 3])
+                 "f"(acc[2 * j].x), "f"(acc[2 * j].y), "f"(acc[2 * j + 1].x), "f"(acc[2 * j + 1].y)
                  : "memory");
   __syncwarp();
   const int c = col + 4 * int(lane & 3);
-#pragma unroll 4
+  const bool whole = P.vec && c < end;             // the row's columns are whole vectors: so are c's
+  float4 d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + 8 * i + int(lane >> 2);
+    d[i] = whole && P.delta && row < P.m ? __ldcs(reinterpret_cast<const float4*>(P.delta + row * P.n + c))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * i + int(lane >> 2);
     const int64_t row = row0 + r;
@@ -132,11 +165,8 @@ __device__ __forceinline__ void lin_store16(const LinArgs& P, uint32_t box, int6
                  : "memory");
     if (row >= P.m || c >= end) continue;
     const int64_t at = row * P.n + c;
-    if (P.vec) {                                   // the row's columns are whole vectors: so is c's
-      if (P.delta) {
-        const float4 d = __ldcs(reinterpret_cast<const float4*>(P.delta + at));
-        v[0] += d.x; v[1] += d.y; v[2] += d.z; v[3] += d.w;
-      }
+    if (whole) {
+      v[0] += d[i].x; v[1] += d[i].y; v[2] += d[i].z; v[3] += d[i].w;
       if (P.out_f32)
         *reinterpret_cast<float4*>(static_cast<float*>(P.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
       else
@@ -171,8 +201,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   const uint32_t never = drain + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kLinStages + 2 * kLinSlots + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  constexpr int kSlots = 512 / (W * DEEP) < kLinSlots ? 512 / (W * DEEP) : kLinSlots;
-  static_assert(kSlots >= 2 && (W >= 32 && W <= 256), "TMEM columns");
+  // An accumulator of 256 columns is two slots, each filled by MMAs and read by four warps of its own.
+  constexpr int kSub = W == 256 ? 2 : 1, kSlotCols = W * DEEP / kSub;
+  constexpr int kSlots = 512 / kSlotCols < kLinSlots ? 512 / kSlotCols : kLinSlots;
+  static_assert(kSlots >= 2 && kSlots % kSub == 0 && (W >= 32 && W <= 256), "TMEM columns");
   static_assert(CG == 1 || W == 256, "pairs take tiles of 256 columns");
 
   const uint32_t warp = warp_id(), lane = lane_id();
@@ -185,7 +217,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     }
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), CG * kEpiWarps);
+      mbar_init(tempty(b), CG * kEpiWarps / kSub);
     }
     mbar_init(drain, 1);
     mbar_init(never, 1);
@@ -209,7 +241,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   const Abort ab = make_abort(abort_flag, status);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   // a copied piece of MN-major B: kChunk columns of 128 rows of the weight, its swizzle span
-  constexpr int kChunk = W < 128 ? W : 128;
+  constexpr int kChunk = lin_chunk(W, CG);
 
   if (warp < 4) {
   if constexpr (W == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLinRegsFew));
@@ -231,7 +263,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
         if (!__all_sync(0xffffffffu, ready || lin_wait(empty(idx), phase ^ 1u, ab, kSiteLinear + 2))) goto given_up;
         const uint32_t st0 = base + uint32_t(idx) * stage_bytes, bar = full0 + 8u * idx, here = full(idx);
         if (++idx == stages) idx = 0, phase ^= 1u;
-        ready = completed(empty(idx), phase ^ 1u);
+        ready = lin_done(empty(idx), phase ^ 1u);
         ++issued;
         if (one) {
           if (rank == 0) mbar_expect_tx(here, uint32_t(CG * (DEEP == 1 ? 1 : min(DEEP, P.nk - kb)) * P.block_bytes));
@@ -270,34 +302,41 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       constexpr uint32_t kSpan = MODE == kLinFwd ? 128 : kChunk, a_step = 32u, b_step = MODE == kLinFwd ? 32u : 32u * kSpan;
       const uint64_t a0 = smem_desc(base, 16u, 1024u, kLayoutSW128);
       const uint64_t b0 = smem_desc(base + P.a_bytes, MODE == kLinFwd ? 16u : kLinBK * kSpan, 8u * kSpan, layout_for_span(kSpan));
+      constexpr uint32_t kHalfBytes = 128 / CG * kLinBK;        // of this CTA's B, what a slot of 128 columns takes
       const bool one = elect_one();
       int idx = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
       bool ready = false, ok = true;
       for (int u = first; u < P.total && ok; u += step) {
-        const uint32_t idesc = idesc_f8(CG * kBM, lin_unit<CG>(P, u).bn, MODE == kLinBwd);
+        const uint32_t idesc = idesc_f8(CG * kBM, lin_unit<CG>(P, u).bn / kSub, MODE == kLinBwd);
         for (int kb = 0; kb < P.nk; kb += DEEP) {
-          ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4) &&
-                                           (ready || lin_wait(full(idx), phase, ab, kSiteLinear + 5)));
+          ok = __all_sync(0xffffffffu, ready || lin_wait(full(idx), phase, ab, kSiteLinear + 5));
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + buf * (W * DEEP), off0 = uint32_t(idx) * stage_bytes, used = empty(idx), done = tfull(buf);
+          const uint32_t off0 = uint32_t(idx) * stage_bytes, used = empty(idx);
           if (++idx == stages) idx = 0, phase ^= 1u;
-          if (++buf == kSlots) buf = 0, tphase ^= 1u;
-          ready = completed(full(idx), phase);
-          if (one) {
 #pragma unroll
-            for (int k = 0; k < DEEP; ++k) {
-              if (k > 0 && kb + k >= P.nk) break;
-              const uint32_t off = off0 + k * P.block_bytes;
+          for (int h = 0; h < kSub; ++h) {
+            ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + buf * kSlotCols, done = tfull(buf);
+            if (++buf == kSlots) buf = 0, tphase ^= 1u;
+            if (one) {
 #pragma unroll
-              for (int j = 0; j < kLinBK / 32; ++j)
-                mma_f8<CG>(d + k * W, desc_advance(a0, off + j * a_step), desc_advance(b0, off + j * b_step), idesc, j ? 1u : 0u);
+              for (int k = 0; k < DEEP; ++k) {
+                if (k > 0 && kb + k >= P.nk) break;
+                const uint32_t off = off0 + k * P.block_bytes;
+#pragma unroll
+                for (int j = 0; j < kLinBK / 32; ++j)
+                  mma_f8<CG>(d + k * W, desc_advance(a0, off + j * a_step), desc_advance(b0, off + h * kHalfBytes + j * b_step), idesc,
+                             j ? 1u : 0u);
+              }
+              commit<CG>(done);
+              if (h == kSub - 1) commit<CG>(used);
             }
-            commit<CG>(used);
-            commit<CG>(done);
+            __syncwarp();
           }
-          __syncwarp();
+          ready = lin_done(full(idx), phase);
         }
       }
       if (one) commit_here<CG>(drain);
@@ -308,32 +347,36 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   } else {
     // ------------------------------------------------------------ epilogue
     if constexpr (W == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLinRegsMany));
-    // A warp has its quarter of the rows and half of the tile's columns, in chunks of C.
+    // A warp has its quarter of the rows and half of the tile's columns, in chunks of C: one after the other, but of a
+    // pair's tile, where a slot holds 64 columns of each CTA's B, 64 from each half of the tile.
     constexpr int C = W >= 64 ? 32 : 16, kChunks = W / 2 / C;
-    constexpr int kScales = W == 256 ? 1 : (W == 64 ? 2 : kChunks);    // the weight's scales of a warp's columns and k-block
+    constexpr int kScales = W == 256 ? CG : 2;                     // the weight's scales of a warp's columns and k-block
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = uint32_t(q * 32) << 16;
-    int buf = 0;
+    const int off = half * (CG == 2 ? 64 : W / 2);                 // its first column in the tile
+    auto column = [&](int i) { return off + i + (CG == 2 && i >= 64 ? 64 : 0); };      // and its i-th
+    // which of the scales its column i has
+    auto scale_of = [](int i) { return W == 256 ? i / 64 * (CG - 1) : i * 2 / (W / 2); };
+    int buf = kSub == 2 ? half : 0;
     uint32_t tphase = 0;
     for (int u = first; u < P.total; u += step) {
       const LinUnit w = lin_unit<CG>(P, u);
       const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32, row = row0 + lane;
-      const int off = half * (W == 256 ? w.bn / 2 : W / 2);          // its first column in the tile
       const bool rows = row0 < P.m;
       const float* sa = P.sa + min(row, int64_t(P.m) - 1) * P.nk;
-      // scale e of a block: of columns 32 e (or, of 64-column tiles, whose width need not be whole chunks, 16 e) on
       const float* sb[kScales];
 #pragma unroll
-      for (int e = 0; e < kScales; ++e) sb[e] = P.sb + min(w.col + off + e * (W == 64 ? 16 : C), P.n - 1) / 128 * P.sb_out;
-      float acc[kChunks * C];
+      for (int e = 0; e < kScales; ++e) sb[e] = P.sb + min(w.col + column(e * (W / 2) / kScales), P.n - 1) / 128 * P.sb_out;
+      float2 acc[kChunks * C / 2];
 #pragma unroll
-      for (int i = 0; i < kChunks * C; ++i) acc[i] = 0.f;
+      for (int i = 0; i < kChunks * C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       bool ok = true;
-      // the scales of the next four blocks
-      float na[4], nb[4][kScales];
+      // the scales of the next blocks
+      constexpr int kAhead = W == 256 ? 2 : 4;
+      float na[kAhead], nb[kAhead][kScales];
       auto fetch = [&](int kb) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kAhead; ++k)
           if (kb + k < P.nk) {
             na[k] = __ldg(sa + kb + k);
 #pragma unroll
@@ -341,44 +384,47 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
           }
       };
       fetch(0);
-      for (int kb0 = 0; kb0 < P.nk; kb0 += 4) {
-        float s[4][kScales];
+      for (int kb0 = 0; kb0 < P.nk; kb0 += kAhead) {
+        float s[kAhead][kScales];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kAhead; ++k)
 #pragma unroll
           for (int e = 0; e < kScales; ++e) s[k][e] = na[k] * nb[k][e];
-        if (kb0 + 4 < P.nk) fetch(kb0 + 4);
+        if (kb0 + kAhead < P.nk) fetch(kb0 + kAhead);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
           if (kb0 + k >= P.nk) break;
+          const bool last = k % DEEP == DEEP - 1 || kb0 + k == P.nk - 1;       // of its slot
           if (k % DEEP == 0) {
             ok = __all_sync(0xffffffffu, lin_wait(tfull(buf), tphase, ab, kSiteLinear + 7)) && ok;
             tc_fence_after();
           }
-          if (ok && rows) {
-            const uint32_t at = tmem + buf * (W * DEEP) + (k % DEEP) * W + lanes + off;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-              if (W == 256 && i * C >= w.bn / 2) break;      // half a tile
-              uint32_t r[C];
-              tmem_ldn(at + i * C, r);
-              tmem_ld_wait();
-              reg_fence(r);
-#pragma unroll
-              for (int e = 0; e < C; ++e) {
-                const float f = s[k][W == 256 ? 0 : (W == 64 ? e / 16 : i)];
-                acc[i * C + e] = fmaf(f, __uint_as_float(r[e]), acc[i * C + e]);
-              }
-            }
-          }
-          if (k % DEEP == DEEP - 1 || kb0 + k == P.nk - 1) {
+          auto leave = [&]() {
             tc_fence_before();
             __syncwarp();
             if (ok && lane == 0) {
-              if constexpr (CG == 2) mbar_arrive_peer(peer_addr(tempty(buf), 0));
+              if constexpr (CG == 2) lin_arrive_peer(peer_addr(tempty(buf), 0));
               else mbar_arrive(tempty(buf));
             }
-            if (++buf == kSlots) buf = 0, tphase ^= 1u;
+            if ((buf += kSub) >= kSlots) buf -= kSlots, tphase ^= 1u;
+          };
+          if (ok && rows) {
+            // a chunk is on its way while the one before is added; the slot is given back when the last has come
+            const uint32_t at = tmem + buf * kSlotCols + (k % DEEP) * W + lanes + (kSub == 2 ? 0 : off);
+            uint32_t r[kChunks > 1 ? 2 : 1][C];
+            tmem_ldn(at, r[0]);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+              uint32_t(&v)[C] = r[kChunks > 1 ? i & 1 : 0];
+              tmem_ld_wait();
+              reg_fence(v);
+              if (i + 1 < kChunks) tmem_ldn(at + (i + 1) * C, r[(i + 1) & 1]);
+              else if (last) leave();
+#pragma unroll
+              for (int e = 0; e < C; e += 2) add_scaled(acc[(i * C + e) / 2], s[k][scale_of(i * C + e)], v[e], v[e + 1]);
+            }
+          } else if (last) {
+            leave();
           }
         }
       }
@@ -387,7 +433,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
         const uint32_t box = base + kLinSmemRing + (warp - 4) * 2048;
 #pragma unroll
         for (int i = 0; i < kChunks * C; i += 16)
-          if (off + i < w.bn && (W != 256 || i < w.bn / 2)) lin_store16(P, box, row0, w.col + off + i, end, acc + i, lane);
+          if (column(i) < w.bn) lin_store16(P, box, row0, w.col + column(i), end, acc + i / 2, lane);
       }
     }
   }

@@ -21,7 +21,7 @@ struct LinArgs {
   int bn;                          // tile columns
   int stages, block_bytes, a_bytes;   // of the ring; of a k-block (all of it copied); of it A's rows
   int tiles_m, tiles_n;
-  int whole, total;                // units of work: `whole` tiles, then halves of the remaining ones
+  int total;                       // tiles
 };
 
 }  // namespace mlp
