@@ -16,13 +16,18 @@
 namespace mlp {
 
 constexpr int kLinBK = 128;                        // depth of a k-block: a block of the scales
-constexpr int kLinSmemRing = 200 * 1024;           // the operand ring
+constexpr int kLinSmemRing = 192 * 1024;           // the operand ring
 constexpr int kLinStages = 16;
 constexpr int kLinSlots = 4;                       // accumulator slots at most
 // Behind the ring, 2 KB of each epilogue warp; the MMAs' reads past a short batch's rows of A (whose products nobody
 // reads) stay inside.
 constexpr int kLinSlack = 16 * 1024;
-constexpr size_t kLinSmem = kLinSmemRing + kLinSlack + 1024 + (2 * kLinStages + 2 * kLinSlots + 2) * 8 + 16;
+// Behind that the ring of scales: groups of four k-blocks, a k-block's products of a row's scale and that of each of the (at
+// most two) column blocks that a tile touches, [block of columns][row].
+constexpr int kScaleGroup = 4, kScaleGroups = 4, kScaleBytes = 2 * kBM * 4;       // (of a k-block)
+constexpr int kLinScales = kScaleGroups * kScaleGroup * kScaleBytes;
+constexpr size_t kLinSmem =
+    kLinSmemRing + kLinSlack + kLinScales + 1024 + (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + 2) * 8 + 16;
 static_assert(kLinSmem < 227 * 1024, "shared memory of a CTA");
 
 // Four warps to load, issue and idle, eight for the epilogue. Of 256-column tiles an epilogue thread holds 128 sums:
@@ -191,15 +196,18 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kLinSmemRing + kLinSlack);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kLinSmemRing + kLinSlack + kLinScales);
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kLinStages + s); };
   auto tfull = [&](int b) { return bar0 + 8u * (2 * kLinStages + b); };
   auto tempty = [&](int b) { return bar0 + 8u * (2 * kLinStages + kLinSlots + b); };
-  const uint32_t drain = bar0 + 8u * (2 * kLinStages + 2 * kLinSlots);
+  auto sfull = [&](int g) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + g); };
+  auto sempty = [&](int g) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + kScaleGroups + g); };
+  const uint32_t scales = base + kLinSmemRing + kLinSlack;
+  const uint32_t drain = bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups);
   const uint32_t never = drain + 8u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kLinStages + 2 * kLinSlots + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   // An accumulator of 256 columns is two slots, each filled by MMAs and read by four warps of its own.
   constexpr int kSub = W == 256 ? 2 : 1, kSlotCols = W * DEEP / kSub;
@@ -218,6 +226,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(tfull(b), 1);
       mbar_init(tempty(b), CG * kEpiWarps / kSub);
+    }
+    for (int g = 0; g < kScaleGroups; ++g) {
+      mbar_init(sfull(g), 1);
+      mbar_init(sempty(g), kEpiWarps);
     }
     mbar_init(drain, 1);
     mbar_init(never, 1);
@@ -343,6 +355,44 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       __syncwarp();
       lin_drain(drain, 0u, ab, kSiteLinear + 6);
     }
+  } else {
+    // ------------------------------------------------------ scales, two warps
+    // Their groups in turn. (Loaded by the epilogue's warps themselves, the scales' latency was most of a k-block's time: of a
+    // pair's 4096 x 17408 -> 5120, SCALEFIG.)
+    uint32_t n = 0;                                // groups so far, of both warps
+    bool ok = true;
+    for (int u = first; u < P.total && ok; u += step) {
+      const LinUnit w = lin_unit<CG>(P, u);
+      const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + lane;
+      const float* sb[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sb[e] = P.sb + min(w.col / 128 + e, (P.n - 1) / 128) * P.sb_out;
+      for (int kb = 0; kb < P.nk && ok; kb += kScaleGroup, ++n) {
+        if ((n & 1u) != (warp & 1u)) continue;
+        float a[kScaleGroup][4], b[kScaleGroup][2];
+#pragma unroll
+        for (int k = 0; k < kScaleGroup; ++k) {
+          const bool in = kb + k < P.nk;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[k][j] = in ? __ldg(P.sa + min(row0 + 32 * j, int64_t(P.m) - 1) * P.nk + kb + k) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) b[k][e] = in ? __ldg(sb[e] + (kb + k) * P.sb_red) : 0.f;
+        }
+        const uint32_t g = n % kScaleGroups, at = scales + g * kScaleGroup * kScaleBytes + lane * 4;
+        ok = __all_sync(0xffffffffu, lin_wait(sempty(g), (n / kScaleGroups & 1u) ^ 1u, ab, kSiteLinear + 9));
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < kScaleGroup; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + k * kScaleBytes + e * kBM * 4 + j * 128), "f"(a[k][j] * b[k][e])
+                           : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfull(g));
+      }
+    }
   }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -350,7 +400,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     // A warp has its quarter of the rows and half of the tile's columns, in chunks of C: one after the other, but of a
     // pair's tile, where a slot holds 64 columns of each CTA's B, 64 from each half of the tile.
     constexpr int C = W >= 64 ? 32 : 16, kChunks = W / 2 / C;
-    constexpr int kScales = W == 256 ? CG : 2;                     // the weight's scales of a warp's columns and k-block
+    constexpr int kScales = W == 256 ? CG : 2;                     // scales of a lane's row, of the warp's columns, a k-block
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = uint32_t(q * 32) << 16;
     const int off = half * (CG == 2 ? 64 : W / 2);                 // its first column in the tile
@@ -358,42 +408,29 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     // which of the scales its column i has
     auto scale_of = [](int i) { return W == 256 ? i / 64 * (CG - 1) : i * 2 / (W / 2); };
     int buf = kSub == 2 ? half : 0;
-    uint32_t tphase = 0;
+    uint32_t tphase = 0, n = 0;                    // groups of scales so far
     for (int u = first; u < P.total; u += step) {
       const LinUnit w = lin_unit<CG>(P, u);
-      const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32, row = row0 + lane;
+      const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32;
       const bool rows = row0 < P.m;
-      const float* sa = P.sa + min(row, int64_t(P.m) - 1) * P.nk;
-      const float* sb[kScales];
+      uint32_t block[kScales];                     // where in a k-block's scales
 #pragma unroll
-      for (int e = 0; e < kScales; ++e) sb[e] = P.sb + min(w.col + column(e * (W / 2) / kScales), P.n - 1) / 128 * P.sb_out;
+      for (int e = 0; e < kScales; ++e)
+        block[e] = uint32_t((w.col + column(e * (W / 2) / kScales)) / 128 - w.col / 128) * (kBM * 4) + (q * 32 + lane) * 4;
       float2 acc[kChunks * C / 2];
 #pragma unroll
       for (int i = 0; i < kChunks * C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       bool ok = true;
-      // the scales of the next blocks
-      constexpr int kAhead = W == 256 ? 2 : 4;
-      float na[kAhead], nb[kAhead][kScales];
-      auto fetch = [&](int kb) {
+      for (int kb0 = 0; kb0 < P.nk; kb0 += kScaleGroup, ++n) {
+        const uint32_t g = n % kScaleGroups, sg = scales + g * kScaleGroup * kScaleBytes;
+        ok = __all_sync(0xffffffffu, lin_wait(sfull(g), n / kScaleGroups & 1u, ab, kSiteLinear + 10)) && ok;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-          if (kb + k < P.nk) {
-            na[k] = __ldg(sa + kb + k);
-#pragma unroll
-            for (int e = 0; e < kScales; ++e) nb[k][e] = __ldg(sb[e] + (kb + k) * P.sb_red);
-          }
-      };
-      fetch(0);
-      for (int kb0 = 0; kb0 < P.nk; kb0 += kAhead) {
-        float s[kAhead][kScales];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-          for (int e = 0; e < kScales; ++e) s[k][e] = na[k] * nb[k][e];
-        if (kb0 + kAhead < P.nk) fetch(kb0 + kAhead);
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
+        for (int k = 0; k < kScaleGroup; ++k) {
           if (kb0 + k >= P.nk) break;
+          float s[kScales];
+#pragma unroll
+          for (int e = 0; e < kScales; ++e)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[e]) : "r"(sg + k * kScaleBytes + block[e]) : "memory");
           const bool last = k % DEEP == DEEP - 1 || kb0 + k == P.nk - 1;       // of its slot
           if (k % DEEP == 0) {
             ok = __all_sync(0xffffffffu, lin_wait(tfull(buf), tphase, ab, kSiteLinear + 7)) && ok;
@@ -421,12 +458,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
               if (i + 1 < kChunks) tmem_ldn(at + (i + 1) * C, r[(i + 1) & 1]);
               else if (last) leave();
 #pragma unroll
-              for (int e = 0; e < C; e += 2) add_scaled(acc[(i * C + e) / 2], s[k][scale_of(i * C + e)], v[e], v[e + 1]);
+              for (int e = 0; e < C; e += 2) add_scaled(acc[(i * C + e) / 2], s[scale_of(i * C + e)], v[e], v[e + 1]);
             }
           } else if (last) {
             leave();
           }
         }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(sempty(g));
       }
       if (ok && rows) {
         const int end = min(P.n, w.col + w.bn);
