@@ -70,27 +70,32 @@ __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, A
   }
 }
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
-  return lin_done(bar, parity) || lin_wait_longer(bar, parity, ab, site, ab.limit_ns, true);
+  return __builtin_expect(lin_done(bar, parity), 1) || lin_wait_longer(bar, parity, ab, site, ab.limit_ns, true);
 }
 __device__ __forceinline__ void lin_drain(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
   if (!lin_done(bar, parity)) lin_wait_longer(bar, parity, ab, site, kDrainLimitNs, false);
 }
 
-template <int CG>
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D (+)= A B^T. Of the operands' descriptors the low words differ from MMA to MMA, the high ones never.
+template <int CG, int ACCUMULATE>
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc) {
   if constexpr (CG == 1)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACCUMULATE)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACCUMULATE)
         : "memory");
 }
 // Instruction descriptor: e4m3 A and B (0), FP32 D, A K-major, B K-major or (b_mn) MN-major.
@@ -225,7 +230,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     }
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), CG * kEpiWarps / kSub);
+      mbar_init(tempty(b), kEpiWarps / kSub + (CG == 2 && rank == 0 ? 1 : 0));
     }
     for (int g = 0; g < kScaleGroups; ++g) {
       mbar_init(sfull(g), 1);
@@ -312,48 +317,63 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     if (rank == 0) {
       // K-major operands step 32 bytes inside the swizzle span per 32 of the reduction; MN-major ones 32 rows.
       constexpr uint32_t kSpan = MODE == kLinFwd ? 128 : kChunk, a_step = 32u, b_step = MODE == kLinFwd ? 32u : 32u * kSpan;
+      constexpr uint32_t kHalfBytes = 128 / CG * kLinBK;        // of this CTA's B, what a slot of 128 columns takes
       const uint64_t a0 = smem_desc(base, 16u, 1024u, kLayoutSW128);
       const uint64_t b0 = smem_desc(base + P.a_bytes, MODE == kLinFwd ? 16u : kLinBK * kSpan, 8u * kSpan, layout_for_span(kSpan));
-      constexpr uint32_t kHalfBytes = 128 / CG * kLinBK;        // of this CTA's B, what a slot of 128 columns takes
+      const uint32_t a_lo = uint32_t(a0), a_hi = uint32_t(a0 >> 32), b_lo = uint32_t(b0), b_hi = uint32_t(b0 >> 32);
+      const uint32_t idesc = idesc_f8(CG * kBM, P.bn / kSub, MODE == kLinBwd);
       const bool one = elect_one();
       int idx = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
-      bool ready = false, ok = true;
+      // Whether stage idx has landed and slot buf has been read: tested as soon as the one before is issued. (This warp's own
+      // steps are what bounds the large tiles.)
+      bool landed = false, free = true, ok = true;
       for (int u = first; u < P.total && ok; u += step) {
-        const uint32_t idesc = idesc_f8(CG * kBM, lin_unit<CG>(P, u).bn / kSub, MODE == kLinBwd);
         for (int kb = 0; kb < P.nk; kb += DEEP) {
-          ok = __all_sync(0xffffffffu, ready || lin_wait(full(idx), phase, ab, kSiteLinear + 5));
+          if (!__all_sync(0xffffffffu, landed)) ok = __all_sync(0xffffffffu, lin_wait(full(idx), phase, ab, kSiteLinear + 5));
           if (!ok) break;
-          const uint32_t off0 = uint32_t(idx) * stage_bytes, used = empty(idx);
+          const uint32_t off = uint32_t(idx) * stage_bytes, used = empty(idx);
           if (++idx == stages) idx = 0, phase ^= 1u;
 #pragma unroll
           for (int h = 0; h < kSub; ++h) {
-            ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4));
+            if (!__all_sync(0xffffffffu, free)) ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d = tmem + buf * kSlotCols, done = tfull(buf);
-            if (++buf == kSlots) buf = 0, tphase ^= 1u;
             if (one) {
+              const uint32_t d = tmem + buf * kSlotCols;
 #pragma unroll
               for (int k = 0; k < DEEP; ++k) {
                 if (k > 0 && kb + k >= P.nk) break;
-                const uint32_t off = off0 + k * P.block_bytes;
+                const uint32_t a = a_lo + ((off + k * P.block_bytes) >> 4), b = b_lo + ((off + k * P.block_bytes + h * kHalfBytes) >> 4);
+                mma_f8<CG, 0>(d + k * W, a, a_hi, b, b_hi, idesc);
 #pragma unroll
-                for (int j = 0; j < kLinBK / 32; ++j)
-                  mma_f8<CG>(d + k * W, desc_advance(a0, off + j * a_step), desc_advance(b0, off + h * kHalfBytes + j * b_step), idesc,
-                             j ? 1u : 0u);
+                for (int j = 1; j < kLinBK / 32; ++j)
+                  mma_f8<CG, 1>(d + k * W, a + (j * a_step >> 4), a_hi, b + (j * b_step >> 4), b_hi, idesc);
               }
-              commit<CG>(done);
+              commit<CG>(tfull(buf));
               if (h == kSub - 1) commit<CG>(used);
             }
-            __syncwarp();
+            if (++buf == kSlots) buf = 0, tphase ^= 1u;
+            free = lin_done(tempty(buf), tphase ^ 1u);
           }
-          ready = lin_done(full(idx), phase);
+          landed = lin_done(full(idx), phase);
         }
       }
       if (one) commit_here<CG>(drain);
       __syncwarp();
       lin_drain(drain, 0u, ab, kSiteLinear + 6);
+    } else {
+      // of a pair's second CTA: tells the first, once for all of its epilogue warps, that they have read a slot (arrivals across
+      // the pair are slow: an arrival of each warp, FORWARDFIG)
+      int buf = 0;
+      uint32_t tphase = 0;
+      bool ok = true;
+      for (int u = first; u < P.total && ok; u += step)
+        for (int i = 0; i < P.nk * kSub && ok; ++i) {
+          ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase, ab, kSiteLinear + 11));
+          if (ok && lane == 0) lin_arrive_peer(peer_addr(tempty(buf), 0));
+          if (++buf == kSlots) buf = 0, tphase ^= 1u;
+        }
     }
   } else {
     // ------------------------------------------------------ scales, two warps
@@ -424,7 +444,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       for (int kb0 = 0; kb0 < P.nk; kb0 += kScaleGroup, ++n) {
         const uint32_t g = n % kScaleGroups, sg = scales + g * kScaleGroup * kScaleBytes;
         ok = __all_sync(0xffffffffu, lin_wait(sfull(g), n / kScaleGroups & 1u, ab, kSiteLinear + 10)) && ok;
-#pragma unroll
+#pragma unroll(DEEP)                               // (code that does not fit the instruction caches costs more)
         for (int k = 0; k < kScaleGroup; ++k) {
           if (kb0 + k >= P.nk) break;
           float s[kScales];
@@ -439,10 +459,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
           auto leave = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) {
-              if constexpr (CG == 2) lin_arrive_peer(peer_addr(tempty(buf), 0));
-              else mbar_arrive(tempty(buf));
-            }
+            if (ok && lane == 0) mbar_arrive(tempty(buf));
             if ((buf += kSub) >= kSlots) buf -= kSlots, tphase ^= 1u;
           };
           if (ok && rows) {
