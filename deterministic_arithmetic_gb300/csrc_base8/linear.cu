@@ -30,7 +30,10 @@ lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void
   if (!b) return LORA_ERR_CUDA;
   P.a_bytes = a_rows * kLinBK;
   P.block_bytes = P.a_bytes + P.bn / CG * kLinBK;
-  P.stages = std::min(kLinStages, kLinSmemRing / (DEEP * P.block_bytes));
+  P.boxes = W == 256 && P.n % (P.out_f32 ? 4 : 8) == 0;
+  if (P.boxes && !tensor_map(&P.o, P.out, P.out_f32 ? Elem::f32 : Elem::bf16, P.m, P.n, P.n, P.out_f32 ? 16 : 32, 32, 64)) return LORA_ERR_CUDA;
+  if (P.boxes && P.delta && !tensor_map(&P.d, P.delta, Elem::f32, P.m, P.n, P.n, 16, 32, 64)) return LORA_ERR_CUDA;
+  P.stages = std::min(kLinStages, lin_ring(W, P.boxes && P.delta) / (DEEP * P.block_bytes));
   P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, P.bn));
   const int64_t total = int64_t(P.tiles_m) * P.tiles_n;

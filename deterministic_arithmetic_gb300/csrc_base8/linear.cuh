@@ -16,23 +16,27 @@
 namespace mlp {
 
 constexpr int kLinBK = 128;                        // depth of a k-block: a block of the scales
-constexpr int kLinSmemRing = 192 * 1024;           // the operand ring
+constexpr int kLinArea = 208 * 1024;               // the operand ring and, behind it, the epilogue warps' boxes
+// A box: 32 rows of 64 bytes that TMA stores or (delta's) loads. Tiles of 256 columns have three of each warp, or five where
+// delta is joined (four loads ahead, and one to store from), which costs the ring a stage or two it does not miss: its
+// 4 x 32 KB are 1.7 % slower than six at 4096 x 17408 -> 5120. Smaller tiles have one; there the MMAs' reads past a short
+// batch's rows of A (whose products nobody reads) end in them.
+constexpr int kBox = 32 * 64, kBoxesPlain = 3, kBoxesDelta = 5;
+constexpr int lin_boxes(int W, bool delta) { return W < 256 ? 1 : (delta ? kBoxesDelta : kBoxesPlain); }
+constexpr int lin_ring(int W, bool delta) { return kLinArea - kEpiWarps * lin_boxes(W, delta) * kBox; }
 constexpr int kLinStages = 16;
 constexpr int kLinSlots = 4;                       // accumulator slots at most
-// Behind the ring, 2 KB of each epilogue warp; the MMAs' reads past a short batch's rows of A (whose products nobody
-// reads) stay inside.
-constexpr int kLinSlack = 16 * 1024;
 // Behind that the ring of scales: groups of four k-blocks, a k-block's products of a row's scale and that of each of the (at
 // most two) column blocks that a tile touches, [block of columns][row].
 constexpr int kScaleGroup = 4, kScaleGroups = 4, kScaleBytes = 2 * kBM * 4;       // (of a k-block)
 constexpr int kLinScales = kScaleGroups * kScaleGroup * kScaleBytes;
-constexpr size_t kLinSmem =
-    kLinSmemRing + kLinSlack + kLinScales + 1024 + (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + 2) * 8 + 16;
+constexpr int kLinBars = 2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + kEpiWarps * (kBoxesDelta - 1) + 2;
+constexpr size_t kLinSmem = kLinArea + kLinScales + 1024 + kLinBars * 8 + 16;
 static_assert(kLinSmem < 227 * 1024, "shared memory of a CTA");
 
 // Four warps to load, issue and idle, eight for the epilogue. Of 256-column tiles an epilogue thread holds 128 sums:
-// it takes registers that the first four warps give up (shares of 56 and 224 of the launch's 168 a thread).
-constexpr int kLinThreads = 384, kLinRegs = 168, kLinRegsFew = 56, kLinRegsMany = 224;
+// it takes registers that the first four warps give up (shares of 40 and 232 of the launch's 168 a thread).
+constexpr int kLinThreads = 384, kLinRegs = 168, kLinRegsFew = 40, kLinRegsMany = 232;
 static_assert(128 * kLinRegsFew + 256 * kLinRegsMany <= kLinThreads * kLinRegs, "the shares fit the launch's registers");
 
 // The bounded waits of waits.cuh, without a call: a kernel that shares out its registers can hold none. And without
@@ -50,30 +54,59 @@ __device__ __forceinline__ bool lin_done(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0u;
 }
-__device__ __forceinline__ void lin_arrive_peer(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// The whole warp arrives once. Predicated, no branch: where lanes part, the code behind may run once for each part (a
+// pair's 4096 x 17408 -> 5120 took 552 us instead of 314 with a warp split so).
+__device__ __forceinline__ void lin_arrive(uint32_t bar, bool one) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(uint32_t(one))
+      : "memory");
 }
-__device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, Abort ab, uint32_t site, uint64_t limit,
-                                                bool honour_abort) {
+__device__ __forceinline__ void lin_arrive_peer(uint32_t cluster_addr, bool one) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr), "r"(uint32_t(one))
+      : "memory");
+}
+// Where a wait that runs out reports (common.cuh's Abort, with what only that needs left where it lies).
+struct LinAbort {
+  uint32_t flag;                   // shared memory
+  uint32_t* status;                // a kernel parameter
+  __device__ __forceinline__ bool raised() const {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(flag) : "memory");
+    return v != 0u;
+  }
+};
+// A wait of the whole warp, which stays together; the same answer in every lane. `quarter`: of the limit (the test hook).
+__device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site, bool teardown = false,
+                                                bool quarter = false) {
   // (the clock takes longer to read than most waits last: not before some tries)
   for (uint32_t it = 0; it < 1024u; ++it)
-    if (mbar_test(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  const uint32_t us = ab.status[3];
+  uint64_t limit = teardown ? kDrainLimitNs : (us ? uint64_t(us) * 1000ull : kWaitLimitNs);
+  if (quarter) limit /= 4;
   const uint64_t t0 = global_ns();
   while (true) {
-    if (honour_abort && *ab.flag) return false;
-    if (mbar_test(bar, parity)) return true;
-    if (global_ns() - t0 > limit) {
-      *ab.flag = 1u;
-      if (ab.status) atomicCAS(ab.status, 0u, (site << 8) | kDevTimeout);   // the first code stays
+    const bool done = mbar_test(bar, parity), out = global_ns() - t0 > limit;
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (__any_sync(0xffffffffu, !teardown && ab.raised())) return false;
+    if (__any_sync(0xffffffffu, out)) {
+      asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(ab.flag), "r"(1u) : "memory");
+      if (lane_id() == 0) atomicCAS(ab.status, 0u, (site << 8) | kDevTimeout);   // the first code stays
+      __syncwarp();
       return false;
     }
   }
 }
-__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
-  return __builtin_expect(lin_done(bar, parity), 1) || lin_wait_longer(bar, parity, ab, site, ab.limit_ns, true);
+__device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site) {
+  return __builtin_expect(__all_sync(0xffffffffu, lin_done(bar, parity)), 1) || lin_wait_longer(bar, parity, ab, site);
 }
-__device__ __forceinline__ void lin_drain(uint32_t bar, uint32_t parity, Abort ab, uint32_t site) {
-  if (!lin_done(bar, parity)) lin_wait_longer(bar, parity, ab, site, kDrainLimitNs, false);
+__device__ __forceinline__ void lin_drain(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site) {
+  if (!__all_sync(0xffffffffu, lin_done(bar, parity))) lin_wait_longer(bar, parity, ab, site, true);
 }
 
 // D (+)= A B^T. Of the operands' descriptors the low words differ from MMA to MMA, the high ones never.
@@ -201,7 +234,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kLinSmemRing + kLinSlack + kLinScales);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + kLinArea + kLinScales);
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kLinStages + s); };
@@ -209,11 +242,11 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   auto tempty = [&](int b) { return bar0 + 8u * (2 * kLinStages + kLinSlots + b); };
   auto sfull = [&](int g) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + g); };
   auto sempty = [&](int g) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + kScaleGroups + g); };
-  const uint32_t scales = base + kLinSmemRing + kLinSlack;
-  const uint32_t drain = bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups);
-  const uint32_t never = drain + 8u;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + 2);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
+  const uint32_t scales = base + kLinArea;
+  // delta's box i of an epilogue warp has come
+  auto came = [&](int w, int i) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + w * (kBoxesDelta - 1) + i); };
+  const uint32_t drain = bar0 + 8u * (kLinBars - 2), never = drain + 8u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kLinBars);
   // An accumulator of 256 columns is two slots, each filled by MMAs and read by four warps of its own.
   constexpr int kSub = W == 256 ? 2 : 1, kSlotCols = W * DEEP / kSub;
   constexpr int kSlots = 512 / kSlotCols < kLinSlots ? 512 / kSlotCols : kLinSlots;
@@ -236,12 +269,14 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       mbar_init(sfull(g), 1);
       mbar_init(sempty(g), kEpiWarps);
     }
+    for (int i = 0; i < kEpiWarps * (kBoxesDelta - 1); ++i) mbar_init(came(0, i), 1);
     mbar_init(drain, 1);
     mbar_init(never, 1);
-    *abort_flag = 0u;
+    tmem_slot[1] = 0u;                             // the abort flag
     mbar_fence_init();
     prefetch_map(&P.a);
     prefetch_map(&P.b);
+    if (W == 256 && P.boxes) prefetch_map(&P.o);
   }
   // (a pair meets before its joint TMEM allocation and after its freeing, as in gemm.cuh)
   __syncwarp();
@@ -255,7 +290,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
   grid_dependents_launch();
-  const Abort ab = make_abort(abort_flag, status);
+  const LinAbort ab{drain + 20u, status};
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   // a copied piece of MN-major B: kChunk columns of 128 rows of the weight, its swizzle span
   constexpr int kChunk = lin_chunk(W, CG);
@@ -265,7 +300,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   if (warp == 0) {
     // ------------------------------------------------------------ producer (gemm.cuh's)
     const bool one = elect_one();
-    if (stall_requested(status, kKindLinear + MODE) && one) lin_wait_longer(never, 0u, ab, kSiteLinear + 1, ab.limit_ns / 4, true);   // test hook
+    if (stall_requested(status, kKindLinear + MODE)) lin_wait_longer(never, 0u, ab, kSiteLinear + 1, false, true);   // test hook
     __syncwarp();
     const uint64_t pa = P.tiles_n > 1 ? policy_evict_last() : policy_normal(), pb = policy_normal();
     const uint32_t full0 = CG == 2 ? peer_addr(full(0), 0) : full(0);
@@ -277,7 +312,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       const int row0 = (w.tm * CG + rank) * kBM;           // this CTA's rows of A
       const int col0 = w.col + rank * (w.bn / 2);          // and columns (of a pair, half of the tile's)
       for (int kb = 0; kb < P.nk; kb += DEEP) {
-        if (!__all_sync(0xffffffffu, ready || lin_wait(empty(idx), phase ^ 1u, ab, kSiteLinear + 2))) goto given_up;
+        if (!__all_sync(0xffffffffu, ready) && !lin_wait(empty(idx), phase ^ 1u, ab, kSiteLinear + 2)) goto given_up;
         const uint32_t st0 = base + uint32_t(idx) * stage_bytes, bar = full0 + 8u * idx, here = full(idx);
         if (++idx == stages) idx = 0, phase ^= 1u;
         ready = lin_done(empty(idx), phase ^ 1u);
@@ -306,9 +341,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     for (uint32_t s = 0; s < uint32_t(stages) && s < issued; ++s) {
       const uint32_t parity = ((issued - 1u - s) / stages) & 1u;       // of the stage's last use
       if (rank == 0) lin_drain(full(s), parity, ab, kSiteLinear + 3);
-      if (!*ab.flag) lin_wait(empty(s), parity, ab, kSiteLinear + 8);
+      if (!ab.raised()) lin_wait(empty(s), parity, ab, kSiteLinear + 8);
     }
-    if (*ab.flag)
+    if (ab.raised())
       for (const uint64_t t0 = global_ns(); global_ns() - t0 < kDrainLimitNs;) {
       }
     __syncwarp();
@@ -330,13 +365,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       bool landed = false, free = true, ok = true;
       for (int u = first; u < P.total && ok; u += step) {
         for (int kb = 0; kb < P.nk; kb += DEEP) {
-          if (!__all_sync(0xffffffffu, landed)) ok = __all_sync(0xffffffffu, lin_wait(full(idx), phase, ab, kSiteLinear + 5));
+          if (!__all_sync(0xffffffffu, landed)) ok = lin_wait(full(idx), phase, ab, kSiteLinear + 5);
           if (!ok) break;
           const uint32_t off = uint32_t(idx) * stage_bytes, used = empty(idx);
           if (++idx == stages) idx = 0, phase ^= 1u;
 #pragma unroll
           for (int h = 0; h < kSub; ++h) {
-            if (!__all_sync(0xffffffffu, free)) ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4));
+            if (!__all_sync(0xffffffffu, free)) ok = lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4);
             if (!ok) break;
             tc_fence_after();
             if (one) {
@@ -353,6 +388,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
               commit<CG>(tfull(buf));
               if (h == kSub - 1) commit<CG>(used);
             }
+            __syncwarp();
             if (++buf == kSlots) buf = 0, tphase ^= 1u;
             free = lin_done(tempty(buf), tphase ^ 1u);
           }
@@ -370,8 +406,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       bool ok = true;
       for (int u = first; u < P.total && ok; u += step)
         for (int i = 0; i < P.nk * kSub && ok; ++i) {
-          ok = __all_sync(0xffffffffu, lin_wait(tempty(buf), tphase, ab, kSiteLinear + 11));
-          if (ok && lane == 0) lin_arrive_peer(peer_addr(tempty(buf), 0));
+          ok = lin_wait(tempty(buf), tphase, ab, kSiteLinear + 11);
+          lin_arrive_peer(peer_addr(tempty(buf), 0), ok && lane == 0);
           if (++buf == kSlots) buf = 0, tphase ^= 1u;
         }
     }
@@ -389,28 +425,32 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       for (int e = 0; e < 2; ++e) sb[e] = P.sb + min(w.col / 128 + e, (P.n - 1) / 128) * P.sb_out;
       for (int kb = 0; kb < P.nk && ok; kb += kScaleGroup, ++n) {
         if ((n & 1u) != (warp & 1u)) continue;
-        float a[kScaleGroup][4], b[kScaleGroup][2];
-#pragma unroll
-        for (int k = 0; k < kScaleGroup; ++k) {
-          const bool in = kb + k < P.nk;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) a[k][j] = in ? __ldg(P.sa + min(row0 + 32 * j, int64_t(P.m) - 1) * P.nk + kb + k) : 0.f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) b[k][e] = in ? __ldg(sb[e] + (kb + k) * P.sb_red) : 0.f;
-        }
-        const uint32_t g = n % kScaleGroups, at = scales + g * kScaleGroup * kScaleBytes + lane * 4;
-        ok = __all_sync(0xffffffffu, lin_wait(sempty(g), (n / kScaleGroups & 1u) ^ 1u, ab, kSiteLinear + 9));
+        const uint32_t g = n % kScaleGroups;
+        ok = lin_wait(sempty(g), (n / kScaleGroups & 1u) ^ 1u, ab, kSiteLinear + 9);
         if (!ok) break;
+        const uint32_t at = scales + g * kScaleGroup * kScaleBytes + lane * 4;
+#pragma unroll 1
+        for (int h = 0; h < kScaleGroup; h += 2) {
+          float a[2][4], b[2][2];
 #pragma unroll
-        for (int k = 0; k < kScaleGroup; ++k)
+          for (int k = 0; k < 2; ++k) {
+            const bool in = kb + h + k < P.nk;
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
+            for (int j = 0; j < 4; ++j) a[k][j] = in ? __ldg(P.sa + min(row0 + 32 * j, int64_t(P.m) - 1) * P.nk + kb + h + k) : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + k * kScaleBytes + e * kBM * 4 + j * 128), "f"(a[k][j] * b[k][e])
-                           : "memory");
+            for (int e = 0; e < 2; ++e) b[k][e] = in ? __ldg(sb[e] + (kb + h + k) * P.sb_red) : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + (h + k) * kScaleBytes + e * kBM * 4 + j * 128), "f"(a[k][j] * b[k][e])
+                             : "memory");
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(sfull(g));
+        lin_arrive(sfull(g), lane == 0);
       }
     }
   }
@@ -429,6 +469,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     auto scale_of = [](int i) { return W == 256 ? i / 64 * (CG - 1) : i * 2 / (W / 2); };
     int buf = kSub == 2 ? half : 0;
     uint32_t tphase = 0, n = 0;                    // groups of scales so far
+    const bool joins = W == 256 && P.boxes && P.delta;
+    const int boxes_each = lin_boxes(W, joins);
+    const uint32_t box0 = base + lin_ring(W, joins) + (warp - 4) * boxes_each * kBox;
+    uint32_t turn = 0, dphase = 0;
     for (int u = first; u < P.total; u += step) {
       const LinUnit w = lin_unit<CG>(P, u);
       const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32;
@@ -437,13 +481,31 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < kScales; ++e)
         block[e] = uint32_t((w.col + column(e * (W / 2) / kScales)) / 128 - w.col / 128) * (kBM * 4) + (q * 32 + lane) * 4;
+      // delta's box i (16 columns), into place i % 4; TMA fills what lies past its ends with zeros
+      auto load_delta = [&](int i) {
+        const uint32_t bar = came(warp - 4, i & 3);
+        if (lane == 0) {
+          mbar_expect_tx(bar, kBox);
+          tma_load(box0 + (i & 3) * kBox, &P.d, bar, w.col + column(16 * i), int(row0), policy_normal());
+        }
+      };
+      auto boxed = [&](int i) { return rows && w.col + column(16 * i) < P.n; };
+      if (joins) {
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          if (!boxed(i)) continue;
+          if (i < kBoxesDelta - 1) load_delta(i);
+          else if (lane == 0) tma_prefetch_l2(&P.d, w.col + column(16 * i), int(row0));
+        }
+      }
       float2 acc[kChunks * C / 2];
 #pragma unroll
       for (int i = 0; i < kChunks * C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       bool ok = true;
       for (int kb0 = 0; kb0 < P.nk; kb0 += kScaleGroup, ++n) {
         const uint32_t g = n % kScaleGroups, sg = scales + g * kScaleGroup * kScaleBytes;
-        ok = __all_sync(0xffffffffu, lin_wait(sfull(g), n / kScaleGroups & 1u, ab, kSiteLinear + 10)) && ok;
+        ok = lin_wait(sfull(g), n / kScaleGroups & 1u, ab, kSiteLinear + 10) && ok;
 #pragma unroll(DEEP)                               // (code that does not fit the instruction caches costs more)
         for (int k = 0; k < kScaleGroup; ++k) {
           if (kb0 + k >= P.nk) break;
@@ -453,13 +515,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[e]) : "r"(sg + k * kScaleBytes + block[e]) : "memory");
           const bool last = k % DEEP == DEEP - 1 || kb0 + k == P.nk - 1;       // of its slot
           if (k % DEEP == 0) {
-            ok = __all_sync(0xffffffffu, lin_wait(tfull(buf), tphase, ab, kSiteLinear + 7)) && ok;
+            ok = lin_wait(tfull(buf), tphase, ab, kSiteLinear + 7) && ok;
             tc_fence_after();
           }
           auto leave = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(tempty(buf));
+            lin_arrive(tempty(buf), ok && lane == 0);
             if ((buf += kSub) >= kSlots) buf -= kSlots, tphase ^= 1u;
           };
           if (ok && rows) {
@@ -482,16 +544,75 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
           }
         }
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(sempty(g));
+        lin_arrive(sempty(g), ok && lane == 0);
       }
-      if (ok && rows) {
+      if (W == 256 && P.boxes) {
+        // 16 columns at a time (64 bytes of fp32): delta's box is read, and its place filled with the one four on; a box is
+        // stored when it is full, every time or (bf16) every other.
+        uint32_t out = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (!boxed(i)) continue;
+          float2* a = acc + 8 * i;
+          if (joins) {
+            ok = lin_wait(came(warp - 4, i & 3), dphase >> (i & 3) & 1u, ab, kSiteLinear + 12) && ok;
+            dphase ^= 1u << (i & 3);
+            const uint32_t at = box0 + (i & 3) * kBox + lane * 64;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float4 v;
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                           : "r"(at + ((j ^ (lane >> 1 & 3)) << 4))
+                           : "memory");
+              a[2 * j].x += v.x; a[2 * j].y += v.y; a[2 * j + 1].x += v.z; a[2 * j + 1].y += v.w;
+            }
+            __syncwarp();
+            if (i < 4 && boxed(i + 4) && ok) load_delta(i + 4);
+          }
+          const bool first = P.out_f32 || i % 2 == 0, full = P.out_f32 || i % 2 == 1 || !boxed(i + 1);
+          if (first) {
+            if (joins) {
+              out = box0 + (kBoxesDelta - 1) * kBox;
+              if (lane == 0) tma_store_wait_read<0>();
+            } else {
+              out = box0 + turn * kBox;
+              turn = turn == kBoxesPlain - 1 ? 0 : turn + 1;
+              if (lane == 0) tma_store_wait_read<kBoxesPlain - 1>();
+            }
+            __syncwarp();
+          }
+          if (P.out_f32) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)),
+                           "f"(a[2 * j].x), "f"(a[2 * j].y), "f"(a[2 * j + 1].x), "f"(a[2 * j + 1].y)
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + (((2 * (i & 1) + j) ^ (lane >> 1 & 3)) << 4)),
+                           "r"(bf16x2_bits(a[4 * j].x, a[4 * j].y)), "r"(bf16x2_bits(a[4 * j + 1].x, a[4 * j + 1].y)),
+                           "r"(bf16x2_bits(a[4 * j + 2].x, a[4 * j + 2].y)), "r"(bf16x2_bits(a[4 * j + 3].x, a[4 * j + 3].y))
+                           : "memory");
+          }
+          if (full) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+              if (ok) tma_store(&P.o, out, w.col + column(P.out_f32 ? 16 * i : 16 * (i & ~1)), int(row0), policy_normal());
+              tma_store_commit();
+            }
+          }
+        }
+      } else if (ok && rows) {
         const int end = min(P.n, w.col + w.bn);
-        const uint32_t box = base + kLinSmemRing + (warp - 4) * 2048;
 #pragma unroll
         for (int i = 0; i < kChunks * C; i += 16)
-          if (column(i) < w.bn) lin_store16(P, box, row0, w.col + column(i), end, acc + i / 2, lane);
+          if (column(i) < w.bn) lin_store16(P, box0, row0, w.col + column(i), end, acc + i / 2, lane);
       }
     }
+    if (W == 256 && lane == 0) tma_store_wait_all<0>();
   }
 
   __syncwarp();
