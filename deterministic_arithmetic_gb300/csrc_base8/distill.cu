@@ -84,6 +84,31 @@ struct Held {
       }
     }
   }
+  // Element e becomes -infinity.
+  __device__ __forceinline__ void drop(int e) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (KIND == kF32) {
+        if (i == e) w[i] = 0xFF800000u;
+      } else {
+        const uint32_t hit = i == e / 2 ? (e & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+        w[i] = (w[i] & ~hit) | (0xFF80FF80u & hit);
+      }
+    }
+  }
+  // The largest (NaN passed over); of bf16 values by pairs.
+  __device__ __forceinline__ float largest() const {
+    if constexpr (KIND == kF32) {
+      float m = __uint_as_float(w[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+      return m;
+    } else {
+      const auto pair = [](uint32_t v) { return *reinterpret_cast<const __nv_bfloat162*>(&v); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(pair(w[0]), pair(w[1])), __hmax2(pair(w[2]), pair(w[3])));
+      return fmaxf(__low2float(m), __high2float(m));
+    }
+  }
   // The values, rounded once, to the same elements.
   static __device__ __forceinline__ void store(void* p, int64_t base, int n, int lane, const float (&v)[8]) {
     if constexpr (KIND == kBf16 && VEC == 8) {
@@ -113,6 +138,22 @@ struct Held {
   static __device__ __forceinline__ int lane_of(int o) { return (o / VEC) & 31; }
   static __device__ __forceinline__ int elem_of(int o) { return o / (32 * VEC) * VEC + o % VEC; }
 };
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 
 struct DistillArgs {
   const void *z, *ids, *teacher;
@@ -191,6 +232,17 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
     }
     return;
   }
+  // The groups of a warp in one sequence q: place q % kOwn of round q / kOwn. As one is taken in, the one kLoads on is sent for; the
+  // first are on their way while the entries' lists are made.
+  const int64_t base = row * P.V;
+  const int rounds = (P.groups + kPlaces * kWarps - 1) / (kPlaces * kWarps), whole = P.V / (kPlaces * kWarps * kGroupElems);
+  const auto group = [&](int q) { return q / kOwn * (kPlaces * kWarps) + (CL * (q % kOwn) + rank) * kWarps + warp; };
+  Held<KIND, VEC> held[kLoads];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int g = group(k);
+    held[k].load(P.z, base + int64_t(g) * kGroupElems, P.V - g * kGroupElems, lane);
+  }
   for (int g = tid; g < P.groups; g += kThreads) L.head[g] = -1;
   __syncthreads();
   for (int i = tid; i < P.top; i += kThreads) {
@@ -223,49 +275,46 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
   Part own[kOwn];
 #pragma unroll
   for (int j = 0; j < kOwn; ++j) own[j] = {-kInf, 0.f};
-  // group of place j of this CTA in round r: (64 r) + (CL j + rank) 8 + warp. Rounds x places in one sequence.
-  const int64_t base = row * P.V;
-  const int rounds = (P.groups + kPlaces * kWarps - 1) / (kPlaces * kWarps);
   constexpr int kBatch = kOwn > kLoads ? kOwn : kLoads;
-  for (int q0 = 0; q0 < rounds * kOwn; q0 += kBatch) {
+  const auto take = [&](Held<KIND, VEC>& v, Part& p, int g) {
+    for (int i = L.head[g]; i >= 0; i = L.next[i]) {           // entries are no part of the rest
+      const int o = L.id[i] - g * kGroupElems;
+      if (Held<KIND, VEC>::lane_of(o) == lane) v.drop(Held<KIND, VEC>::elem_of(o));
+    }
+    const float m = v.largest();
+    if (m > p.m) {
+      p.s = rescale(p.s, p.m, m, c);
+      p.m = m;
+    }
+    const float ref = p.m == -kInf ? 0.f : p.m;               // nothing but -infinity so far: all terms are 0
+    float x[8];
+    v.get(x);
+    float2 y[4];
 #pragma unroll
-    for (int h = 0; h < kBatch; h += kLoads) {
-      Held<KIND, VEC> held[kLoads];
+    for (int e = 0; e < 4; ++e) {
+      y[e] = mul2(add2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(-ref, -ref)), make_float2(c, c));
+      y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+    }
+    const float2 t = add2(add2(y[0], y[1]), add2(y[2], y[3]));
+    p.s += t.x + t.y;
+  };
+  int q0 = 0;
+  for (; (q0 + kBatch + kLoads) <= whole * kOwn; q0 += kBatch) {       // whole groups only, the ones sent for too
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int qq = q0 + h + k, j = (h + k) % kOwn;
-        const int g = qq / kOwn * (kPlaces * kWarps) + (CL * j + rank) * kWarps + warp;
-        held[k].load(P.z, base + int64_t(g) * kGroupElems, P.V - g * kGroupElems, lane);
-      }
+    for (int k = 0; k < kBatch; ++k) {
+      Held<KIND, VEC>& v = held[k % kLoads];
+      take(v, own[k % kOwn], group(q0 + k));
+      v.load(P.z, base + int64_t(group(q0 + k + kLoads)) * kGroupElems, kGroupElems, lane);
+    }
+  }
+#pragma unroll 1
+  for (; q0 < rounds * kOwn; q0 += kBatch) {
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int qq = q0 + h + k, j = (h + k) % kOwn;
-        const int g = qq / kOwn * (kPlaces * kWarps) + (CL * j + rank) * kWarps + warp;
-        if (g >= P.groups) continue;
-        float x[8];
-        held[k].get(x);
-        for (int i = L.head[g]; i >= 0; i = L.next[i]) {       // entries are no part of the rest
-          const int o = L.id[i] - g * kGroupElems, e0 = Held<KIND, VEC>::elem_of(o);
-          if (Held<KIND, VEC>::lane_of(o) == lane) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e == e0) x[e] = -kInf;
-          }
-        }
-        float m = x[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) m = fmaxf(m, x[e]);
-        Part& p = own[j];
-        if (m > p.m) {
-          p.s = rescale(p.s, p.m, m, c);
-          p.m = m;
-        }
-        const float ref = p.m == -kInf ? 0.f : p.m;           // nothing but -infinity so far: all terms are 0
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = ex2((x[e] - ref) * c);
-        p.s += ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-      }
+    for (int k = 0; k < kBatch; ++k) {
+      const int g = group(q0 + k), next = group(q0 + k + kLoads);
+      Held<KIND, VEC>& v = held[k % kLoads];
+      if (g < P.groups) take(v, own[k % kOwn], g);
+      v.load(P.z, base + int64_t(next) * kGroupElems, P.V - next * kGroupElems, lane);
     }
   }
 

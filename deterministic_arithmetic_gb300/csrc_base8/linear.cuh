@@ -302,7 +302,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     const bool one = elect_one();
     if (stall_requested(status, kKindLinear + MODE)) lin_wait_longer(never, 0u, ab, kSiteLinear + 1, false, true);   // test hook
     __syncwarp();
-    const uint64_t pa = P.tiles_n > 1 ? policy_evict_last() : policy_normal(), pb = policy_normal();
+    // (of one row of tiles each byte of the weight is read once: 1 x 5120 <- 17408 25.7 -> 24.4 us)
+    const uint64_t pa = P.tiles_n > 1 ? policy_evict_last() : policy_normal();
+    const uint64_t pb = P.tiles_m > 1 ? policy_normal() : policy_evict_first();
     const uint32_t full0 = CG == 2 ? peer_addr(full(0), 0) : full(0);
     int idx = 0;
     uint32_t phase = 0, issued = 0;
