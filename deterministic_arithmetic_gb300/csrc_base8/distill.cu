@@ -5,14 +5,17 @@
 // relative to it, of everything that is no entry of the teacher's; the row's few entries are read on their own, and
 // their part joined at the end. So the mass of the rest is a sum, and no difference. Bound by HBM.
 //
-// A row is cut into groups of 256 elements, dealt in turn to 64 places (8 of a CTA's 8 warps each); each
-// thread of a place holds a maximum and a sum of its own, and the places' are joined in a fixed order. A batch of
+// A row is cut into groups of 256 elements, dealt in turn to the places of eight warps (1, 2, 4 or 8 each, by the row's length
+// alone); each thread of a place holds a maximum and a sum of its own, and the places' are joined in a fixed order. A batch of
 // few rows has its rows' places spread over the CTAs of a cluster: the places, and so the bits, stay the same.
 #include "../csrc/common.cuh"
 #include "../csrc/kernels.h"
 #include "../csrc_mlp/elems.cuh"
 #include "base8.h"
 #include "block8.cuh"
+
+#include <algorithm>
+#include <type_traits>
 
 namespace mlp {
 namespace {
@@ -29,47 +32,120 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// What a thread holds of a group of 256 elements of its warp: 8 of them, in pieces of VEC consecutive ones, 32 VEC apart. VEC
-// is what rows of V elements allow (16 bytes where whole vectors fit a row).
-template <int KIND, int VEC>
+// 8 bf16 elements from element `first` on (in pairs) of the 16 in u.
+__device__ __forceinline__ void shifted(uint32_t (&u)[8], int first, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 6; ++i) u[i] = first & 4 ? u[i + 2] : u[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) u[i] = first & 2 ? u[i + 1] : u[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(u[i], u[i + 1], first & 1 ? 16 : 0);
+}
+
+// What a thread holds of a group of 256 elements of its warp: 8 of them, in pieces of VEC consecutive ones, 32 VEC apart:
+// one of 8 (bf16), two of 4 (fp32), or (fp32 rows of odd lengths) single ones. SHIFT: bf16 rows whose length is no multiple of
+// 8 start at any element; their pieces are put together from the two 16-byte vectors that hold them (loads of 2 bytes took
+// 4096 x 50257 forward 201 us, SHIFTFIG so, and 405 backward, SHIFTBWD).
+template <int KIND, int VEC, bool SHIFT>
 struct Held {
+  static_assert(KIND == kF32 ? !SHIFT : VEC == 8, "");
   static constexpr int kWords = KIND == kF32 ? 8 : 4;
-  uint32_t w[kWords];
+  uint32_t w[SHIFT ? 8 : kWords];                  // SHIFT: the two vectors, until settle()
   static __device__ __forceinline__ int at(int e, int lane) { return (e / VEC) * 32 * VEC + lane * VEC + e % VEC; }
-  // Elements of the group at p, of which `n` exist; the others are -infinity.
-  __device__ __forceinline__ void load(const void* p, int64_t base, int n, int lane) {
-    if constexpr (KIND == kBf16 && VEC == 8) {
-      if (8 * lane < n) {
-        const uint4 t = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + base + 8 * lane);
-        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
-      } else {
-        w[0] = w[1] = w[2] = w[3] = 0xFF80FF80u;
+  // The lane's first byte of a group that starts at element `base` (SHIFT: of the vector that holds it).
+  static __device__ __forceinline__ const uint8_t* place(const void* p, int64_t base, int off, int lane) {
+    constexpr int kBytes = KIND == kF32 ? 4 : 2;
+    return static_cast<const uint8_t*>(p) + (base - off + lane * VEC) * kBytes;
+  }
+  // Elements of the group whose lane's place is `at`, of which n exist (the others stay what they were). off: the row's first
+  // element % 8. edge: nothing lies behind the row's end.
+  __device__ __forceinline__ void load_whole(const uint8_t* at, int off) {
+    if constexpr (KIND == kBf16) {
+      uint4 t = *reinterpret_cast<const uint4*>(at);
+      w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+      if constexpr (SHIFT) {
+        if (off) {
+          t = *reinterpret_cast<const uint4*>(at + 16);
+          w[4] = t.x; w[5] = t.y; w[6] = t.z; w[7] = t.w;
+        }
       }
-    } else if constexpr (KIND == kBf16 && VEC == 2) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = 64 * j + 2 * lane < n
-                   ? *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p) + base + 64 * j + 2 * lane)
-                   : 0xFF80FF80u;
-    } else if constexpr (KIND == kBf16) {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + base + lane;
-      uint32_t h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = 32 * j + lane < n ? q[32 * j] : 0xFF80u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = h[2 * j] | (h[2 * j + 1] << 16);
     } else if constexpr (VEC == 4) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float4 t = make_float4(-kInf, -kInf, -kInf, -kInf);
-        if (128 * j + 4 * lane < n) t = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + base + 128 * j + 4 * lane);
+        const float4 t = *reinterpret_cast<const float4*>(at + 512 * j);
         w[4 * j] = __float_as_uint(t.x); w[4 * j + 1] = __float_as_uint(t.y);
         w[4 * j + 2] = __float_as_uint(t.z); w[4 * j + 3] = __float_as_uint(t.w);
       }
     } else {
-      const float* q = static_cast<const float*>(p) + base + lane;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(32 * j + lane < n ? q[32 * j] : -kInf);
+      for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint32_t*>(at + 128 * j);
+    }
+  }
+  __device__ __forceinline__ void load(const uint8_t* at, int off, int n, bool edge, int lane) {
+    if constexpr (KIND == kBf16 && !SHIFT) {
+      if (8 * lane < n) {
+        const uint4 t = *reinterpret_cast<const uint4*>(at);
+        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+      }
+    } else if constexpr (KIND == kBf16) {
+      // elements of the row from the first and from the second vector's start on
+      const int n0 = n + off - 8 * lane, n1 = n0 - 8;
+      uint4 t;
+      if (n0 > off) {
+        t = !edge || n0 >= 8 ? *reinterpret_cast<const uint4*>(at) : some(at, n0);
+        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+      }
+      if (off && n1 > 0) {
+        t = !edge || n1 >= 8 ? *reinterpret_cast<const uint4*>(at + 16) : some(at + 16, n1);
+        w[4] = t.x; w[5] = t.y; w[6] = t.z; w[7] = t.w;
+      }
+    } else if constexpr (VEC == 4) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (128 * j + 4 * lane < n) {
+          const float4 t = *reinterpret_cast<const float4*>(at + 512 * j);
+          w[4 * j] = __float_as_uint(t.x); w[4 * j + 1] = __float_as_uint(t.y);
+          w[4 * j + 2] = __float_as_uint(t.z); w[4 * j + 3] = __float_as_uint(t.w);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (32 * j + lane < n) w[j] = *reinterpret_cast<const uint32_t*>(at + 128 * j);
+    }
+  }
+  // The first n elements of a vector that does not lie in the tensor whole.
+  static __device__ __noinline__ uint4 some(const uint8_t* at, int n) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(at);
+    uint32_t t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = (2 * i < n ? uint32_t(q[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(q[2 * i + 1]) << 16 : 0u);
+    return make_uint4(t[0], t[1], t[2], t[3]);
+  }
+  // Makes the elements themselves of what load() brought.
+  __device__ __forceinline__ void settle(int off) {
+    if constexpr (SHIFT) {
+      uint32_t t[4];
+      shifted(w, off, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = t[i];
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = KIND == kF32 ? 0xFF800000u : 0xFF80FF80u;
+  }
+  // -infinity where the row has no more elements.
+  __device__ __forceinline__ void end(int n, int lane) {
+    if constexpr (KIND == kF32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (at(e, lane) >= n) w[e] = 0xFF800000u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (at(2 * i, lane) >= n) w[i] = 0xFF80FF80u;
+        else if (at(2 * i + 1, lane) >= n) w[i] = (w[i] & 0xFFFFu) | 0xFF800000u;
+      }
     }
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -84,14 +160,17 @@ struct Held {
       }
     }
   }
-  // Element e becomes -infinity.
-  __device__ __forceinline__ void drop(int e) {
+  // The group's element o (0 to 255) becomes -infinity, where the lane has it.
+  __device__ __forceinline__ void drop(uint32_t o, uint32_t lane) {
+    if constexpr (KIND == kF32) {
+      const uint32_t e = (o / VEC % 32 == lane) ? o / (32 * VEC) * VEC + o % VEC : 8u;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      if constexpr (KIND == kF32) {
-        if (i == e) w[i] = 0xFF800000u;
-      } else {
-        const uint32_t hit = i == e / 2 ? (e & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+      for (int i = 0; i < 8; ++i) w[i] = e == uint32_t(i) ? 0xFF800000u : w[i];
+    } else {
+      const uint32_t half = o / 8 == lane ? (o & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u, word = o / 2 % 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t hit = word == uint32_t(i) ? half : 0u;
         w[i] = (w[i] & ~hit) | (0xFF80FF80u & hit);
       }
     }
@@ -109,19 +188,32 @@ struct Held {
       return fmaxf(__low2float(m), __high2float(m));
     }
   }
-  // The values, rounded once, to the same elements.
-  static __device__ __forceinline__ void store(void* p, int64_t base, int n, int lane, const float (&v)[8]) {
-    if constexpr (KIND == kBf16 && VEC == 8) {
-      if (8 * lane < n) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + base + 8 * lane) = pack_bf16x8(v);
-    } else if constexpr (KIND == kBf16 && VEC == 2) {
+  // The values, rounded once, to the same elements. (The whole warp calls.)
+  static __device__ __forceinline__ void store(void* p, int64_t base, int off, int n, int lane, const float (&v)[8]) {
+    if constexpr (KIND == kBf16) {
+      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + base;
+      const uint4 own = pack_bf16x8(v);
+      if constexpr (!SHIFT) {
+        if (8 * lane < n) *reinterpret_cast<uint4*>(q + 8 * lane) = own;
+      } else if (off == 0 && n >= kGroupElems) {
+        *reinterpret_cast<uint4*>(q + 8 * lane) = own;
+      } else {
+        // a whole vector of memory is the last `off` elements of the lane before and this lane's first; the group's ends are single
+        uint32_t u[8] = {__shfl_up_sync(0xffffffffu, own.x, 1), __shfl_up_sync(0xffffffffu, own.y, 1),
+                         __shfl_up_sync(0xffffffffu, own.z, 1), __shfl_up_sync(0xffffffffu, own.w, 1), own.x, own.y, own.z, own.w};
+        const uint32_t mine[4] = {own.x, own.y, own.z, own.w};
+        uint32_t w[4];
+        shifted(u, 8 - off, w);
+        const bool whole = n >= kGroupElems;
+        if (whole && lane > 0) *reinterpret_cast<uint4*>(q + 8 * lane - off) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (!whole || lane == 0 || lane == 31) {
+          const int lo = whole && lane == 31 ? 8 - off : 0, hi = whole && lane == 0 ? 8 - off : 8;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (64 * j + 2 * lane < n)
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p) + base + 64 * j + 2 * lane) = bf16x2_bits(v[2 * j], v[2 * j + 1]);
-    } else if constexpr (KIND == kBf16) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (32 * j + lane < n) static_cast<__nv_bfloat16*>(p)[base + 32 * j + lane] = __float2bfloat16_rn(v[j]);
+          for (int e = 0; e < 8; ++e)
+            if (e >= lo && e < hi && 8 * lane + e < n)
+              reinterpret_cast<uint16_t*>(q)[8 * lane + e] = uint16_t(e & 1 ? mine[e / 2] >> 16 : mine[e / 2]);
+        }
+      }
     } else if constexpr (VEC == 4) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
@@ -134,9 +226,10 @@ struct Held {
         if (32 * j + lane < n) static_cast<float*>(p)[base + 32 * j + lane] = v[j];
     }
   }
-  // Of the lane and element that hold the group's element o.
-  static __device__ __forceinline__ int lane_of(int o) { return (o / VEC) & 31; }
-  static __device__ __forceinline__ int elem_of(int o) { return o / (32 * VEC) * VEC + o % VEC; }
+  // Which of the lane's elements is the group's element o; 8: none.
+  static __device__ __forceinline__ uint32_t elem_of(uint32_t o, uint32_t lane) {
+    return o / VEC % 32 == lane ? o / (32 * VEC) * VEC + o % VEC : 8u;
+  }
 };
 
 // Two fp32 operations in one instruction.
@@ -155,12 +248,21 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 struct DistillArgs {
   const void *z, *ids, *teacher;
   const float *teacher_lse, *weight, *dloss;
   int id8, teacher_type;           // ids in 64 bits; the teacher's type
   int64_t M;
-  int V, top, groups;              // groups of 256 elements of a row
+  int V, top, groups, places;      // groups of 256 elements of a row; forward: places of a warp
   float temperature;
   float *loss, *probs, *stats;
   void* dz;
@@ -177,13 +279,15 @@ __device__ __forceinline__ int id_at(const DistillArgs& P, int64_t i) {
   const int v = __ldg(static_cast<const int*>(P.ids) + i);
   return v >= 0 && v < P.V ? v : -1;
 }
-__device__ __forceinline__ float logit_at(const DistillArgs& P, int kind, int64_t i) { return param_at(P.z, kind, i); }
 
-// The entries of a row by group: head[g] the first of group g, next[i] the one after entry i, -1 at the end. The
-// order within a group is no fixed one; nothing depends on it.
+// The entries of a row by group: head[g] the first of group g, link[i] the one after entry i, -1 at the end, and its id (-1 where
+// it is none). The order within a group is no fixed one; nothing depends on it.
 struct Lists {
-  int *head, *next, *id;           // shared memory: groups, top, top
+  int* head;                       // shared memory: groups
+  int2* link;                      // top of (the next one, id)
 };
+
+__host__ __device__ constexpr int even(int n) { return (n + 1) & ~1; }
 
 // The sum (maximum) over a warp, in a fixed order; every lane has it.
 __device__ __forceinline__ float warp_sum(float v) {
@@ -206,147 +310,64 @@ __device__ __forceinline__ float rescale(float s, float from, float to, float c)
   return from == -kInf && s == 0.f ? 0.f : s * ex2((from - to) * c);
 }
 
+#ifndef FMIN
+#define FMIN 3
+#define FLOADS 8
+#define BMIN 5
+#define BLOADS 4
+#endif
+// CTAs of an SM.
+template <int KIND, bool SHIFT>
+constexpr int kMinCtas = KIND == kF32 || SHIFT ? 2 : FMIN;
+
 // ----------------------------------------------------------------- forward
-// CL: CTAs of a row's cluster. Of the 8 places of a thread, CTA r has those congruent to r.
-template <int KIND, int VEC, int CL>
-__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_kernel(const __grid_constant__ DistillArgs P) {
-  constexpr int kOwn = kPlaces / CL;               // places of a thread of this CTA
-  constexpr int kLoads = KIND == kF32 ? 4 : 8;     // groups of a warp in flight
-  extern __shared__ int smem[];
-  __shared__ Part sent[CL > 1 ? kPlaces : 1][CL > 1 ? kThreads : 1];    // what the cluster's CTAs send to the first
-  __shared__ Part warps[kWarps];
-  const Lists L{smem, smem + P.groups, smem + P.groups + P.top};
-  float* tl = reinterpret_cast<float*>(L.id + P.top);      // the entries' teacher logits; -infinity where dropped
-  float* zl = tl + P.top;                                  // and student logits
-  const int lane = int(lane_id()), warp = int(warp_id()), tid = int(threadIdx.x);
-  const int rank = CL > 1 ? int(cluster_rank()) : 0;
-  const int64_t row = blockIdx.x / CL;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  const float weight = P.weight ? __ldg(P.weight + row) : 1.f;
-  if (weight == 0.f) {                             // the same in every CTA of the cluster
-    if (rank == 0) {
-      for (int i = tid; i < P.top; i += kThreads) P.probs[row * P.top + i] = -1.f;
-      if (tid < 4) P.stats[row * 4 + tid] = 0.f;
-      if (tid == 0) P.loss[row] = 0.f;
-    }
-    return;
-  }
-  // The groups of a warp in one sequence q: place q % kOwn of round q / kOwn. As one is taken in, the one kLoads on is sent for; the
-  // first are on their way while the entries' lists are made.
-  const int64_t base = row * P.V;
-  const int rounds = (P.groups + kPlaces * kWarps - 1) / (kPlaces * kWarps), whole = P.V / (kPlaces * kWarps * kGroupElems);
-  const auto group = [&](int q) { return q / kOwn * (kPlaces * kWarps) + (CL * (q % kOwn) + rank) * kWarps + warp; };
-  Held<KIND, VEC> held[kLoads];
-#pragma unroll
-  for (int k = 0; k < kLoads; ++k) {
-    const int g = group(k);
-    held[k].load(P.z, base + int64_t(g) * kGroupElems, P.V - g * kGroupElems, lane);
-  }
-  for (int g = tid; g < P.groups; g += kThreads) L.head[g] = -1;
-  __syncthreads();
-  for (int i = tid; i < P.top; i += kThreads) {
+// A CTA has eight warps that stream its rows, and a ninth for their entries: it makes the lists of the next row and ends the one
+// before while the others stream. (With all warps at a row's entries first and one at its end, a row of 4096 x 131072 took
+// 5 us beside its 18 of streaming.) The loads run on from row to row.
+constexpr int kFwdThreads = kThreads + 32;
+constexpr uint32_t kBarLists = 1, kBarParts = 3;   // named barriers, two of each: rows in turn
+
+__device__ __forceinline__ void bar_arrive(uint32_t id) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kFwdThreads) : "memory"); }
+
+// What the ninth warp makes of a row's entries.
+struct Row {
+  Lists lists;
+  float *t, *z;                    // the entries' teacher logits, -infinity where dropped; and student logits
+};
+
+// The lists, of all lanes. Logits only where they are wanted (the cluster's first CTA).
+__device__ __forceinline__ void make_lists(const DistillArgs& P, const Row& r, int kind, int64_t row, bool logits, int lane) {
+  const Lists& L = r.lists;
+  for (int g = lane; g < P.groups; g += 32) L.head[g] = -1;
+  __syncwarp();
+#pragma unroll 2
+  for (int i = lane; i < P.top; i += 32) {
     const int64_t at = row * P.top + i;
     int id = id_at(P, at);
     const float t = param_at(P.teacher, P.teacher_type, at);
     if (t == -kInf) id = -1;
-    L.id[i] = id;
-    tl[i] = id < 0 ? -kInf : t;
-    if (id >= 0) {
-      L.next[i] = atomicExch(&L.head[id / kGroupElems], i);
-      if (rank == 0) zl[i] = logit_at(P, KIND, row * P.V + id);
-    }
+    r.t[i] = id < 0 ? -kInf : t;
+    L.link[i] = make_int2(id < 0 ? -1 : atomicExch(&L.head[id / kGroupElems], i), id);
+    if (id >= 0 && logits) r.z[i] = param_at(P.z, kind, row * P.V + id);
   }
-  if constexpr (CL > 1) cluster_sync_all();        // (every CTA of the cluster runs: its shared memory may be written)
-  else __syncthreads();
+  __syncwarp();
   // of several entries of one id the first counts
-  if (rank == 0)
-    for (int i = tid; i < P.top; i += kThreads) {
-      const int id = L.id[i];
-      if (id < 0) continue;
-      for (int j = L.head[id / kGroupElems]; j >= 0; j = L.next[j])
-        if (j < i && L.id[j] == id) {
-          tl[i] = -kInf;
-          break;
-        }
-    }
+  for (int i = lane; i < P.top; i += 32) {
+    const int id = L.link[i].y;
+    if (id < 0) continue;
+    for (int j = L.head[id / kGroupElems]; j >= 0; j = L.link[j].x)
+      if (j < i && L.link[j].y == id) {
+        r.t[i] = -kInf;
+        break;
+      }
+  }
+  __syncwarp();
+}
 
+// The row's end, from the eight warps' parts: of one warp.
+__device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, const Part* warps, int64_t row, float weight, int lane) {
   const float c = kLog2e / P.temperature;
-  Part own[kOwn];
-#pragma unroll
-  for (int j = 0; j < kOwn; ++j) own[j] = {-kInf, 0.f};
-  constexpr int kBatch = kOwn > kLoads ? kOwn : kLoads;
-  const auto take = [&](Held<KIND, VEC>& v, Part& p, int g) {
-    for (int i = L.head[g]; i >= 0; i = L.next[i]) {           // entries are no part of the rest
-      const int o = L.id[i] - g * kGroupElems;
-      if (Held<KIND, VEC>::lane_of(o) == lane) v.drop(Held<KIND, VEC>::elem_of(o));
-    }
-    const float m = v.largest();
-    if (m > p.m) {
-      p.s = rescale(p.s, p.m, m, c);
-      p.m = m;
-    }
-    const float ref = p.m == -kInf ? 0.f : p.m;               // nothing but -infinity so far: all terms are 0
-    float x[8];
-    v.get(x);
-    float2 y[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y[e] = mul2(add2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(-ref, -ref)), make_float2(c, c));
-      y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
-    }
-    const float2 t = add2(add2(y[0], y[1]), add2(y[2], y[3]));
-    p.s += t.x + t.y;
-  };
-  int q0 = 0;
-  for (; (q0 + kBatch + kLoads) <= whole * kOwn; q0 += kBatch) {       // whole groups only, the ones sent for too
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      Held<KIND, VEC>& v = held[k % kLoads];
-      take(v, own[k % kOwn], group(q0 + k));
-      v.load(P.z, base + int64_t(group(q0 + k + kLoads)) * kGroupElems, kGroupElems, lane);
-    }
-  }
-#pragma unroll 1
-  for (; q0 < rounds * kOwn; q0 += kBatch) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int g = group(q0 + k), next = group(q0 + k + kLoads);
-      Held<KIND, VEC>& v = held[k % kLoads];
-      if (g < P.groups) take(v, own[k % kOwn], g);
-      v.load(P.z, base + int64_t(next) * kGroupElems, P.V - next * kGroupElems, lane);
-    }
-  }
-
-  // the thread's places, in order; then the warp's lanes, the warps
-  Part all[kPlaces];
-  if constexpr (CL > 1) {
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-      const uint32_t at = peer_addr(smem_u32(&sent[CL * j + rank][tid]), 0);
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(own[j].m), "f"(own[j].s) : "memory");
-    }
-    cluster_sync_all();
-    if (rank != 0) return;
-#pragma unroll
-    for (int j = 0; j < kPlaces; ++j) all[j] = sent[j][tid];
-  } else {
-#pragma unroll
-    for (int j = 0; j < kPlaces; ++j) all[j] = own[j];
-  }
-  Part t = all[0];
-#pragma unroll
-  for (int j = 1; j < kPlaces; ++j) t.m = fmaxf(t.m, all[j].m);
-  t.m = warp_max(t.m);
-  t.s = 0.f;
-#pragma unroll
-  for (int j = 0; j < kPlaces; ++j) t.s += rescale(all[j].s, all[j].m, t.m, c);
-  t.s = warp_sum(t.s);
-  if (lane == 0) warps[warp] = t;
-  __syncthreads();
-  if (warp != 0) return;
-
-  // ---- the row's end, one warp. The rest of the vocabulary:
+  // the rest of the vocabulary
   Part rest = warps[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) rest.m = fmaxf(rest.m, warps[w].m);
@@ -357,41 +378,48 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
   float zm = -kInf, tm = -kInf;
   bool any = false;
   for (int i = lane; i < P.top; i += 32)
-    if (tl[i] != -kInf) {
+    if (r.t[i] != -kInf) {
       any = true;
-      zm = fmaxf(zm, zl[i]);
-      tm = fmaxf(tm, tl[i]);
+      zm = fmaxf(zm, r.z[i]);
+      tm = fmaxf(tm, r.t[i]);
     }
   any = __any_sync(0xffffffffu, any);
   zm = warp_max(zm);
   tm = warp_max(tm);
+  // (without the teacher's mass of the rest nobody asks for the student's: the stream then has the entries too)
   const float m = fmaxf(rest.m, zm);
   float s_top = 0.f, s_teacher = 0.f;
   for (int i = lane; i < P.top; i += 32)
-    if (tl[i] != -kInf) {
-      s_top += ex2((zl[i] - m) * c);
-      s_teacher += ex2((tl[i] - tm) * c);
+    if (r.t[i] != -kInf) {
+      s_top += ex2((r.z[i] - m) * c);
+      s_teacher += ex2((r.t[i] - tm) * c);
     }
   s_top = warp_sum(s_top);
   s_teacher = warp_sum(s_teacher);
-  const float s_rest = rescale(rest.s, rest.m, m, c), s = s_rest + s_top;
+  const float s_rest = rescale(rest.s, rest.m, m, c), s = P.teacher_lse ? s_rest + s_top : s_rest;
   // log p - log q = (t - z) / T - (norm - log sum exp(z / T)): a difference of an entry's own two logits, and one of the
-  // row's, taken in 64 bits. The terms of a small divergence cancel, and so keep their digits.
-  const float inv_t = 1.f / P.temperature, log_s = logf(s);
-  const float lse = P.teacher_lse ? __ldg(P.teacher_lse + row) : 0.f, log_t = logf(s_teacher);
-  const double it = 1.0 / double(P.temperature);
-  const float gap = float((P.teacher_lse ? double(lse) : double(tm) * it + double(log_t)) - (double(m) * it + double(log_s)));
-  const float it_lo = float(it - double(inv_t));
+  // row's. The terms of a small divergence cancel, and so keep their digits: what a product or 1 / T leaves is carried along.
+  const float inv_t = 1.f / P.temperature, inv_lo = fmaf(-P.temperature, inv_t, 1.f) * inv_t;
+  const float log_s = logf(s), log_t = logf(s_teacher), lse = P.teacher_lse ? __ldg(P.teacher_lse + row) : 0.f;
+  // (v / T as a float and its rest)
+  const auto over_t = [&](float v, float* lo) {
+    const float h = v * inv_t;
+    *lo = fmaf(v, inv_t, -h) + v * inv_lo;
+    return h;
+  };
+  float m_lo;
+  const float m_hi = over_t(m, &m_lo);
+  const float gap = P.teacher_lse ? ((lse - m_hi) - m_lo) - log_s : fmaf(tm - m, inv_t, log_t - log_s);
   float sum_p = 0.f, loss = 0.f;
   for (int i = lane; i < P.top; i += 32) {
-    const float ti = tl[i];
+    const float ti = r.t[i];
     float p = -1.f;
     if (ti != -kInf) {
-      // t / T - lse by an exact product and its rest; (t - the largest t) / T - log of the sum
-      const float h = ti * inv_t, rest_h = fmaf(ti, inv_t, -h) + ti * it_lo;
-      p = expf(P.teacher_lse ? (h - lse) + rest_h : (ti - tm) * inv_t - log_t);
+      float lo;
+      const float h = over_t(ti, &lo);
+      p = expf(P.teacher_lse ? (h - lse) + lo : (ti - tm) * inv_t - log_t);
       sum_p += p;
-      if (p != 0.f) loss += p * ((ti - zl[i]) * inv_t - gap);
+      if (p != 0.f) loss += p * ((ti - r.z[i]) * inv_t - gap);
     }
     P.probs[row * P.top + i] = p;
   }
@@ -400,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
   if (lane == 0) {
     float keep = 1.f;
     if (P.teacher_lse) {
-      const float r = sum_p >= 1.f ? 0.f : 1.f - sum_p, ratio = s_top / s_rest;   // log rho = -log(1 + ratio)
-      if (r != 0.f) loss += r * (log1pf(-sum_p) + log1pf(ratio));                 // (NaN too)
-      if (s_rest != 0.f) keep = 1.f - r * (1.f + ratio);
+      const float left = sum_p >= 1.f ? 0.f : 1.f - sum_p, ratio = s_top / s_rest;   // log rho = -log(1 + ratio)
+      if (left != 0.f) loss += left * (log1pf(-sum_p) + log1pf(ratio));                 // (NaN too)
+      if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
     }
     P.loss[row] = any ? weight * loss : 0.f;
     *reinterpret_cast<float4*>(P.stats + row * 4) =
@@ -410,14 +438,258 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_fwd_ke
   }
 }
 
+template <class H>
+__device__ __noinline__ H ended(H v, int n, int lane) {
+  v.end(n, lane);
+  return v;
+}
+// The sum of 2^((x - m) c) over a group, for maxima far from 0, where the products x c have no digits behind the point.
+template <class H>
+__device__ __noinline__ float far_sum(H v, float m, float c) {
+  float x[8], sum = 0.f;
+  v.get(x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum += ex2((x[e] - m) * c);
+  return sum;
+}
+
+constexpr int set_of(int kind) { return kind == kF32 ? 4 : 8; }
+
+// CL: CTAs of a row's cluster. Of a thread's places, CTA r has those congruent to r.
+//
+// A place's groups are taken in eight (fp32: four) rounds at a time: one maximum, and at most one rescaling of the sum, for a
+// thread's 64 (32) elements. (Group by group, a thread's instructions were more of the time than its loads.)
+template <int KIND, int VEC, bool SHIFT, int CL>
+__global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fwd_kernel(const __grid_constant__ DistillArgs P) {
+  constexpr int kSet = set_of(KIND);               // groups of a set
+  using H = Held<KIND, VEC, SHIFT>;
+  extern __shared__ int smem[];
+  __shared__ Part sent[kPlaces][kThreads];         // the threads' places; in a cluster's first CTA all of them
+  __shared__ Part parts[2][kWarps];
+  __shared__ int64_t rows[2];                      // the rows in turn; -1: no more
+  const int lane = int(lane_id()), warp = int(warp_id()), tid = int(threadIdx.x);
+  const int rank = CL > 1 ? int(cluster_rank()) : 0;
+  const auto entries = [&](int b) {
+    int2* at = reinterpret_cast<int2*>(smem + b * (even(P.groups) + 4 * P.top));
+    float* t = reinterpret_cast<float*>(at + P.top);
+    return Row{{reinterpret_cast<int*>(t + 2 * P.top), at}, t, t + P.top};
+  };
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if constexpr (CL > 1) cluster_sync_all();        // every CTA of the cluster runs: its shared memory may be written
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------- the entries
+    int64_t next = blockIdx.x / CL, was = -1;
+    float weight = 0.f, w_next = P.weight ? __ldg(P.weight + next) : 1.f;
+    const int64_t step = gridDim.x / CL;
+    for (int b = 0;; b ^= 1) {
+      // the next row that is read, its lists; what the ones passed over leave
+      int64_t row = -1;
+      float w = 0.f;
+      for (; row < 0 && next < P.M; next += step) {
+        w = w_next;
+        if (P.weight && next + step < P.M) w_next = __ldg(P.weight + next + step);
+        if (w != 0.f) {
+          row = next;
+        } else if (rank == 0) {
+          for (int i = lane; i < P.top; i += 32) P.probs[next * P.top + i] = -1.f;
+          if (lane < 4) P.stats[next * 4 + lane] = 0.f;
+          if (lane == 0) P.loss[next] = 0.f;
+        }
+      }
+      if (row >= 0) make_lists(P, entries(b), KIND, row, rank == 0, lane);
+      if (lane == 0) rows[b] = row;
+      __syncwarp();
+      bar_arrive(kBarLists + b);
+      if (was >= 0) {
+        if constexpr (CL > 1) cluster_sync_all();  // (a cluster has one row)
+        if (rank == 0) {
+          named_bar(kBarParts + (b ^ 1), kFwdThreads);
+          end_row(P, entries(b ^ 1), parts[b ^ 1], was, weight, lane);
+        }
+      }
+      if (row < 0) return;
+      was = row;
+      weight = w;
+    }
+  }
+
+  // ---------------------------------------------------------------- the stream
+  // A set of groups is sent for, taken in, and the next one sent for, of the next row when this one has no more: warps wait in
+  // turn.
+  const float c = kLog2e / P.temperature;
+  constexpr int kBytes = KIND == kF32 ? 4 : 2;
+  const int stride = P.places * kWarps, round = stride * kGroupElems;      // groups and elements of a round
+  const int sets = (P.groups + stride * kSet - 1) / (stride * kSet);       // of a place
+  const int places = P.places / CL;                // of this CTA
+  const auto first_of = [&](int j) { return ((CL * j + rank) * kWarps + warp) * kGroupElems; };
+  const auto offset = [&](int64_t row) { return SHIFT ? int(row * P.V & 7) : 0; };
+  // what is sent for next: row `to`, its place and rounds; nothing when to is -1
+  int64_t to = -1;
+  int to_b = 1, to_j = places, to_q = 0, to_left = 0, to_off = 0;
+  const uint8_t* to_at = nullptr;
+  bool to_edge = false, more = true;
+  const auto send = [&](H (&h)[kSet]) {
+    if (to_j == places && more) {                  // the next row; its lists are there
+      to_b ^= 1;
+      named_bar(kBarLists + to_b, kFwdThreads);
+      to = rows[to_b];
+      more = to >= 0;
+      to_j = 0;
+      to_off = offset(to);
+      to_edge = to == P.M - 1;
+      to_left = P.V - first_of(0);
+      to_at = H::place(P.z, to * P.V + first_of(0), to_off, lane);
+    }
+    if (!more) return;
+    if (to_left >= (kSet - 1) * round + kGroupElems + 8) {     // (the second vector of an unaligned group's last lane, too)
+#pragma unroll
+      for (int i = 0; i < kSet; ++i) h[i].load_whole(to_at + int64_t(i * round) * kBytes, to_off);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSet; ++i) {
+        const int n = to_left - i * round;
+        if (n >= kGroupElems + 8) h[i].load_whole(to_at + int64_t(i * round) * kBytes, to_off);
+        else if (n > 0) h[i].load(to_at + int64_t(i * round) * kBytes, to_off, n, to_edge, lane);
+      }
+    }
+    if (++to_q < sets) {
+      to_at += int64_t(kSet * round) * kBytes;
+      to_left -= kSet * round;
+    } else {
+      to_q = 0;
+      ++to_j;
+      to_left = P.V - first_of(to_j);
+      to_at = H::place(P.z, to * P.V + first_of(to_j), to_off, lane);
+    }
+  };
+  H h[kSet];
+  send(h);
+  int64_t row = to;
+  if (row < 0) return;
+  // what is taken in next
+  int b = 0, j = 0, q = 0, left = P.V - first_of(0), off = offset(row);
+  Part p{-kInf, 0.f};
+  // Takes a set in; true when that was the end of the row.
+  const auto take = [&]() {
+    if (left > 0) {
+      const Lists L = entries(b).lists;
+      const int* head = L.head + (P.V - left) / kGroupElems;
+      const bool whole = left >= (kSet - 1) * round + kGroupElems;
+#pragma unroll
+      for (int i = 0; i < kSet; ++i)
+        if (whole || left > i * round) h[i].settle(off);
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < kSet; ++i) {
+          const int n = left - i * round;
+          if (n <= 0) h[i].clear();
+          else if (n < kGroupElems) h[i] = ended(h[i], n, lane);
+        }
+      }
+      if (P.teacher_lse) {                         // the entries are no part of the rest
+#pragma unroll
+        for (int i = 0; i < kSet; ++i) {
+          if (!whole && left <= i * round) break;
+          const int first = P.V - left + i * round;
+          for (int e = head[i * stride]; e >= 0;) {
+            const int2 link = L.link[e];
+            h[i].drop(uint32_t(link.y - first), uint32_t(lane));
+            e = link.x;
+          }
+        }
+      }
+      float m = h[0].largest();
+#pragma unroll
+      for (int i = 1; i < kSet; ++i) m = fmaxf(m, h[i].largest());
+      if (m > p.m) {
+        p.s = rescale(p.s, p.m, m, c);
+        p.m = m;
+      }
+      // 2^((x - m) c) = 2^(x c - r) 2^(r - m c) with r = m c rounded to an integer: one fma an element
+      const float ref = p.m == -kInf ? 0.f : p.m, mc = ref * c;            // (nothing but -infinity so far: all terms are 0)
+      if (__any_sync(0xffffffffu, !(fabsf(mc) < 65536.f))) {
+#pragma unroll
+        for (int i = 0; i < kSet; ++i)
+          if (whole || left > i * round) p.s += far_sum(h[i], ref, c);
+      } else {
+        const float r = rintf(mc);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kSet; ++i) {
+          if (!whole && left <= i * round) break;
+          float x[8];
+          h[i].get(x);
+          float2 y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = fma2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(c, c), make_float2(-r, -r));
+            y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
+          }
+          sum = add2(sum, add2(add2(y[0], y[1]), add2(y[2], y[3])));
+        }
+        p.s += (sum.x + sum.y) * ex2(fmaf(-ref, c, r));
+      }
+    }
+    if (++q < sets) {
+      left -= kSet * round;
+      return false;
+    }
+    // the place is done
+    if constexpr (CL > 1)
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(peer_addr(smem_u32(&sent[CL * j + rank][tid]), 0)), "f"(p.m), "f"(p.s) : "memory");
+    else
+      sent[j][tid] = p;
+    p = {-kInf, 0.f};
+    q = 0;
+    ++j;
+    left = P.V - first_of(j);
+    if (j < places) return false;
+    // and the row: the thread's places, in order; then the warp's lanes
+    if constexpr (CL > 1) {
+      cluster_sync_all();
+      if (rank != 0) return true;
+    }
+    Part all[kPlaces];
+#pragma unroll
+    for (int i = 0; i < kPlaces; ++i) all[i] = i < P.places ? sent[i][tid] : Part{-kInf, 0.f};
+    Part t = all[0];
+#pragma unroll
+    for (int i = 1; i < kPlaces; ++i) t.m = fmaxf(t.m, all[i].m);
+    t.m = warp_max(t.m);
+    t.s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPlaces; ++i) t.s += rescale(all[i].s, all[i].m, t.m, c);
+    t.s = warp_sum(t.s);
+    if (lane == 0) parts[b][warp] = t;
+    __syncwarp();
+    bar_arrive(kBarParts + b);
+    return true;
+  };
+  while (true) {
+    const bool ended = take();
+    if (CL > 1 && ended) return;                   // (a cluster has one row)
+    send(h);
+    if (!ended) continue;
+    row = to;
+    if (row < 0) return;
+    off = to_off;
+    b ^= 1;
+    j = 0;
+    left = P.V - first_of(0);
+  }
+}
+
 // ---------------------------------------------------------------- backward
 // A CTA takes P.seg groups of a row; each element is written by the thread that read it. OUT8: in 8-bit blocks.
-template <int KIND, int VEC, bool OUT8>
-__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
-  constexpr int kLoads = KIND == kF32 ? 4 : 8;
+template <int KIND, int VEC, bool SHIFT, bool OUT8>
+__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : BMIN) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
+  constexpr int kLoads = KIND == kF32 || SHIFT ? 4 : BLOADS;
+  using H = Held<KIND, VEC, SHIFT>;
   extern __shared__ int smem[];
-  const Lists L{smem, smem + P.seg, smem + P.seg + P.top};
-  float* pl = reinterpret_cast<float*>(L.id + P.top);
+  const Lists L{smem + 3 * P.top + (P.top & 1), reinterpret_cast<int2*>(smem)};
+  float* pl = reinterpret_cast<float*>(smem + 2 * P.top);
   const int lane = int(lane_id()), warp = int(warp_id()), tid = int(threadIdx.x);
   const int segs = (P.groups + P.seg - 1) / P.seg;
   const int64_t row = blockIdx.x / segs;
@@ -434,22 +706,22 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_ke
     const int id = id_at(P, at);
     const float p = __ldg(P.probs + at);
     if (id >= 0 && !(p < 0.f) && id / kGroupElems >= g0 && id / kGroupElems < g1) {
-      L.id[i] = id;
       pl[i] = p;
-      L.next[i] = atomicExch(&L.head[id / kGroupElems - g0], i);
+      L.link[i] = make_int2(atomicExch(&L.head[id / kGroupElems - g0], i), id);
     }
   }
   __syncthreads();
   // q = 2^((x - m) c - log2 sum): the difference first, which is exact where q is large
   const float c = kLog2e / P.temperature, m = st.x, log_s = -st.y, gr = g * st.z;
   const int64_t base = row * P.V, ld = code_ld(P.V);
+  const int first = SHIFT ? int(base & 7) : 0;
   const int cblocks = (P.V + kBlock - 1) / kBlock;
   for (int gb = g0 + warp; gb < g1; gb += kWarps * kLoads) {
-    Held<KIND, VEC> held[kLoads];
+    H held[kLoads];
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       const int gi = gb + kWarps * k;
-      if (gi < g1 && !zero) held[k].load(P.z, base + int64_t(gi) * kGroupElems, P.V - gi * kGroupElems, lane);
+      if (gi < g1 && !zero) held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, row == P.M - 1, lane);
     }
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
@@ -461,30 +733,41 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_ke
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
       } else {
         float x[8];
+        held[k].settle(first);
         held[k].get(x);
+        if (n < kGroupElems) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = ex2(fmaf(x[e] - m, c, log_s));
-          v[e] = x[e] * gr;
+          for (int e = 0; e < 8; ++e)
+            if (H::at(e, lane) >= n) x[e] = -kInf;
         }
-        for (int i = L.head[gi - g0]; i >= 0; i = L.next[i]) {
-          const int o = L.id[i] - gi * kGroupElems, e0 = Held<KIND, VEC>::elem_of(o);
-          if (Held<KIND, VEC>::lane_of(o) == lane) {
-            const float pg = pl[i] * g;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e == e0) v[e] = fmaf(x[e], g, -pg);
-          }
+        for (int e = 0; e < 8; e += 2) {
+          const float2 y = fma2(add2(make_float2(x[e], x[e + 1]), make_float2(-m, -m)), make_float2(c, c), make_float2(log_s, log_s));
+          x[e] = ex2(y.x);
+          x[e + 1] = ex2(y.y);
+          const float2 t = mul2(make_float2(x[e], x[e + 1]), make_float2(gr, gr));
+          v[e] = t.x;
+          v[e + 1] = t.y;
+        }
+        for (int i = L.head[gi - g0]; i >= 0;) {
+          const int2 link = L.link[i];
+          const uint32_t mine = H::elem_of(uint32_t(link.y - gi * kGroupElems), uint32_t(lane));
+          const float pg = pl[i] * g;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = mine == uint32_t(e) ? fmaf(x[e], g, -pg) : v[e];
+          i = link.x;
         }
       }
       if constexpr (!OUT8) {
-        Held<KIND, VEC>::store(P.dz, base + int64_t(gi) * kGroupElems, n, lane, v);
+        H::store(P.dz, base + int64_t(gi) * kGroupElems, first, n, lane, v);
       } else {
         // the two blocks of the group: of 8 consecutive elements a lane, 16 lanes each; else the first and last four
         // of every lane. (What lies past column V is no value: 0, and written up to the codes' row length.)
+        if (n < kGroupElems) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (Held<KIND, VEC>::at(e, lane) >= n) v[e] = 0.f;
+          for (int e = 0; e < 8; ++e)
+            if (H::at(e, lane) >= n) v[e] = 0.f;
+        }
         uint32_t a[2] = {0u, 0u};
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[VEC == 8 ? 0 : e / 4] = max(a[VEC == 8 ? 0 : e / 4], abs_bits(v[e]));
@@ -506,11 +789,10 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : 3) distill_bwd_ke
           const BlockScale s[2] = {block_scale(a[0]), block_scale(a[1])};
 #pragma unroll
           for (int h = 0; h < 8; h += VEC) {
-            const int at = Held<KIND, VEC>::at(h, lane);
+            const int at = H::at(h, lane);
             const float inv = s[h / 4].inv;
             if (at >= nld) continue;
             if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(out + at) = codes4(v[h], v[h + 1], v[h + 2], v[h + 3], inv);
-            else if constexpr (VEC == 2) *reinterpret_cast<uint16_t*>(out + at) = uint16_t(codes2(v[h], v[h + 1], inv));
             else out[at] = uint8_t(codes2(v[h], 0.f, inv));
           }
           if (lane < 2 && 128 * lane < n) sc[lane] = lane == 0 ? s[0].scale : s[1].scale;
@@ -526,14 +808,17 @@ bool args_ok(int type, int id_bytes, float temperature, int64_t M, int64_t V, in
 }
 
 // Shared memory of a vocabulary's and a row's lists may pass the 48 KB that a launch has without asking.
-constexpr size_t kMostSmem = (16384 + 4 * kMaxTop) * 4;
+constexpr size_t kMostSmem = 2 * (16384 + 4 * kMaxTop) * 4;
 
-template <int KIND, int VEC>
-cudaError_t launch_fwd(DistillArgs& P, int cl, cudaStream_t st) {
-  const size_t smem = size_t(P.groups + 4 * P.top) * 4;
+template <int KIND, int VEC, bool SHIFT>
+cudaError_t launch_fwd(DistillArgs& P, int cl, int nsm, cudaStream_t st) {
+  const size_t smem = size_t(cl > 1 ? 1 : 2) * (even(P.groups) + 4 * P.top) * 4;
+  // as many CTAs as are resident (the lists of a long vocabulary leave room for fewer)
+  const int64_t room = std::max<int64_t>(1, 227 * 1024 / int64_t(smem + 2048));
+  const int64_t ctas = nsm * std::min<int64_t>(kMinCtas<KIND, SHIFT>, room);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(P.M * cl));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(unsigned(cl > 1 ? P.M * cl : std::min<int64_t>(P.M, ctas)));
+  cfg.blockDim = dim3(kFwdThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -543,51 +828,53 @@ cudaError_t launch_fwd(DistillArgs& P, int cl, cudaStream_t st) {
   attr[1].val.clusterDim = {unsigned(cl), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
-  if (cl == 8) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, 8>, P);
-  if (cl == 2) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, 2>, P);
-  return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, 1>, P);
+  if (cl == 8) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 8>, P);
+  if (cl == 4) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 4>, P);
+  if (cl == 2) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 2>, P);
+  return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 1>, P);
 }
-template <int KIND, int VEC>
+template <int KIND, int VEC, bool SHIFT>
 cudaError_t launch_bwd(DistillArgs& P, bool out8, cudaStream_t st) {
-  const size_t smem = size_t(P.seg + 3 * P.top) * 4;
+  const size_t smem = size_t(P.seg + 3 * P.top + 1) * 4;
   const dim3 grid(unsigned(P.M * cdiv(P.groups, P.seg)));
-  return out8 ? launch_pdl(distill_bwd_kernel<KIND, VEC, true>, grid, dim3(kThreads), smem, st, P)
-              : launch_pdl(distill_bwd_kernel<KIND, VEC, false>, grid, dim3(kThreads), smem, st, P);
+  return out8 ? launch_pdl(distill_bwd_kernel<KIND, VEC, SHIFT, true>, grid, dim3(kThreads), smem, st, P)
+              : launch_pdl(distill_bwd_kernel<KIND, VEC, SHIFT, false>, grid, dim3(kThreads), smem, st, P);
 }
-template <int KIND, int VEC>
+template <int KIND, int VEC, bool SHIFT>
 cudaError_t prepare() {
   cudaError_t e = cudaSuccess;
   auto set = [&](auto kernel) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostSmem));
   };
-  set(distill_fwd_kernel<KIND, VEC, 1>);
-  set(distill_fwd_kernel<KIND, VEC, 2>);
-  set(distill_fwd_kernel<KIND, VEC, 8>);
-  set(distill_bwd_kernel<KIND, VEC, false>);
-  set(distill_bwd_kernel<KIND, VEC, true>);
+  set(distill_fwd_kernel<KIND, VEC, SHIFT, 1>);
+  set(distill_fwd_kernel<KIND, VEC, SHIFT, 2>);
+  set(distill_fwd_kernel<KIND, VEC, SHIFT, 4>);
+  set(distill_fwd_kernel<KIND, VEC, SHIFT, 8>);
+  set(distill_bwd_kernel<KIND, VEC, SHIFT, false>);
+  set(distill_bwd_kernel<KIND, VEC, SHIFT, true>);
   return e;
 }
 
-// By the widest vector that fits every row.
+// By what the rows' length allows.
 template <class F>
-cudaError_t by_vector(int type, int64_t V, F&& f) {
+cudaError_t by_length(int type, int64_t V, F&& f) {
   using std::integral_constant;
+  const auto as = [&](auto kind, auto vec, auto shift) { return f(kind, vec, shift); };
   if (type == LORA_F32)
-    return V % 4 == 0 ? f(integral_constant<int, kF32>{}, integral_constant<int, 4>{})
-                      : f(integral_constant<int, kF32>{}, integral_constant<int, 1>{});
-  return V % 8 == 0   ? f(integral_constant<int, kBf16>{}, integral_constant<int, 8>{})
-         : V % 2 == 0 ? f(integral_constant<int, kBf16>{}, integral_constant<int, 2>{})
-                      : f(integral_constant<int, kBf16>{}, integral_constant<int, 1>{});
+    return V % 4 == 0 ? as(integral_constant<int, kF32>{}, integral_constant<int, 4>{}, std::false_type{})
+                      : as(integral_constant<int, kF32>{}, integral_constant<int, 1>{}, std::false_type{});
+  return V % 8 == 0 ? as(integral_constant<int, kBf16>{}, integral_constant<int, 8>{}, std::false_type{})
+                    : as(integral_constant<int, kBf16>{}, integral_constant<int, 8>{}, std::true_type{});
 }
 
 }  // namespace
 
 cudaError_t prepare_distill() {
   cudaError_t e;
-  if ((e = prepare<kBf16, 8>()) != cudaSuccess || (e = prepare<kBf16, 2>()) != cudaSuccess ||
-      (e = prepare<kBf16, 1>()) != cudaSuccess || (e = prepare<kF32, 4>()) != cudaSuccess)
+  if ((e = prepare<kBf16, 8, false>()) != cudaSuccess || (e = prepare<kBf16, 8, true>()) != cudaSuccess ||
+      (e = prepare<kF32, 4, false>()) != cudaSuccess)
     return e;
-  return prepare<kF32, 1>();
+  return prepare<kF32, 1, false>();
 }
 
 }  // namespace mlp
@@ -625,10 +912,14 @@ lora_status lora_distill_topk_fwd(const void* logits, int type, const void* ids,
   P.loss = loss;
   P.probs = probs;
   P.stats = stats;
-  // few rows: a row's groups over the CTAs of a cluster, while each of their warps has one
-  const int cl = M * 4 <= nsm && P.groups >= 4 * kWarps ? 8 : (M <= 2 * nsm && P.groups >= 2 * kWarps ? 2 : 1);
-  const cudaError_t e = by_vector(type, V, [&](auto kind, auto vec) {
-    return launch_fwd<kind.value, vec.value>(P, cl, static_cast<cudaStream_t>(stream));
+  // as many places as leave each a set's rounds, of the row's length alone
+  P.places = 1;
+  while (P.places < kPlaces && P.places * kWarps * set_of(type == LORA_F32 ? kF32 : kBf16) < P.groups) P.places *= 2;
+  // few rows: a row's places over the CTAs of a cluster
+  int cl = 1;
+  while (cl < P.places && M * cl * 2 <= 2 * nsm) cl *= 2;
+  const cudaError_t e = by_length(type, V, [&](auto kind, auto vec, auto shift) {
+    return launch_fwd<kind.value, vec.value, shift.value>(P, cl, nsm, static_cast<cudaStream_t>(stream));
   });
   return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
@@ -660,8 +951,8 @@ lora_status lora_distill_topk_bwd(const float* dloss, const void* logits, int ty
   if (M * cdiv(P.groups, P.seg) >= (int64_t(1) << 31)) return LORA_ERR_SHAPE;
   int nsm = 0;
   if ((s = device_ready(&nsm)) != LORA_OK) return s;
-  const cudaError_t e = by_vector(type, V, [&](auto kind, auto vec) {
-    return launch_bwd<kind.value, vec.value>(P, scales != nullptr, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = by_length(type, V, [&](auto kind, auto vec, auto shift) {
+    return launch_bwd<kind.value, vec.value, shift.value>(P, scales != nullptr, static_cast<cudaStream_t>(stream));
   });
   return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
 }
