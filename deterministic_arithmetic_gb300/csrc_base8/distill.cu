@@ -90,13 +90,17 @@ struct Held {
     } else if constexpr (KIND == kBf16) {
       // elements of the row from the first and from the second vector's start on
       const int n0 = n + off - 8 * lane, n1 = n0 - 8;
-      uint4 t;
+      if (edge) {
+        if (n0 > off) some(at, n0, w);
+        if (off && n1 > 0) some(at + 16, n1, w + 4);
+        return;
+      }
       if (n0 > off) {
-        t = !edge || n0 >= 8 ? *reinterpret_cast<const uint4*>(at) : some(at, n0);
+        const uint4 t = *reinterpret_cast<const uint4*>(at);
         w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
       }
       if (off && n1 > 0) {
-        t = !edge || n1 >= 8 ? *reinterpret_cast<const uint4*>(at + 16) : some(at + 16, n1);
+        const uint4 t = *reinterpret_cast<const uint4*>(at + 16);
         w[4] = t.x; w[5] = t.y; w[6] = t.z; w[7] = t.w;
       }
     } else if constexpr (VEC == 4) {
@@ -113,13 +117,11 @@ struct Held {
         if (32 * j + lane < n) w[j] = *reinterpret_cast<const uint32_t*>(at + 128 * j);
     }
   }
-  // The first n elements of a vector that does not lie in the tensor whole.
-  static __device__ __noinline__ uint4 some(const uint8_t* at, int n) {
+  // The first n elements of a vector that need not lie in the tensor whole.
+  static __device__ __forceinline__ void some(const uint8_t* at, int n, uint32_t* w) {
     const uint16_t* q = reinterpret_cast<const uint16_t*>(at);
-    uint32_t t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = (2 * i < n ? uint32_t(q[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(q[2 * i + 1]) << 16 : 0u);
-    return make_uint4(t[0], t[1], t[2], t[3]);
+    for (int i = 0; i < 4; ++i) w[i] = (2 * i < n ? uint32_t(q[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(q[2 * i + 1]) << 16 : 0u);
   }
   // Makes the elements themselves of what load() brought.
   __device__ __forceinline__ void settle(int off) {
@@ -129,10 +131,6 @@ struct Held {
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = t[i];
     }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = KIND == kF32 ? 0xFF800000u : 0xFF80FF80u;
   }
   // -infinity where the row has no more elements.
   __device__ __forceinline__ void end(int n, int lane) {
@@ -310,15 +308,9 @@ __device__ __forceinline__ float rescale(float s, float from, float to, float c)
   return from == -kInf && s == 0.f ? 0.f : s * ex2((from - to) * c);
 }
 
-#ifndef FMIN
-#define FMIN 3
-#define FLOADS 8
-#define BMIN 5
-#define BLOADS 4
-#endif
-// CTAs of an SM.
+// CTAs of an SM (2, 3 and 4 of bf16: 283, 202 and 193 us at 4096 x 131072).
 template <int KIND, bool SHIFT>
-constexpr int kMinCtas = KIND == kF32 || SHIFT ? 2 : FMIN;
+constexpr int kMinCtas = KIND == kF32 || SHIFT ? 2 : 4;
 
 // ----------------------------------------------------------------- forward
 // A CTA has eight warps that stream its rows, and a ninth for their entries: it makes the lists of the next row and ends the one
@@ -438,11 +430,6 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
   }
 }
 
-template <class H>
-__device__ __noinline__ H ended(H v, int n, int lane) {
-  v.end(n, lane);
-  return v;
-}
 // The sum of 2^((x - m) c) over a group, for maxima far from 0, where the products x c have no digits behind the point.
 template <class H>
 __device__ __noinline__ float far_sum(H v, float m, float c) {
@@ -548,11 +535,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
       for (int i = 0; i < kSet; ++i) h[i].load_whole(to_at + int64_t(i * round) * kBytes, to_off);
     } else {
 #pragma unroll
-      for (int i = 0; i < kSet; ++i) {
-        const int n = to_left - i * round;
-        if (n >= kGroupElems + 8) h[i].load_whole(to_at + int64_t(i * round) * kBytes, to_off);
-        else if (n > 0) h[i].load(to_at + int64_t(i * round) * kBytes, to_off, n, to_edge, lane);
-      }
+      for (int i = 0; i < kSet; ++i) h[i].load(to_at + int64_t(i * round) * kBytes, to_off, to_left - i * round, to_edge, lane);
     }
     if (++to_q < sets) {
       to_at += int64_t(kSet * round) * kBytes;
@@ -576,22 +559,22 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
     if (left > 0) {
       const Lists L = entries(b).lists;
       const int* head = L.head + (P.V - left) / kGroupElems;
-      const bool whole = left >= (kSet - 1) * round + kGroupElems;
+      // (half a set where the rest of it has no elements)
+      const bool all = left > kSet / 2 * round;
 #pragma unroll
-      for (int i = 0; i < kSet; ++i)
-        if (whole || left > i * round) h[i].settle(off);
-      if (!whole) {
+      for (int i = 0; i < kSet; ++i) {
+        if (i >= kSet / 2 && !all) break;
+        h[i].settle(off);
+      }
+      if (left < (kSet - 1) * round + kGroupElems) {
 #pragma unroll
-        for (int i = 0; i < kSet; ++i) {
-          const int n = left - i * round;
-          if (n <= 0) h[i].clear();
-          else if (n < kGroupElems) h[i] = ended(h[i], n, lane);
-        }
+        for (int i = 0; i < kSet; ++i)
+          if (left - i * round < kGroupElems) h[i].end(left - i * round, lane);
       }
       if (P.teacher_lse) {                         // the entries are no part of the rest
 #pragma unroll
         for (int i = 0; i < kSet; ++i) {
-          if (!whole && left <= i * round) break;
+          if (left <= i * round) break;
           const int first = P.V - left + i * round;
           for (int e = head[i * stride]; e >= 0;) {
             const int2 link = L.link[e];
@@ -602,7 +585,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
       }
       float m = h[0].largest();
 #pragma unroll
-      for (int i = 1; i < kSet; ++i) m = fmaxf(m, h[i].largest());
+      for (int i = 1; i < kSet; ++i) m = fmaxf(m, h[i].largest());           // (-infinity where there are none)
       if (m > p.m) {
         p.s = rescale(p.s, p.m, m, c);
         p.m = m;
@@ -612,13 +595,11 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
       if (__any_sync(0xffffffffu, !(fabsf(mc) < 65536.f))) {
 #pragma unroll
         for (int i = 0; i < kSet; ++i)
-          if (whole || left > i * round) p.s += far_sum(h[i], ref, c);
+          if (left > i * round) p.s += far_sum(h[i], ref, c);
       } else {
         const float r = rintf(mc);
         float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kSet; ++i) {
-          if (!whole && left <= i * round) break;
+        const auto add = [&](int i) {
           float x[8];
           h[i].get(x);
           float2 y[4];
@@ -628,6 +609,12 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
             y[e] = make_float2(ex2(y[e].x), ex2(y[e].y));
           }
           sum = add2(sum, add2(add2(y[0], y[1]), add2(y[2], y[3])));
+        };
+#pragma unroll
+        for (int i = 0; i < kSet / 2; ++i) add(i);
+        if (all) {
+#pragma unroll
+          for (int i = kSet / 2; i < kSet; ++i) add(i);
         }
         p.s += (sum.x + sum.y) * ex2(fmaf(-ref, c, r));
       }
@@ -684,8 +671,8 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
 // ---------------------------------------------------------------- backward
 // A CTA takes P.seg groups of a row; each element is written by the thread that read it. OUT8: in 8-bit blocks.
 template <int KIND, int VEC, bool SHIFT, bool OUT8>
-__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : BMIN) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
-  constexpr int kLoads = KIND == kF32 || SHIFT ? 4 : BLOADS;
+__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 || SHIFT ? 4 : 5)) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
+  constexpr int kLoads = 4;                        // groups of a warp in flight
   using H = Held<KIND, VEC, SHIFT>;
   extern __shared__ int smem[];
   const Lists L{smem + 3 * P.top + (P.top & 1), reinterpret_cast<int2*>(smem)};
@@ -734,12 +721,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : BMIN) distill_bwd
       } else {
         float x[8];
         held[k].settle(first);
-        held[k].get(x);
-        if (n < kGroupElems) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (H::at(e, lane) >= n) x[e] = -kInf;
-        }
+        held[k].get(x);                            // (what lies past the row's end is not stored)
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const float2 y = fma2(add2(make_float2(x[e], x[e + 1]), make_float2(-m, -m)), make_float2(c, c), make_float2(log_s, log_s));
