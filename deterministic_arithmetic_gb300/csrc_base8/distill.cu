@@ -45,7 +45,7 @@ __device__ __forceinline__ void shifted(uint32_t (&u)[8], int first, uint32_t (&
 // What a thread holds of a group of 256 elements of its warp: 8 of them, in pieces of VEC consecutive ones, 32 VEC apart:
 // one of 8 (bf16), two of 4 (fp32), or (fp32 rows of odd lengths) single ones. SHIFT: bf16 rows whose length is no multiple of
 // 8 start at any element; their pieces are put together from the two 16-byte vectors that hold them (loads of 2 bytes took
-// 4096 x 50257 forward 201 us, SHIFTFIG so, and 405 backward, SHIFTBWD).
+// 4096 x 50257 forward 201 us, 166 so, and 405 backward, 226).
 template <int KIND, int VEC, bool SHIFT>
 struct Held {
   static_assert(KIND == kF32 ? !SHIFT : VEC == 8, "");

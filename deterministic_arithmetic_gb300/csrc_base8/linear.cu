@@ -16,13 +16,13 @@ bool shape_ok(int64_t M, int64_t K, int64_t N) {
 
 int g_pairs[64];                                   // pairs of CTAs that a device holds at once
 
-template <int MODE, int CG, int W, int DEEP>
+template <int MODE, int CG, int W, int DEEP, bool JOINS = false>
 lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void* w, int64_t red, int64_t w_rows,
                       int64_t w_cols, int nsm, int pairs, cudaStream_t st) {
   P.bn = plan.bn;
   // a batch smaller than a tile: only its rows are copied, and the ring holds more stages
   const int a_rows = P.m < kBM ? int((P.m + 7) & ~7) : kBM;
-  constexpr int chunk = lin_chunk(W, CG);
+  constexpr int chunk = lin_chunk(W);
   if (!tensor_map(&P.a, a, Elem::u8, P.m, red, code_ld(red), kLinBK, a_rows, 128)) return LORA_ERR_CUDA;
   const bool b = MODE == kLinFwd
                      ? tensor_map(&P.b, w, Elem::u8, w_rows, w_cols, code_ld(w_cols), kLinBK, P.bn / CG, 128)
@@ -30,10 +30,9 @@ lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void
   if (!b) return LORA_ERR_CUDA;
   P.a_bytes = a_rows * kLinBK;
   P.block_bytes = P.a_bytes + P.bn / CG * kLinBK;
-  P.boxes = W == 256 && P.n % (P.out_f32 ? 4 : 8) == 0;
   if (P.boxes && !tensor_map(&P.o, P.out, P.out_f32 ? Elem::f32 : Elem::bf16, P.m, P.n, P.n, P.out_f32 ? 16 : 32, 32, 64)) return LORA_ERR_CUDA;
-  if (P.boxes && P.delta && !tensor_map(&P.d, P.delta, Elem::f32, P.m, P.n, P.n, 16, 32, 64)) return LORA_ERR_CUDA;
-  P.stages = std::min(kLinStages, lin_ring(W, P.boxes && P.delta) / (DEEP * P.block_bytes));
+  if (JOINS && !tensor_map(&P.d, P.delta, Elem::f32, P.m, P.n, P.n, 16, 32, 64)) return LORA_ERR_CUDA;
+  P.stages = std::min(kLinStages, lin_ring(W, JOINS) / (DEEP * P.block_bytes));
   P.tiles_m = int(cdiv(P.m, CG * kBM));
   P.tiles_n = int(cdiv(P.n, P.bn));
   const int64_t total = int64_t(P.tiles_m) * P.tiles_n;
@@ -52,7 +51,7 @@ lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void
   attr[1].val.clusterDim = {unsigned(CG), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = CG > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, CG, W, DEEP>, P, status_block()) == cudaSuccess ? LORA_OK
+  return cudaLaunchKernelEx(&cfg, linear_kernel<MODE, CG, W, DEEP, JOINS>, P, status_block()) == cudaSuccess ? LORA_OK
                                                                                                      : LORA_ERR_CUDA;
 }
 
@@ -83,8 +82,11 @@ lora_status linear(const void* a, const float* sa, const void* w, const float* s
   P.vec = cols % 4 == 0;
   const int pairs = g_pairs[dev];
   const LinPlan plan = lin_plan(MODE == kLinBwd, P.m, P.n, nsm, pairs);
+  P.boxes = plan.w == 256 && cols % (P.out_f32 ? 4 : 8) == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto go = [&](auto cg, auto width, auto deep) {
+    if constexpr (width.value == 256)
+      if (P.boxes && P.delta) return launch_as<MODE, cg.value, 256, 1, true>(P, plan, a, w, red, N, K, nsm, pairs, st);
     return launch_as<MODE, cg.value, width.value, deep.value>(P, plan, a, w, red, N, K, nsm, pairs, st);
   };
   using std::integral_constant;
@@ -108,11 +110,13 @@ cudaError_t prepare(int* pairs) {
     if (e == cudaSuccess && a.numRegs < kLinRegs) e = cudaErrorInvalidConfiguration;
     set(kernel);
   };
-  set_shared(linear_kernel<MODE, 2, 256, 1>);
-  set_shared(linear_kernel<MODE, 1, 256, 1>);
-  set(linear_kernel<MODE, 1, 128, 2>);
-  set(linear_kernel<MODE, 1, 64, 4>);
-  set(linear_kernel<MODE, 1, 32, 4>);
+  set_shared(linear_kernel<MODE, 2, 256, 1, false>);
+  set_shared(linear_kernel<MODE, 2, 256, 1, true>);
+  set_shared(linear_kernel<MODE, 1, 256, 1, false>);
+  set_shared(linear_kernel<MODE, 1, 256, 1, true>);
+  set(linear_kernel<MODE, 1, 128, 2, false>);
+  set(linear_kernel<MODE, 1, 64, 4, false>);
+  set(linear_kernel<MODE, 1, 32, 4, false>);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
@@ -123,7 +127,7 @@ cudaError_t prepare(int* pairs) {
   attr[0].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(pairs, linear_kernel<MODE, 2, 256, 1>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(pairs, linear_kernel<MODE, 2, 256, 1, true>, &cfg) != cudaSuccess) {
     cudaGetLastError();                            // (an answer, not an error of a later call)
     *pairs = 0;
   }

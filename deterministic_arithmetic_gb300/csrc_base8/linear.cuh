@@ -17,11 +17,10 @@ namespace mlp {
 
 constexpr int kLinBK = 128;                        // depth of a k-block: a block of the scales
 constexpr int kLinArea = 208 * 1024;               // the operand ring and, behind it, the epilogue warps' boxes
-// A box: 32 rows of 64 bytes that TMA stores or (delta's) loads. Tiles of 256 columns have three of each warp, or five where
-// delta is joined (four loads ahead, and one to store from), which costs the ring a stage or two it does not miss: its
-// 4 x 32 KB are 1.7 % slower than six at 4096 x 17408 -> 5120. Smaller tiles have one; there the MMAs' reads past a short
-// batch's rows of A (whose products nobody reads) end in them.
-constexpr int kBox = 32 * 64, kBoxesPlain = 3, kBoxesDelta = 5;
+// A box: 32 rows of 64 bytes that TMA stores or (delta's) loads. Tiles of 256 columns have four of each warp, five with delta,
+// which leaves the ring four of its 32 KB stages; six are no faster (8192 x 4096 -> 4096: 101 and 100 us). Smaller tiles
+// have one; there the MMAs' reads past a short batch's rows of A (whose products nobody reads) end in them.
+constexpr int kBox = 32 * 64, kBoxesPlain = 4, kBoxesDelta = 5;
 constexpr int lin_boxes(int W, bool delta) { return W < 256 ? 1 : (delta ? kBoxesDelta : kBoxesPlain); }
 constexpr int lin_ring(int W, bool delta) { return kLinArea - kEpiWarps * lin_boxes(W, delta) * kBox; }
 constexpr int kLinStages = 16;
@@ -30,7 +29,7 @@ constexpr int kLinSlots = 4;                       // accumulator slots at most
 // most two) column blocks that a tile touches, [block of columns][row].
 constexpr int kScaleGroup = 4, kScaleGroups = 4, kScaleBytes = 2 * kBM * 4;       // (of a k-block)
 constexpr int kLinScales = kScaleGroups * kScaleGroup * kScaleBytes;
-constexpr int kLinBars = 2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + kEpiWarps * (kBoxesDelta - 1) + 2;
+constexpr int kLinBars = 2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + kEpiWarps * 2 + 2;
 constexpr size_t kLinSmem = kLinArea + kLinScales + 1024 + kLinBars * 8 + 16;
 static_assert(kLinSmem < 227 * 1024, "shared memory of a CTA");
 
@@ -162,7 +161,7 @@ __device__ __forceinline__ void tmem_ldn(uint32_t taddr, uint32_t (&r)[N]) {
 }
 
 // Columns of a copied piece of MN-major B, which is its swizzle span; an MMA takes whole pieces.
-constexpr int lin_chunk(int W, int CG) { return CG == 2 ? 64 : (W < 128 ? W : 128); }
+constexpr int lin_chunk(int W) { return W < 128 ? W : 128; }
 
 // The tile of a unit: groups of up to 16 row tiles, row tiles fastest (gemm.cuh).
 struct LinUnit {
@@ -228,8 +227,9 @@ __device__ __forceinline__ void lin_store16(const LinArgs& P, uint32_t box, int6
 }
 
 // W: columns of an accumulator (bn rounded up to a power of two); DEEP: k-blocks of a stage, each with an
-// accumulator of its own in the slot.
-template <int MODE, int CG, int W, int DEEP>
+// accumulator of its own in the slot. JOINS: tiles of 256 columns whose delta comes by boxes (one more thing that the
+// epilogue's registers would hold).
+template <int MODE, int CG, int W, int DEEP, bool JOINS>
 __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_constant__ LinArgs P, uint32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -243,14 +243,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   auto sfull = [&](int g) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + g); };
   auto sempty = [&](int g) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + kScaleGroups + g); };
   const uint32_t scales = base + kLinArea;
-  // delta's box i of an epilogue warp has come
-  auto came = [&](int w, int i) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + w * (kBoxesDelta - 1) + i); };
+  // delta's boxes of half i of an epilogue warp's columns have come
+  auto came = [&](int w, int i) { return bar0 + 8u * (2 * kLinStages + 2 * kLinSlots + 2 * kScaleGroups + 2 * w + i); };
   const uint32_t drain = bar0 + 8u * (kLinBars - 2), never = drain + 8u;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kLinBars);
-  // An accumulator of 256 columns is two slots, each filled by MMAs and read by four warps of its own.
-  constexpr int kSub = W == 256 ? 2 : 1, kSlotCols = W * DEEP / kSub;
+  constexpr int kSlotCols = W * DEEP;              // of TMEM: a stage's accumulators
   constexpr int kSlots = 512 / kSlotCols < kLinSlots ? 512 / kSlotCols : kLinSlots;
-  static_assert(kSlots >= 2 && kSlots % kSub == 0 && (W >= 32 && W <= 256), "TMEM columns");
+  static_assert(kSlots >= 2 && (W >= 32 && W <= 256), "TMEM columns");
   static_assert(CG == 1 || W == 256, "pairs take tiles of 256 columns");
 
   const uint32_t warp = warp_id(), lane = lane_id();
@@ -263,13 +262,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     }
     for (int b = 0; b < kSlots; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), kEpiWarps / kSub + (CG == 2 && rank == 0 ? 1 : 0));
+      mbar_init(tempty(b), kEpiWarps + (CG == 2 && rank == 0 ? 1 : 0));
     }
     for (int g = 0; g < kScaleGroups; ++g) {
       mbar_init(sfull(g), 1);
       mbar_init(sempty(g), kEpiWarps);
     }
-    for (int i = 0; i < kEpiWarps * (kBoxesDelta - 1); ++i) mbar_init(came(0, i), 1);
+    for (int i = 0; i < kEpiWarps * 2; ++i) mbar_init(came(0, i), 1);
     mbar_init(drain, 1);
     mbar_init(never, 1);
     tmem_slot[1] = 0u;                             // the abort flag
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   const LinAbort ab{drain + 20u, status};
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
   // a copied piece of MN-major B: kChunk columns of 128 rows of the weight, its swizzle span
-  constexpr int kChunk = lin_chunk(W, CG);
+  constexpr int kChunk = lin_chunk(W);
 
   if (warp < 4) {
   if constexpr (W == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLinRegsFew));
@@ -354,11 +353,10 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     if (rank == 0) {
       // K-major operands step 32 bytes inside the swizzle span per 32 of the reduction; MN-major ones 32 rows.
       constexpr uint32_t kSpan = MODE == kLinFwd ? 128 : kChunk, a_step = 32u, b_step = MODE == kLinFwd ? 32u : 32u * kSpan;
-      constexpr uint32_t kHalfBytes = 128 / CG * kLinBK;        // of this CTA's B, what a slot of 128 columns takes
       const uint64_t a0 = smem_desc(base, 16u, 1024u, kLayoutSW128);
       const uint64_t b0 = smem_desc(base + P.a_bytes, MODE == kLinFwd ? 16u : kLinBK * kSpan, 8u * kSpan, layout_for_span(kSpan));
       const uint32_t a_lo = uint32_t(a0), a_hi = uint32_t(a0 >> 32), b_lo = uint32_t(b0), b_hi = uint32_t(b0 >> 32);
-      const uint32_t idesc = idesc_f8(CG * kBM, P.bn / kSub, MODE == kLinBwd);
+      const uint32_t idesc = idesc_f8(CG * kBM, P.bn, MODE == kLinBwd);
       const bool one = elect_one();
       int idx = 0, buf = 0;
       uint32_t phase = 0, tphase = 0;
@@ -371,29 +369,26 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
           if (!ok) break;
           const uint32_t off = uint32_t(idx) * stage_bytes, used = empty(idx);
           if (++idx == stages) idx = 0, phase ^= 1u;
+          if (!__all_sync(0xffffffffu, free)) ok = lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4);
+          if (!ok) break;
+          tc_fence_after();
+          if (one) {
+            const uint32_t d = tmem + buf * kSlotCols;
 #pragma unroll
-          for (int h = 0; h < kSub; ++h) {
-            if (!__all_sync(0xffffffffu, free)) ok = lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4);
-            if (!ok) break;
-            tc_fence_after();
-            if (one) {
-              const uint32_t d = tmem + buf * kSlotCols;
+            for (int k = 0; k < DEEP; ++k) {
+              if (k > 0 && kb + k >= P.nk) break;
+              const uint32_t a = a_lo + ((off + k * P.block_bytes) >> 4), b = b_lo + ((off + k * P.block_bytes) >> 4);
+              mma_f8<CG, 0>(d + k * W, a, a_hi, b, b_hi, idesc);
 #pragma unroll
-              for (int k = 0; k < DEEP; ++k) {
-                if (k > 0 && kb + k >= P.nk) break;
-                const uint32_t a = a_lo + ((off + k * P.block_bytes) >> 4), b = b_lo + ((off + k * P.block_bytes + h * kHalfBytes) >> 4);
-                mma_f8<CG, 0>(d + k * W, a, a_hi, b, b_hi, idesc);
-#pragma unroll
-                for (int j = 1; j < kLinBK / 32; ++j)
-                  mma_f8<CG, 1>(d + k * W, a + (j * a_step >> 4), a_hi, b + (j * b_step >> 4), b_hi, idesc);
-              }
-              commit<CG>(tfull(buf));
-              if (h == kSub - 1) commit<CG>(used);
+              for (int j = 1; j < kLinBK / 32; ++j)
+                mma_f8<CG, 1>(d + k * W, a + (j * a_step >> 4), a_hi, b + (j * b_step >> 4), b_hi, idesc);
             }
-            __syncwarp();
-            if (++buf == kSlots) buf = 0, tphase ^= 1u;
-            free = lin_done(tempty(buf), tphase ^ 1u);
+            commit<CG>(tfull(buf));
+            commit<CG>(used);
           }
+          __syncwarp();
+          if (++buf == kSlots) buf = 0, tphase ^= 1u;
+          free = lin_done(tempty(buf), tphase ^ 1u);
           landed = lin_done(full(idx), phase);
         }
       }
@@ -402,12 +397,12 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       lin_drain(drain, 0u, ab, kSiteLinear + 6);
     } else {
       // of a pair's second CTA: tells the first, once for all of its epilogue warps, that they have read a slot (arrivals across
-      // the pair are slow: an arrival of each warp, FORWARDFIG)
+      // the pair are slow: an arrival of each warp, 332 us and 293 at 4096 x 17408 -> 5120)
       int buf = 0;
       uint32_t tphase = 0;
       bool ok = true;
       for (int u = first; u < P.total && ok; u += step)
-        for (int i = 0; i < P.nk * kSub && ok; ++i) {
+        for (int i = 0; i < P.nk && ok; ++i) {
           ok = lin_wait(tempty(buf), tphase, ab, kSiteLinear + 11);
           lin_arrive_peer(peer_addr(tempty(buf), 0), ok && lane == 0);
           if (++buf == kSlots) buf = 0, tphase ^= 1u;
@@ -416,7 +411,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   } else {
     // ------------------------------------------------------ scales, two warps
     // Their groups in turn. (Loaded by the epilogue's warps themselves, the scales' latency was most of a k-block's time: of a
-    // pair's 4096 x 17408 -> 5120, SCALEFIG.)
+    // pair's 4096 x 17408 -> 5120, 411 us so, 337 with these warps.)
     uint32_t n = 0;                                // groups so far, of both warps
     bool ok = true;
     for (int u = first; u < P.total && ok; u += step) {
@@ -459,22 +454,18 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
   } else {
     // ------------------------------------------------------------ epilogue
     if constexpr (W == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLinRegsMany));
-    // A warp has its quarter of the rows and half of the tile's columns, in chunks of C: one after the other, but of a
-    // pair's tile, where a slot holds 64 columns of each CTA's B, 64 from each half of the tile.
+    // A warp has its quarter of the rows and half of the tile's columns, in chunks of C.
     constexpr int C = W >= 64 ? 32 : 16, kChunks = W / 2 / C;
-    constexpr int kScales = W == 256 ? CG : 2;                     // scales of a lane's row, of the warp's columns, a k-block
+    constexpr int kScales = W == 256 ? 1 : 2;                      // scales of a lane's row, of the warp's columns, a k-block
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = uint32_t(q * 32) << 16;
-    const int off = half * (CG == 2 ? 64 : W / 2);                 // its first column in the tile
-    auto column = [&](int i) { return off + i + (CG == 2 && i >= 64 ? 64 : 0); };      // and its i-th
-    // which of the scales its column i has
-    auto scale_of = [](int i) { return W == 256 ? i / 64 * (CG - 1) : i * 2 / (W / 2); };
-    int buf = kSub == 2 ? half : 0;
+    const int off = half * (W / 2);                                // its first column in the tile
+    auto column = [&](int i) { return off + i; };                  // and its i-th
+    auto scale_of = [](int i) { return i * kScales / (W / 2); };   // which of the scales that has
+    int buf = 0;
     uint32_t tphase = 0, n = 0;                    // groups of scales so far
-    const bool joins = W == 256 && P.boxes && P.delta;
-    const int boxes_each = lin_boxes(W, joins);
-    const uint32_t box0 = base + lin_ring(W, joins) + (warp - 4) * boxes_each * kBox;
-    uint32_t turn = 0, dphase = 0;
+    const uint32_t box0 = base + lin_ring(W, JOINS) + (warp - 4) * lin_boxes(W, JOINS) * kBox;
+    uint32_t dphase = 0;
     for (int u = first; u < P.total; u += step) {
       const LinUnit w = lin_unit<CG>(P, u);
       const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + q * 32;
@@ -483,22 +474,33 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < kScales; ++e)
         block[e] = uint32_t((w.col + column(e * (W / 2) / kScales)) / 128 - w.col / 128) * (kBM * 4) + (q * 32 + lane) * 4;
-      // delta's box i (16 columns), into place i % 4; TMA fills what lies past its ends with zeros
-      auto load_delta = [&](int i) {
-        const uint32_t bar = came(warp - 4, i & 3);
-        if (lane == 0) {
-          mbar_expect_tx(bar, kBox);
-          tma_load(box0 + (i & 3) * kBox, &P.d, bar, w.col + column(16 * i), int(row0), policy_normal());
-        }
-      };
       auto boxed = [&](int i) { return rows && w.col + column(16 * i) < P.n; };
-      if (joins) {
-        __syncwarp();
+      // delta's box i (16 columns), into a place; TMA fills what lies past its ends with zeros. The boxes of a half of the tile
+      // complete one barrier, which is told how many there are.
+      auto load_delta = [&](int i, int place, int half) {
+        if (lane == 0)
+          tma_load(box0 + place * kBox, &P.d, came(warp - 4, half), w.col + column(16 * i), int(row0), policy_normal());
+      };
+      auto expect = [&](int half) {
+        int boxes = 0;
+        for (int i = 4 * half; i < 4 * half + 4; ++i) boxes += boxed(i);
+        if (lane == 0) mbar_expect_tx(came(warp - 4, half), boxes * kBox);
+      };
+      if constexpr (JOINS) {
+        if (boxed(0)) {
+          if (lane == 0) tma_store_wait_read<0>();   // the tile before has left the places
+          __syncwarp();
+          expect(0);
 #pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          if (!boxed(i)) continue;
-          if (i < kBoxesDelta - 1) load_delta(i);
-          else if (lane == 0) tma_prefetch_l2(&P.d, w.col + column(16 * i), int(row0));
+          for (int i = 0; i < 4; ++i)
+            if (boxed(i)) load_delta(i, i, 0);
+          if (boxed(4)) {
+            expect(1);
+            load_delta(4, 4, 1);
+#pragma unroll 1
+            for (int i = 5; i < 8; ++i)
+              if (boxed(i) && lane == 0) tma_prefetch_l2(&P.d, w.col + column(16 * i), int(row0));
+          }
         }
       }
       float2 acc[kChunks * C / 2];
@@ -524,11 +526,11 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
             tc_fence_before();
             __syncwarp();
             lin_arrive(tempty(buf), ok && lane == 0);
-            if ((buf += kSub) >= kSlots) buf -= kSlots, tphase ^= 1u;
+            if (++buf == kSlots) buf = 0, tphase ^= 1u;
           };
           if (ok && rows) {
             // a chunk is on its way while the one before is added; the slot is given back when the last has come
-            const uint32_t at = tmem + buf * kSlotCols + (k % DEEP) * W + lanes + (kSub == 2 ? 0 : off);
+            const uint32_t at = tmem + buf * kSlotCols + (k % DEEP) * W + lanes + off;
             uint32_t r[kChunks > 1 ? 2 : 1][C];
             tmem_ldn(at, r[0]);
 #pragma unroll
@@ -549,61 +551,112 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
         lin_arrive(sempty(g), ok && lane == 0);
       }
       if (W == 256 && P.boxes) {
-        // 16 columns at a time (64 bytes of fp32): delta's box is read, and its place filled with the one four on; a box is
-        // stored when it is full, every time or (bf16) every other.
-        uint32_t out = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (!boxed(i)) continue;
-          float2* a = acc + 8 * i;
-          if (joins) {
-            ok = lin_wait(came(warp - 4, i & 3), dphase >> (i & 3) & 1u, ab, kSiteLinear + 12) && ok;
-            dphase ^= 1u << (i & 3);
-            const uint32_t at = box0 + (i & 3) * kBox + lane * 64;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float4 v;
-              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                           : "r"(at + ((j ^ (lane >> 1 & 3)) << 4))
-                           : "memory");
-              a[2 * j].x += v.x; a[2 * j].y += v.y; a[2 * j + 1].x += v.z; a[2 * j + 1].y += v.w;
-            }
-            __syncwarp();
-            if (i < 4 && boxed(i + 4) && ok) load_delta(i + 4);
-          }
-          const bool first = P.out_f32 || i % 2 == 0, full = P.out_f32 || i % 2 == 1 || !boxed(i + 1);
-          if (first) {
-            if (joins) {
-              out = box0 + (kBoxesDelta - 1) * kBox;
-              if (lane == 0) tma_store_wait_read<0>();
-            } else {
-              out = box0 + turn * kBox;
-              turn = turn == kBoxesPlain - 1 ? 0 : turn + 1;
-              if (lane == 0) tma_store_wait_read<kBoxesPlain - 1>();
-            }
-            __syncwarp();
-          }
+        // The warp's 128 columns, in boxes of 32 (bf16) or 16 (fp32). A box holds 32 rows of 64 bytes, whose 16-byte pieces are
+        // permuted by the row's bits 1 and 2; a lane reads and writes its own row's.
+        const uint32_t mine = box0 + lane * 64, turn = lane >> 1 & 3;
+        auto put = [&](int i, uint32_t box) {      // 16 columns from the i-th 16 on
+          const float2* a = acc + 8 * i;
           if (P.out_f32) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)),
-                           "f"(a[2 * j].x), "f"(a[2 * j].y), "f"(a[2 * j + 1].x), "f"(a[2 * j + 1].y)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + box * kBox + ((j ^ turn) << 4)), "f"(a[2 * j].x),
+                           "f"(a[2 * j].y), "f"(a[2 * j + 1].x), "f"(a[2 * j + 1].y)
                            : "memory");
           } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 64 + (((2 * (i & 1) + j) ^ (lane >> 1 & 3)) << 4)),
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + box * kBox + (((2 * (i & 1) + j) ^ turn) << 4)),
                            "r"(bf16x2_bits(a[4 * j].x, a[4 * j].y)), "r"(bf16x2_bits(a[4 * j + 1].x, a[4 * j + 1].y)),
                            "r"(bf16x2_bits(a[4 * j + 2].x, a[4 * j + 2].y)), "r"(bf16x2_bits(a[4 * j + 3].x, a[4 * j + 3].y))
                            : "memory");
           }
-          if (full) {
-            fence_proxy_async();
-            __syncwarp();
+        };
+        auto send = [&](int i, uint32_t box) {     // lane 0: a box whose first column is the i-th 16's
+          if (ok && boxed(i)) tma_store(&P.o, box0 + box * kBox, w.col + column(16 * i), int(row0), policy_normal());
+        };
+        auto join = [&](int i, uint32_t place) {   // delta's box i
+          float2* a = acc + 8 * i;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float4 v;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                         : "r"(mine + place * kBox + ((j ^ turn) << 4))
+                         : "memory");
+            a[2 * j].x += v.x; a[2 * j].y += v.y; a[2 * j + 1].x += v.z; a[2 * j + 1].y += v.w;
+          }
+        };
+        auto handed = [&]() {                      // the boxes are written
+          fence_proxy_async();
+          __syncwarp();
+        };
+        if (!boxed(0)) {
+          // (nothing of the tile is the warp's)
+        } else if constexpr (JOINS) {
+          // First half: delta's boxes have come during the k-blocks. The results go over them, and what is free again takes
+          // the second half's boxes (all but one: that came with the first).
+          ok = lin_wait(came(warp - 4, 0), dphase & 1u, ab, kSiteLinear + 12) && ok;
+          dphase ^= 1u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) join(i, i);
+          __syncwarp();
+          if (!P.out_f32 && ok && boxed(4)) {
+            if (boxed(5)) load_delta(5, 2, 1);
+            if (boxed(6)) load_delta(6, 3, 1);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put(i, P.out_f32 ? i : i / 2);
+          handed();
+          if (lane == 0) {
+            for (int i = 0; i < 4; i += P.out_f32 ? 1 : 2) send(i, P.out_f32 ? i : i / 2);
+            tma_store_commit();
+            tma_store_wait_read<0>();
+          }
+          __syncwarp();
+          if (ok && boxed(4)) {
+            if (P.out_f32) {
+              if (boxed(5)) load_delta(5, 2, 1);
+              if (boxed(6)) load_delta(6, 3, 1);
+            }
+            if (boxed(7)) load_delta(7, 0, 1);
+          }
+          if (boxed(4)) {
+            ok = lin_wait(came(warp - 4, 1), dphase >> 1 & 1u, ab, kSiteLinear + 12) && ok;
+            dphase ^= 2u;
+            join(4, 4);
+            join(5, 2);
+            join(6, 3);
+            join(7, 0);
+            put(4, 4);
+            put(5, P.out_f32 ? 2 : 4);
+            put(6, P.out_f32 ? 3 : 2);
+            put(7, P.out_f32 ? 0 : 2);
+            handed();
             if (lane == 0) {
-              if (ok) tma_store(&P.o, out, w.col + column(P.out_f32 ? 16 * i : 16 * (i & ~1)), int(row0), policy_normal());
+              send(4, 4);
+              if (P.out_f32) send(5, 2);
+              send(6, P.out_f32 ? 3 : 2);
+              if (P.out_f32) send(7, 0);
               tma_store_commit();
+            }
+          }
+        } else {
+          // (bf16: all at once; fp32 fills the four boxes twice)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 0 || P.out_f32) {
+              if (lane == 0) tma_store_wait_read<0>();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int i = 4 * h; i < 4 * h + 4; ++i) put(i, P.out_f32 ? i & 3 : i / 2);
+            if (h == 1 || P.out_f32) {
+              handed();
+              if (lane == 0) {
+                const int step = P.out_f32 ? 1 : 2;
+                for (int i = P.out_f32 ? 4 * h : 0; i < 4 * h + 4; i += step) send(i, P.out_f32 ? i & 3 : i / 2);
+                tma_store_commit();
+              }
             }
           }
         }
