@@ -15,6 +15,7 @@
 #include "block8.cuh"
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 namespace mlp {
@@ -402,16 +403,19 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
   float m_lo;
   const float m_hi = over_t(m, &m_lo);
   const float gap = P.teacher_lse ? ((lse - m_hi) - m_lo) - log_s : fmaf(tm - m, inv_t, log_t - log_s);
+  // Logits far from the teacher's (a row whose mask leaves only the type's lowest value) lose the digits of t in t - z:
+  // there, log p and log q each from its own maximum.
+  const bool near = fabsf(gap) < 64.f;
   float sum_p = 0.f, loss = 0.f;
   for (int i = lane; i < P.top; i += 32) {
     const float ti = r.t[i];
     float p = -1.f;
     if (ti != -kInf) {
       float lo;
-      const float h = over_t(ti, &lo);
-      p = expf(P.teacher_lse ? (h - lse) + lo : (ti - tm) * inv_t - log_t);
+      const float h = over_t(ti, &lo), log_p = P.teacher_lse ? (h - lse) + lo : (ti - tm) * inv_t - log_t;
+      p = expf(log_p);
       sum_p += p;
-      if (p != 0.f) loss += p * ((ti - r.z[i]) * inv_t - gap);
+      if (p != 0.f) loss += p * (near ? (ti - r.z[i]) * inv_t - gap : log_p - ((r.z[i] - m) * inv_t - log_s));
     }
     P.probs[row * P.top + i] = p;
   }
@@ -785,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 || SHIFT ? 
 }
 
 bool args_ok(int type, int id_bytes, float temperature, int64_t M, int64_t V, int64_t top) {
-  return type_ok(type) && (id_bytes == 4 || id_bytes == 8) && temperature > 0.f && temperature < kInf && M >= 0 &&
+  return type_ok(type) && (id_bytes == 4 || id_bytes == 8) && temperature >= FLT_MIN && temperature < kInf && M >= 0 &&
          M < (int64_t(1) << 28) && V >= 1 && V < (int64_t(1) << 22) && top >= 1 && top <= kMaxTop;
 }
 
@@ -796,7 +800,7 @@ template <int KIND, int VEC, bool SHIFT>
 cudaError_t launch_fwd(DistillArgs& P, int cl, int nsm, cudaStream_t st) {
   const size_t smem = size_t(cl > 1 ? 1 : 2) * (even(P.groups) + 4 * P.top) * 4;
   // as many CTAs as are resident (the lists of a long vocabulary leave room for fewer)
-  const int64_t room = std::max<int64_t>(1, 227 * 1024 / int64_t(smem + 2048));
+  const int64_t room = std::max<int64_t>(1, 227 * 1024 / int64_t(smem + sizeof(Part) * kPlaces * kThreads + 2048));
   const int64_t ctas = nsm * std::min<int64_t>(kMinCtas<KIND, SHIFT>, room);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(cl > 1 ? P.M * cl : std::min<int64_t>(P.M, ctas)));

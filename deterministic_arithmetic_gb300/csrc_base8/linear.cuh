@@ -83,8 +83,10 @@ struct LinAbort {
 __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site, bool teardown = false,
                                                 bool quarter = false) {
   // (the clock takes longer to read than most waits last: not before some tries)
-  for (uint32_t it = 0; it < 1024u; ++it)
+  for (uint32_t it = 1; it <= 1024u; ++it) {
     if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    if (it % 64u == 0u && !teardown && __any_sync(0xffffffffu, ab.raised())) return false;
+  }
   const uint32_t us = ab.status[3];
   uint64_t limit = teardown ? kDrainLimitNs : (us ? uint64_t(us) * 1000ull : kWaitLimitNs);
   if (quarter) limit /= 4;
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       // Whether stage idx has landed and slot buf has been read: tested as soon as the one before is issued. (This warp's own
       // steps are what bounds the large tiles.)
       bool landed = false, free = true, ok = true;
-      for (int u = first; u < P.total && ok; u += step) {
+      for (int u = first; u < P.total; u += step) {
         for (int kb = 0; kb < P.nk; kb += DEEP) {
           if (!__all_sync(0xffffffffu, landed)) ok = lin_wait(full(idx), phase, ab, kSiteLinear + 5);
           if (!ok) break;
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       int buf = 0;
       uint32_t tphase = 0;
       bool ok = true;
-      for (int u = first; u < P.total && ok; u += step)
+      for (int u = first; u < P.total; u += step)
         for (int i = 0; i < P.nk && ok; ++i) {
           ok = lin_wait(tempty(buf), tphase, ab, kSiteLinear + 11);
           lin_arrive_peer(peer_addr(tempty(buf), 0), ok && lane == 0);
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     // pair's 4096 x 17408 -> 5120, 411 us so, 337 with these warps.)
     uint32_t n = 0;                                // groups so far, of both warps
     bool ok = true;
-    for (int u = first; u < P.total && ok; u += step) {
+    for (int u = first; u < P.total; u += step) {
       const LinUnit w = lin_unit<CG>(P, u);
       const int64_t row0 = int64_t(w.tm * CG + rank) * kBM + lane;
       const float* sb[2];
@@ -464,6 +466,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     auto scale_of = [](int i) { return i * kScales / (W / 2); };   // which of the scales that has
     int buf = 0;
     uint32_t tphase = 0, n = 0;                    // groups of scales so far
+    bool ok = true;                                // no wait has run out: once one has, nothing more is loaded or stored
     const uint32_t box0 = base + lin_ring(W, JOINS) + (warp - 4) * lin_boxes(W, JOINS) * kBox;
     uint32_t dphase = 0;
     for (int u = first; u < P.total; u += step) {
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
         if (lane == 0) mbar_expect_tx(came(warp - 4, half), boxes * kBox);
       };
       if constexpr (JOINS) {
-        if (boxed(0)) {
+        if (ok && boxed(0)) {
           if (lane == 0) tma_store_wait_read<0>();   // the tile before has left the places
           __syncwarp();
           expect(0);
@@ -506,7 +509,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       float2 acc[kChunks * C / 2];
 #pragma unroll
       for (int i = 0; i < kChunks * C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-      bool ok = true;
       for (int kb0 = 0; kb0 < P.nk; kb0 += kScaleGroup, ++n) {
         const uint32_t g = n % kScaleGroups, sg = scales + g * kScaleGroup * kScaleBytes;
         ok = lin_wait(sfull(g), n / kScaleGroups & 1u, ab, kSiteLinear + 10) && ok;
