@@ -5,7 +5,7 @@
 // relative to it, of everything that is no entry of the teacher's; the row's few entries are read on their own, and
 // their part joined at the end. So the mass of the rest is a sum, and no difference. Bound by HBM.
 //
-// A row is cut into groups of 256 elements, dealt in turn to the places of eight warps (1, 2, 4 or 8 each, by the row's length
+// A row is cut into groups of 256 elements, dealt in turn to the places of eight warps (1, 2 or 4 each, by the row's length
 // alone); each thread of a place holds a maximum and a sum of its own, and the places' are joined in a fixed order. A batch of
 // few rows has its rows' places spread over the CTAs of a cluster: the places, and so the bits, stay the same.
 #include "../csrc/common.cuh"
@@ -23,7 +23,7 @@ namespace {
 
 using namespace lora;
 
-constexpr int kThreads = 256, kWarps = 8, kGroupElems = 256, kPlaces = 8;
+constexpr int kThreads = 256, kWarps = 8, kGroupElems = 256, kPlaces = 4;
 constexpr int kMaxTop = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kInf = __builtin_huge_valf();
 
@@ -46,7 +46,7 @@ __device__ __forceinline__ void shifted(uint32_t (&u)[8], int first, uint32_t (&
 // What a thread holds of a group of 256 elements of its warp: 8 of them, in pieces of VEC consecutive ones, 32 VEC apart:
 // one of 8 (bf16), two of 4 (fp32), or (fp32 rows of odd lengths) single ones. SHIFT: bf16 rows whose length is no multiple of
 // 8 start at any element; their pieces are put together from the two 16-byte vectors that hold them (loads of 2 bytes took
-// 4096 x 50257 forward 201 us, 166 so, and 405 backward, 226).
+// 4096 x 50257 forward 201 us where this took 166; by pairs, from words, 232).
 template <int KIND, int VEC, bool SHIFT>
 struct Held {
   static_assert(KIND == kF32 ? !SHIFT : VEC == 8, "");
@@ -187,42 +187,55 @@ struct Held {
       return fmaxf(__low2float(m), __high2float(m));
     }
   }
-  // The values, rounded once, to the same elements. (The whole warp calls.)
-  static __device__ __forceinline__ void store(void* p, int64_t base, int off, int n, int lane, const float (&v)[8]) {
+  // The values, rounded once, to the same elements.
+  static __device__ __forceinline__ void store(void* p, int64_t base, int n, int lane, const float (&v)[8]) {
+    static_assert(!SHIFT && VEC > 1, "");
     if constexpr (KIND == kBf16) {
-      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + base;
-      const uint4 own = pack_bf16x8(v);
-      if constexpr (!SHIFT) {
-        if (8 * lane < n) *reinterpret_cast<uint4*>(q + 8 * lane) = own;
-      } else if (off == 0 && n >= kGroupElems) {
-        *reinterpret_cast<uint4*>(q + 8 * lane) = own;
-      } else {
-        // a whole vector of memory is the last `off` elements of the lane before and this lane's first; the group's ends are single
-        uint32_t u[8] = {__shfl_up_sync(0xffffffffu, own.x, 1), __shfl_up_sync(0xffffffffu, own.y, 1),
-                         __shfl_up_sync(0xffffffffu, own.z, 1), __shfl_up_sync(0xffffffffu, own.w, 1), own.x, own.y, own.z, own.w};
-        const uint32_t mine[4] = {own.x, own.y, own.z, own.w};
-        uint32_t w[4];
-        shifted(u, 8 - off, w);
-        const bool whole = n >= kGroupElems;
-        if (whole && lane > 0) *reinterpret_cast<uint4*>(q + 8 * lane - off) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (!whole || lane == 0 || lane == 31) {
-          const int lo = whole && lane == 31 ? 8 - off : 0, hi = whole && lane == 0 ? 8 - off : 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e >= lo && e < hi && 8 * lane + e < n)
-              reinterpret_cast<uint16_t*>(q)[8 * lane + e] = uint16_t(e & 1 ? mine[e / 2] >> 16 : mine[e / 2]);
-        }
-      }
-    } else if constexpr (VEC == 4) {
+      if (8 * lane < n) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + base + 8 * lane) = pack_bf16x8(v);
+    } else {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (128 * j + 4 * lane < n)
           *reinterpret_cast<float4*>(static_cast<float*>(p) + base + 128 * j + 4 * lane) =
               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
+    }
+  }
+  // load() and store() of a row that starts `lead` elements behind a 16-byte boundary, and whose groups are cut from there: `from`
+  // is the row's element (its group's first ones may lie before it) that the group starts at, `row` the row's first.
+  __device__ __forceinline__ void load_led(const void* p, int64_t row, int from, int V, bool edge, int lane) {
+    static_assert(!SHIFT && VEC > 1, "");
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (32 * j + lane < n) static_cast<float*>(p)[base + 32 * j + lane] = v[j];
+    for (int j = 0; j < 8 / VEC; ++j) {
+      const int i = from + at(VEC * j, lane);
+      uint32_t* to = w + 4 * j;
+      if (i >= V) continue;
+      if (i + VEC <= V || !edge) {
+        const uint4 t = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + (row + i) * (16 / VEC));
+        to[0] = t.x; to[1] = t.y; to[2] = t.z; to[3] = t.w;
+      } else if constexpr (KIND == kBf16) {
+        some(static_cast<const uint8_t*>(p) + (row + i) * 2, V - i, to);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = i + e < V ? static_cast<const uint32_t*>(p)[row + i + e] : 0u;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store_led(void* p, int64_t row, int from, int V, int lane, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8 / VEC; ++j) {
+      const int i = from + at(VEC * j, lane);
+      if (i >= V) continue;
+      if (i >= 0 && i + VEC <= V) {
+        if constexpr (KIND == kBf16) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + row + i) = pack_bf16x8(v);
+        else *reinterpret_cast<float4*>(static_cast<float*>(p) + row + i) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (i + e >= 0 && i + e < V) {
+            if constexpr (KIND == kBf16) static_cast<__nv_bfloat16*>(p)[row + i + e] = __float2bfloat16_rn(v[e]);
+            else static_cast<float*>(p)[row + i + e] = v[4 * j + e];
+          }
+      }
     }
   }
   // Which of the lane's elements is the group's element o; 8: none.
@@ -309,9 +322,10 @@ __device__ __forceinline__ float rescale(float s, float from, float to, float c)
   return from == -kInf && s == 0.f ? 0.f : s * ex2((from - to) * c);
 }
 
-// CTAs of an SM (2, 3 and 4 of bf16: 283, 202 and 193 us at 4096 x 131072).
+// CTAs of an SM: bf16 3, 4 and 5 194, 177 and 289 us at 4096 x 131072 (five spill), SHIFT 2 and 3 128 and 136 at 4096 x 50258, fp32
+// 2, 3 and 4 172, 167 and 176 at 2048 x 131072.
 template <int KIND, bool SHIFT>
-constexpr int kMinCtas = KIND == kF32 || SHIFT ? 2 : 4;
+constexpr int kMinCtas = KIND == kF32 ? 3 : (SHIFT ? 2 : 4);
 
 // ----------------------------------------------------------------- forward
 // A CTA has eight warps that stream its rows, and a ninth for their entries: it makes the lists of the next row and ends the one
@@ -675,9 +689,12 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
 // ---------------------------------------------------------------- backward
 // A CTA takes P.seg groups of a row; each element is written by the thread that read it. OUT8: in 8-bit blocks.
 template <int KIND, int VEC, bool SHIFT, bool OUT8>
-__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 || SHIFT ? 4 : 5)) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
+__global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 ? 4 : 5)) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
   constexpr int kLoads = 4;                        // groups of a warp in flight
-  using H = Held<KIND, VEC, SHIFT>;
+  // Rows that vectors do not fit, element by element: cut into groups from a 16-byte boundary on (4096 x 50257 bf16 226 -> 143 us,
+  // 2048 x 50257 fp32 148 -> 131). The blocks of OUT8 start with their row.
+  constexpr bool LED = !OUT8 && (SHIFT || VEC == 1);
+  using H = Held<KIND, LED ? (KIND == kF32 ? 4 : 8) : VEC, SHIFT && !LED>;
   extern __shared__ int smem[];
   const Lists L{smem + 3 * P.top + (P.top & 1), reinterpret_cast<int2*>(smem)};
   float* pl = reinterpret_cast<float*>(smem + 2 * P.top);
@@ -687,6 +704,8 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 || SHIFT ? 
   const int g0 = int(blockIdx.x - row * segs) * P.seg, g1 = min(P.groups, g0 + P.seg);
   grid_dependency_wait();
   grid_dependents_launch();
+  const int64_t base = row * P.V, ld = code_ld(P.V);
+  const int first = SHIFT && !LED ? int(base & 7) : 0, lead = LED ? int(base & (KIND == kF32 ? 3 : 7)) : 0;
   const float4 st = __ldg(reinterpret_cast<const float4*>(P.stats + row * 4));
   const float g = __ldg(P.dloss + row) * st.w / P.temperature;
   const bool zero = g == 0.f;
@@ -696,23 +715,24 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 || SHIFT ? 
     const int64_t at = row * P.top + i;
     const int id = id_at(P, at);
     const float p = __ldg(P.probs + at);
-    if (id >= 0 && !(p < 0.f) && id / kGroupElems >= g0 && id / kGroupElems < g1) {
+    const int at_group = (id + lead) / kGroupElems;
+    if (id >= 0 && !(p < 0.f) && at_group >= g0 && at_group < g1) {
       pl[i] = p;
-      L.link[i] = make_int2(atomicExch(&L.head[id / kGroupElems - g0], i), id);
+      L.link[i] = make_int2(atomicExch(&L.head[at_group - g0], i), id);
     }
   }
   __syncthreads();
   // q = 2^((x - m) c - log2 sum): the difference first, which is exact where q is large
   const float c = kLog2e / P.temperature, m = st.x, log_s = -st.y, gr = g * st.z;
-  const int64_t base = row * P.V, ld = code_ld(P.V);
-  const int first = SHIFT ? int(base & 7) : 0;
   const int cblocks = (P.V + kBlock - 1) / kBlock;
   for (int gb = g0 + warp; gb < g1; gb += kWarps * kLoads) {
     H held[kLoads];
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       const int gi = gb + kWarps * k;
-      if (gi < g1 && !zero) held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, row == P.M - 1, lane);
+      if (gi >= g1 || zero) continue;
+      if constexpr (LED) held[k].load_led(P.z, base, gi * kGroupElems - lead, P.V, row == P.M - 1, lane);
+      else held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, row == P.M - 1, lane);
     }
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
@@ -737,15 +757,17 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 || SHIFT ? 
         }
         for (int i = L.head[gi - g0]; i >= 0;) {
           const int2 link = L.link[i];
-          const uint32_t mine = H::elem_of(uint32_t(link.y - gi * kGroupElems), uint32_t(lane));
+          const uint32_t mine = H::elem_of(uint32_t(link.y + lead - gi * kGroupElems), uint32_t(lane));
           const float pg = pl[i] * g;
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = mine == uint32_t(e) ? fmaf(x[e], g, -pg) : v[e];
           i = link.x;
         }
       }
-      if constexpr (!OUT8) {
-        H::store(P.dz, base + int64_t(gi) * kGroupElems, first, n, lane, v);
+      if constexpr (LED) {
+        H::store_led(P.dz, base, gi * kGroupElems - lead, P.V, lane, v);
+      } else if constexpr (!OUT8) {
+        H::store(P.dz, base + int64_t(gi) * kGroupElems, n, lane, v);
       } else {
         // the two blocks of the group: of 8 consecutive elements a lane, 16 lanes each; else the first and last four
         // of every lane. (What lies past column V is no value: 0, and written up to the codes' row length.)
@@ -814,13 +836,14 @@ cudaError_t launch_fwd(DistillArgs& P, int cl, int nsm, cudaStream_t st) {
   attr[1].val.clusterDim = {unsigned(cl), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = cl > 1 ? 2 : 1;
-  if (cl == 8) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 8>, P);
   if (cl == 4) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 4>, P);
   if (cl == 2) return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 2>, P);
   return cudaLaunchKernelEx(&cfg, distill_fwd_kernel<KIND, VEC, SHIFT, 1>, P);
 }
 template <int KIND, int VEC, bool SHIFT>
 cudaError_t launch_bwd(DistillArgs& P, bool out8, cudaStream_t st) {
+  // (a row that starts behind a 16-byte boundary may reach one group further)
+  if (!out8 && (SHIFT || VEC == 1)) P.groups = int(cdiv(P.V + (KIND == kF32 ? 3 : 7), kGroupElems));
   const size_t smem = size_t(P.seg + 3 * P.top + 1) * 4;
   const dim3 grid(unsigned(P.M * cdiv(P.groups, P.seg)));
   return out8 ? launch_pdl(distill_bwd_kernel<KIND, VEC, SHIFT, true>, grid, dim3(kThreads), smem, st, P)
@@ -835,7 +858,6 @@ cudaError_t prepare() {
   set(distill_fwd_kernel<KIND, VEC, SHIFT, 1>);
   set(distill_fwd_kernel<KIND, VEC, SHIFT, 2>);
   set(distill_fwd_kernel<KIND, VEC, SHIFT, 4>);
-  set(distill_fwd_kernel<KIND, VEC, SHIFT, 8>);
   set(distill_bwd_kernel<KIND, VEC, SHIFT, false>);
   set(distill_bwd_kernel<KIND, VEC, SHIFT, true>);
   return e;
@@ -898,9 +920,13 @@ lora_status lora_distill_topk_fwd(const void* logits, int type, const void* ids,
   P.loss = loss;
   P.probs = probs;
   P.stats = stats;
-  // as many places as leave each a set's rounds, of the row's length alone
-  P.places = 1;
-  while (P.places < kPlaces && P.places * kWarps * set_of(type == LORA_F32 ? kF32 : kBf16) < P.groups) P.places *= 2;
+  // Of the row's length alone: one place while a row is short, two, or four where that leaves no warp more half sets. Of many
+  // rows fewer places are faster, of few rows more (4096 x 32000 by 1, 2, 4, 8: 61.5, 61.1, 97.7 and 176 us; 4096 x 50257 135, 141, 160
+  // and 249, one row of it 15.6, 9.6, 9.8 and 8.4; 4096 x 131072 179, 179, 181 and 187, one row 16.5, 10.8, 8.2 and 8.1; 4096 x
+  // 151936 219, 222, 253 and 333).
+  const int half = kWarps * set_of(type == LORA_F32 ? kF32 : kBf16) / 2;
+  const auto halves = [&](int places) { return places * cdiv(P.groups, places * half); };
+  P.places = P.groups <= 96 ? 1 : (P.groups >= 448 && halves(4) == halves(1) ? 4 : 2);
   // few rows: a row's places over the CTAs of a cluster
   int cl = 1;
   while (cl < P.places && M * cl * 2 <= 2 * nsm) cl *= 2;
@@ -934,7 +960,7 @@ lora_status lora_distill_topk_bwd(const float* dloss, const void* logits, int ty
   P.dz = dlogits;
   P.scales = scales;
   P.seg = 64;
-  if (M * cdiv(P.groups, P.seg) >= (int64_t(1) << 31)) return LORA_ERR_SHAPE;
+  if (M * (cdiv(P.groups, P.seg) + 1) >= (int64_t(1) << 31)) return LORA_ERR_SHAPE;
   int nsm = 0;
   if ((s = device_ready(&nsm)) != LORA_OK) return s;
   const cudaError_t e = by_length(type, V, [&](auto kind, auto vec, auto shift) {

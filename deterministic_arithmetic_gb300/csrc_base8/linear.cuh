@@ -85,7 +85,6 @@ __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, L
   // (the clock takes longer to read than most waits last: not before some tries)
   for (uint32_t it = 1; it <= 1024u; ++it) {
     if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
-    if (it % 64u == 0u && !teardown && __any_sync(0xffffffffu, ab.raised())) return false;
   }
   const uint32_t us = ab.status[3];
   uint64_t limit = teardown ? kDrainLimitNs : (us ? uint64_t(us) * 1000ull : kWaitLimitNs);
@@ -466,7 +465,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
     auto scale_of = [](int i) { return i * kScales / (W / 2); };   // which of the scales that has
     int buf = 0;
     uint32_t tphase = 0, n = 0;                    // groups of scales so far
-    bool ok = true;                                // no wait has run out: once one has, nothing more is loaded or stored
+    // No wait has run out. Once one has, no more of delta is loaded: a barrier that was told of boxes is told no second time.
+    bool ok = true;
     const uint32_t box0 = base + lin_ring(W, JOINS) + (warp - 4) * lin_boxes(W, JOINS) * kBox;
     uint32_t dphase = 0;
     for (int u = first; u < P.total; u += step) {
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
         }
       }
       float2 acc[kChunks * C / 2];
+      if constexpr (!JOINS) ok = true;               // (kept across tiles, it costs the large ones 2 %)
 #pragma unroll
       for (int i = 0; i < kChunks * C / 2; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int kb0 = 0; kb0 < P.nk; kb0 += kScaleGroup, ++n) {
