@@ -59,7 +59,7 @@ struct Held {
     return static_cast<const uint8_t*>(p) + (base - off + lane * VEC) * kBytes;
   }
   // Elements of the group whose lane's place is `at`, of which n exist (the others stay what they were). off: the row's first
-  // element % 8. edge: nothing lies behind the row's end.
+  // element % 8. edge: nothing need lie behind the row's end.
   __device__ __forceinline__ void load_whole(const uint8_t* at, int off) {
     if constexpr (KIND == kBf16) {
       uint4 t = *reinterpret_cast<const uint4*>(at);
@@ -291,6 +291,9 @@ __device__ __forceinline__ int id_at(const DistillArgs& P, int64_t i) {
   const int v = __ldg(static_cast<const int*>(P.ids) + i);
   return v >= 0 && v < P.V ? v : -1;
 }
+
+// Whether a vector that holds elements of the row may reach past the tensor's end.
+__device__ __forceinline__ bool at_edge(const DistillArgs& P, int64_t row) { return (P.M - 1 - row) * P.V < 8; }
 
 // The entries of a row by group: head[g] the first of group g, link[i] the one after entry i, -1 at the end, and its id (-1 where
 // it is none). The order within a group is no fixed one; nothing depends on it.
@@ -543,7 +546,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fw
       more = to >= 0;
       to_j = 0;
       to_off = offset(to);
-      to_edge = to == P.M - 1;
+      to_edge = at_edge(P, to);
       to_left = P.V - first_of(0);
       to_at = H::place(P.z, to * P.V + first_of(0), to_off, lane);
     }
@@ -706,6 +709,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 ? 4 : 5)) d
   grid_dependents_launch();
   const int64_t base = row * P.V, ld = code_ld(P.V);
   const int first = SHIFT && !LED ? int(base & 7) : 0, lead = LED ? int(base & (KIND == kF32 ? 3 : 7)) : 0;
+  const bool edge = at_edge(P, row);
   const float4 st = __ldg(reinterpret_cast<const float4*>(P.stats + row * 4));
   const float g = __ldg(P.dloss + row) * st.w / P.temperature;
   const bool zero = g == 0.f;
@@ -731,8 +735,8 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 2 : (OUT8 ? 4 : 5)) d
     for (int k = 0; k < kLoads; ++k) {
       const int gi = gb + kWarps * k;
       if (gi >= g1 || zero) continue;
-      if constexpr (LED) held[k].load_led(P.z, base, gi * kGroupElems - lead, P.V, row == P.M - 1, lane);
-      else held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, row == P.M - 1, lane);
+      if constexpr (LED) held[k].load_led(P.z, base, gi * kGroupElems - lead, P.V, edge, lane);
+      else held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, edge, lane);
     }
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {

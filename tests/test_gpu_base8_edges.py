@@ -254,3 +254,34 @@ def test_refusals():
     for bad in (lambda: g(d, z, i, probs, stats, block8=True, dlogits=z), lambda: g(d, z, i, probs, stats, dlogits=x)):
         with pytest.raises((TypeError, ValueError)):
             bad()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("v", [1, 2, 3, 5, 7, 9])
+def test_what_lies_behind_the_last_row_has_no_part(v, dtype):
+    """Rows shorter than a vector, the last of them in one with what is not the tensor's."""
+    for m in (1, 2, 5, 13):
+        c = make(m, v, 2, dtype, tail=v > 2)
+        room = torch.full((m * v + 16,), float("nan"), dtype=dtype, device="cuda")
+        room[:m * v] = c["logits"].flatten()
+        c["logits"] = room[:m * v].view(m, v)
+        check(c)
+        _, probs, stats = fwd(c)
+        bwd(c, torch.ones(m, device="cuda"), probs, stats, dlogits=c["logits"])
+        assert bool(room[:m * v].isfinite().all()) and bool(room[m * v:].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("v", [24576, 24577, 32000, 114688, 115001, 131072])
+def test_long_rows(v, dtype):
+    """Rows of one, two and four places: a row alone, in a few and in many."""
+    c = make(400, v, 30, dtype, tail=True)
+    loss, probs, stats = fwd(c)
+    dl = torch.rand(400, device="cuda")
+    dz = bwd(c, dl, probs, stats)
+    for rows in (slice(3, 4), slice(5, 30), slice(60, 260)):
+        d = {k: (x[rows].clone() if isinstance(x, torch.Tensor) else x) for k, x in c.items()}
+        got = fwd(d)
+        assert all(same(a, b[rows]) for a, b in zip(got, (loss, probs, stats)))
+        assert same(bwd(d, dl[rows].clone(), got[1], got[2]), dz[rows])
+    check({k: (x[5:8].clone() if isinstance(x, torch.Tensor) else x) for k, x in c.items()})
