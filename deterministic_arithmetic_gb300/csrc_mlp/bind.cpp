@@ -96,6 +96,17 @@ int first(const Tensor& t, const char* name, int64_t* rows, int64_t* cols) {
 Tensor empty(c10::IntArrayRef shape, at::ScalarType type, int dev) {
   return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, c10::DeviceIndex(dev)), std::nullopt);
 }
+// A tensor over part of another's memory. Small outputs of one call share an allocation (a call with three outputs takes 4.4 us
+// of the host so, 5.8 with one each); large ones do not: a caller that keeps one would keep all.
+constexpr int64_t kShared = 1 << 20;
+Tensor part(const Tensor& whole, int64_t from, c10::IntArrayRef shape, at::ScalarType type) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                      c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(from / int64_t(c10::elementSize(type)));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+int64_t to_16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
 // An output: the caller's tensor, checked, or a new one.
 Tensor out(PyObject* o, const char* name, c10::IntArrayRef shape, at::ScalarType type, int dev) {
   if (o == Py_None) return empty(shape, type, dev);
@@ -413,13 +424,24 @@ Block check_block(PyObject* o, const char* name, int64_t rows, int64_t cols, int
 }
 // A new Block8; *b its parts.
 PyObject* new_block(int64_t rows, int64_t cols, int64_t tile, int dev, Block* b) {
-  const Tensor c = empty({rows, code_ld(cols)}, F8, dev), s = empty({blocks(rows, tile), blocks(cols, 128)}, F32, dev);
+  const int64_t codes = rows * code_ld(cols), scales = 4 * blocks(rows, tile) * blocks(cols, 128);
+  Tensor c, s;
+  if (codes + scales <= kShared) {
+    const Tensor all = empty({codes + scales}, U8, dev);
+    c = part(all, 0, {rows, code_ld(cols)}, F8);
+    s = part(all, codes, {blocks(rows, tile), blocks(cols, 128)}, F32);
+  } else {
+    c = empty({rows, code_ld(cols)}, F8, dev);
+    s = empty({blocks(rows, tile), blocks(cols, 128)}, F32, dev);
+  }
   *b = {c.data_ptr(), s.data_ptr<float>(), rows, cols, tile, dev};
   Ref a(wrap(c)), t(wrap(s)), n(PyLong_FromLongLong(cols)), r(PyLong_FromLongLong(tile));
-  PyObject* args[] = {a.p, t.p, n.p, r.p};
-  PyObject* made = PyObject_Vectorcall(block_type, args, 4, nullptr);
-  if (!made) throw Raised{};
-  return made;
+  PyTypeObject* type = reinterpret_cast<PyTypeObject*>(block_type);
+  Ref made(type->tp_alloc(type, 0));               // (its fields, without the call of its __init__)
+  if (PyObject_SetAttr(made.p, codes_name, a.p) || PyObject_SetAttr(made.p, scales_name, t.p) ||
+      PyObject_SetAttr(made.p, cols_name, n.p) || PyObject_SetAttr(made.p, tile_name, r.p))
+    throw Raised{};
+  return made.release();
 }
 
 PyObject* block8(PyObject* const* a) {                        // x, tile, out
@@ -480,8 +502,18 @@ PyObject* distill_topk_fwd(PyObject* const* a) {  // logits, ids, teacher, tempe
   const float temperature = float(number(a[3]));
   const float* lse = a[4] == Py_None ? nullptr : static_cast<const float*>(check(a[4], "teacher_lse", {M}, F32, dev));
   const float* w = a[5] == Py_None ? nullptr : static_cast<const float*>(check(a[5], "weight", {M}, F32, dev));
-  const Tensor loss = out(a[6], "loss", {M}, F32, dev), probs = out(a[7], "probs", {M, top}, F32, dev);
-  const Tensor stats = out(a[8], "stats", {M, 4}, F32, dev);
+  Tensor loss, probs, stats;
+  const int64_t at_probs = 16 * M, at_loss = at_probs + to_16(4 * M * top), all = at_loss + 4 * M;
+  if (a[6] == Py_None && a[7] == Py_None && a[8] == Py_None && all <= kShared) {
+    const Tensor whole = empty({all}, U8, dev);
+    stats = part(whole, 0, {M, 4}, F32);
+    probs = part(whole, at_probs, {M, top}, F32);
+    loss = part(whole, at_loss, {M}, F32);
+  } else {
+    loss = out(a[6], "loss", {M}, F32, dev);
+    probs = out(a[7], "probs", {M, top}, F32, dev);
+    stats = out(a[8], "stats", {M, 4}, F32, dev);
+  }
   done(lora_distill_topk_fwd(zp, type, ip, bytes, tp, tt, lse, w, temperature, M, V, top, loss.data_ptr<float>(),
                              probs.data_ptr<float>(), stats.data_ptr<float>(), stream(dev)), "lora_distill_topk_fwd");
   return tuple(wrap(loss), wrap(probs), wrap(stats));

@@ -21,7 +21,8 @@ def distill_topk_fwd(logits, ids, teacher, *, temperature: float = 1.0, teacher_
     An id outside the vocabulary (-1, say), a logit of -infinity and a second entry of an id are no entries.
     ``teacher_lse`` [M] fp32: log(sum of exp(t / T)) over the teacher's vocabulary. ``weight`` [M] fp32 multiplies
     the loss; rows of weight 0 are not read. ``loss`` [M] is fp32, unreduced, without a factor of T * T; ``probs``
-    [M, top] (the teacher's probabilities, -1 for no entry) and ``stats`` [M, 4] are for the backward pass."""
+    [M, top] (the teacher's probabilities, -1 for no entry) and ``stats`` [M, 4] are for the backward pass. (New ones of up
+    to 1 MiB together lie in one allocation.)"""
     return c.mlp.distill_topk_fwd(logits, ids, teacher, temperature, teacher_lse, weight, loss, probs, stats)
 
 

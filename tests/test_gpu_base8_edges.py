@@ -285,3 +285,31 @@ def test_long_rows(v, dtype):
         assert all(same(a, b[rows]) for a, b in zip(got, (loss, probs, stats)))
         assert same(bwd(d, dl[rows].clone(), got[1], got[2]), dz[rows])
     check({k: (x[5:8].clone() if isinstance(x, torch.Tensor) else x) for k, x in c.items()})
+
+
+def test_outputs_of_one_call_are_tensors_of_their_own():
+    """Small outputs may lie in one allocation: each can be written, kept, saved and viewed alone, and outlives the others."""
+    import io
+
+    x = rnd(5, 300)
+    p = b8().block8(x)
+    want = b8().unblock8(p)
+    q = b8().Block8(p.codes, p.scales.clone(), p.cols, p.tile)
+    p.scales.zero_()
+    assert same(b8().unblock8(q), want) and repr(p).startswith("Block8(codes=") and p == p
+    assert p.codes.is_contiguous() and p.scales.is_contiguous() and p.codes.data_ptr() % 16 == p.scales.data_ptr() % 16 == 0
+    c = make(7, 130, 5)
+    loss, probs, stats = fwd(c)
+    ref = [t.clone() for t in (loss, probs, stats)]
+    f = io.BytesIO()
+    torch.save(probs, f)
+    f.seek(0)
+    assert torch.equal(torch.load(f), ref[1])
+    loss.fill_(3.0)
+    assert torch.equal(probs, ref[1]) and torch.equal(stats, ref[2])
+    del probs, loss
+    torch.cuda.synchronize()
+    junk = [torch.full((7, 5), 9.0, device="cuda") for _ in range(20)]
+    assert torch.equal(stats, ref[2]) and len(junk) == 20
+    stats.requires_grad_()
+    assert (stats * 2).sum().requires_grad
