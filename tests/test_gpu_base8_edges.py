@@ -313,3 +313,31 @@ def test_outputs_of_one_call_are_tensors_of_their_own():
     assert torch.equal(stats, ref[2]) and len(junk) == 20
     stats.requires_grad_()
     assert (stats * 2).sum().requires_grad
+
+
+@pytest.mark.parametrize("m,k,n,back", [(2, (1 << 22) - 1, 8, False), (3, 24, (1 << 22) - 1, True), (2, 40, (1 << 22) - 1, False),
+                                        (1, (1 << 22) - 1, 40, True), ((1 << 22) - 1, 24, 16, False)])
+def test_products_of_the_largest_sizes(m, k, n, back):
+    from test_gpu_block8 import check_product
+
+    x, w = operands(m, k, n, back)
+    y = check_product(x, w, back)
+    assert bool(y.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_longest_rows_and_most_entries(dtype):
+    m, v = 320, (1 << 22) - 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.empty(m, v, dtype=dtype, device="cuda").normal_(generator=g)
+    ids = torch.randint(0, v, (m, 1024), generator=g, device="cuda")
+    t = torch.randn(m, 1024, generator=g, device="cuda")
+    c = dict(logits=z, ids=ids, teacher=t, teacher_lse=torch.logsumexp(t, 1) + 0.5, weight=None, temperature=1.0)
+    loss, probs, stats = fwd(c)
+    few = {k: (x[-2:].clone() if isinstance(x, torch.Tensor) else x) for k, x in c.items()}
+    got = check(few)
+    assert all(same(a, b[-2:]) for a, b in zip(got[:3], (loss, probs, stats)))
+    dl = torch.rand(m, device="cuda")
+    dz = bwd(few, dl[-2:].clone(), *got[1:3])
+    bwd(c, dl, probs, stats, dlogits=z)
+    assert same(z[-2:], dz)
