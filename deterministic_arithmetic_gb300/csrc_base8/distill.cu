@@ -46,7 +46,7 @@ __device__ __forceinline__ void shifted(uint32_t (&u)[8], int first, uint32_t (&
 // What a thread holds of a group of 256 elements of its warp: 8 of them, in pieces of VEC consecutive ones, 32 VEC apart:
 // one of 8 (bf16), two of 4 (fp32), or (fp32 rows of odd lengths) single ones. SHIFT: bf16 rows whose length is no multiple of
 // 8 start at any element; their pieces are put together from the two 16-byte vectors that hold them (loads of 2 bytes took
-// 4096 x 50257 forward 201 us where this took 166; by pairs, from words, 232).
+// 4096 x 50257 forward 201 us where this took 166; by pairs, from words, 232; 115 since, in sets of four).
 template <int KIND, int VEC, bool SHIFT>
 struct Held {
   static_assert(KIND == kF32 ? !SHIFT : VEC == 8, "");
@@ -325,10 +325,10 @@ __device__ __forceinline__ float rescale(float s, float from, float to, float c)
   return from == -kInf && s == 0.f ? 0.f : s * ex2((from - to) * c);
 }
 
-// CTAs of an SM: bf16 3, 4 and 5 194, 177 and 289 us at 4096 x 131072 (five spill), SHIFT 2 and 3 128 and 136 at 4096 x 50258, fp32
-// 2, 3 and 4 172, 167 and 176 at 2048 x 131072.
-template <int KIND, bool SHIFT>
-constexpr int kMinCtas = KIND == kF32 ? 3 : (SHIFT ? 2 : 4);
+// CTAs of an SM: bf16 3, 4 and 5 194, 177 and 289 us at 4096 x 131072 (five spill), fp32 2, 3 and 4 172, 167 and 176 at 2048 x
+// 131072.
+template <int KIND>
+constexpr int kMinCtas = KIND == kF32 ? 3 : 4;
 
 // ----------------------------------------------------------------- forward
 // A CTA has eight warps that stream its rows, and a ninth for their entries: it makes the lists of the next row and ends the one
@@ -461,15 +461,16 @@ __device__ __noinline__ float far_sum(H v, float m, float c) {
   return sum;
 }
 
-constexpr int set_of(int kind) { return kind == kF32 ? 4 : 8; }
+// Groups of a set. (SHIFT holds twice the words of a group: sets of eight, two CTAs an SM, took 4096 x 50257 154 us, sets of four 115.)
+constexpr int set_of(int kind, bool shift) { return kind == kF32 || shift ? 4 : 8; }
 
 // CL: CTAs of a row's cluster. Of a thread's places, CTA r has those congruent to r.
 //
-// A place's groups are taken in eight (fp32: four) rounds at a time: one maximum, and at most one rescaling of the sum, for a
-// thread's 64 (32) elements. (Group by group, a thread's instructions were more of the time than its loads.)
+// A place's groups are taken in a set of eight (fp32: four) rounds at a time: one maximum, and at most one rescaling of the sum, for
+// a thread's 64 (32) elements. (Group by group, a thread's instructions were more of the time than its loads.)
 template <int KIND, int VEC, bool SHIFT, int CL>
-__global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND, SHIFT>) distill_fwd_kernel(const __grid_constant__ DistillArgs P) {
-  constexpr int kSet = set_of(KIND);               // groups of a set
+__global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND>) distill_fwd_kernel(const __grid_constant__ DistillArgs P) {
+  constexpr int kSet = set_of(KIND, SHIFT);
   using H = Held<KIND, VEC, SHIFT>;
   extern __shared__ int smem[];
   __shared__ Part sent[kPlaces][kThreads];         // the threads' places; in a cluster's first CTA all of them
@@ -828,7 +829,7 @@ cudaError_t launch_fwd(DistillArgs& P, int cl, int nsm, cudaStream_t st) {
   const size_t smem = size_t(cl > 1 ? 1 : 2) * (even(P.groups) + 4 * P.top) * 4;
   // as many CTAs as are resident (the lists of a long vocabulary leave room for fewer)
   const int64_t room = std::max<int64_t>(1, 227 * 1024 / int64_t(smem + sizeof(Part) * kPlaces * kThreads + 2048));
-  const int64_t ctas = nsm * std::min<int64_t>(kMinCtas<KIND, SHIFT>, room);
+  const int64_t ctas = nsm * std::min<int64_t>(kMinCtas<KIND>, room);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(cl > 1 ? P.M * cl : std::min<int64_t>(P.M, ctas)));
   cfg.blockDim = dim3(kFwdThreads);
@@ -926,10 +927,10 @@ lora_status lora_distill_topk_fwd(const void* logits, int type, const void* ids,
   P.probs = probs;
   P.stats = stats;
   // Of the row's length alone: one place while a row is short, two, or four where that leaves no warp more half sets. Of many
-  // rows fewer places are faster, of few rows more (4096 x 32000 by 1, 2, 4, 8: 61.5, 61.1, 97.7 and 176 us; 4096 x 50257 135, 141, 160
-  // and 249, one row of it 15.6, 9.6, 9.8 and 8.4; 4096 x 131072 179, 179, 181 and 187, one row 16.5, 10.8, 8.2 and 8.1; 4096 x
+  // rows fewer places are faster, of few rows more (4096 x 32000 by 1, 2, 4, 8: 61.5, 61.1, 97.7 and 176 us; 4096 x 50256 96, 101, 110
+  // and 178, one row of 50257 15.6, 9.6, 9.8 and 8.4; 4096 x 131072 179, 179, 181 and 187, one row 16.5, 10.8, 8.2 and 8.1; 4096 x
   // 151936 219, 222, 253 and 333).
-  const int half = kWarps * set_of(type == LORA_F32 ? kF32 : kBf16) / 2;
+  const int half = kWarps * set_of(type == LORA_F32 ? kF32 : kBf16, V % 8 != 0) / 2;
   const auto halves = [&](int places) { return places * cdiv(P.groups, places * half); };
   P.places = P.groups <= 96 ? 1 : (P.groups >= 448 && halves(4) == halves(1) ? 4 : 2);
   // few rows: a row's places over the CTAs of a cluster
