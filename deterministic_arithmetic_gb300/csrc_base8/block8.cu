@@ -2,7 +2,7 @@
 //
 // One pass: a block's elements are read once into registers, their largest magnitude is found by shuffles (and,
 // for a weight's 128 x 128, through shared memory), and the codes are written. Bound by HBM: 3 bytes an element of
-// a bf16 tensor.
+// a bf16 tensor (17408 x 5120 in 128 x 128 40 us, 6.7 TB/s; back 41).
 #include "../csrc/common.cuh"
 #include "../csrc/kernels.h"
 #include "../csrc_mlp/elems.cuh"
