@@ -44,14 +44,30 @@ constexpr int kLinThreads = 384, kLinRegs = 168, kLinRegsFew = 40, kLinRegsMany 
 static_assert(128 * kLinRegsFew + 256 * kLinRegsMany <= kLinThreads * kLinRegs, "the shares fit the launch's registers");
 
 // The bounded waits of waits.cuh, without a call: a kernel that shares out its registers can hold none. And without
-// ordering at cluster scope: what the barriers of this kernel stand for is written by copies and tensor cores, never
-// by a peer's stores. (Acquiring at that scope throws the SM's L1 away, and a release waits for the thread's loads: of a
+// acquires and releases at cluster scope: what the barriers of this kernel stand for is written by copies and tensor cores,
+// never by a peer's stores. (Acquiring at that scope throws the SM's L1 away, and a release waits for the thread's loads: of a
 // pair's 4096 x 17408 -> 5120, 943 us with both, 411 with neither.)
 __device__ __forceinline__ bool lin_done(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0u;
+}
+// The same of a barrier that says who may use an accumulator. Across a pair the arrival may be the peer's, so the test is one at
+// cluster scope; relaxed, for nothing but TMEM hangs on it, and that the threads' tcgen05 fences order: in turn, the tensor
+// operation and its wait, fence before, arrival; test, fence after, tensor operation.
+template <int CG>
+__device__ __forceinline__ bool lin_done_acc(uint32_t bar, uint32_t parity) {
+  if constexpr (CG == 1) return lin_done(bar, parity);
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity)
@@ -85,18 +101,32 @@ struct LinAbort {
   }
 };
 // A wait of the whole warp, which stays together; the same answer in every lane. `quarter`: of the limit (the test hook).
+// CG 2: lin_done_acc's, of a pair.
+template <int CG = 1>
 __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site, bool teardown = false,
                                                 bool quarter = false) {
+  const auto test = [&]() {
+    if constexpr (CG == 1) return mbar_test(bar, parity);
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0u;
+  };
   // (the clock takes longer to read than most waits last: not before some tries)
   for (uint32_t it = 1; it <= 1024u; ++it) {
-    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, test())) return true;
   }
   const uint32_t us = ab.status[3];
   uint64_t limit = teardown ? kDrainLimitNs : (us ? uint64_t(us) * 1000ull : kWaitLimitNs);
   if (quarter) limit /= 4;
   const uint64_t t0 = global_ns();
   while (true) {
-    const bool done = mbar_test(bar, parity), out = global_ns() - t0 > limit;
+    const bool done = test(), out = global_ns() - t0 > limit;
     if (__all_sync(0xffffffffu, done)) return true;
     if (__any_sync(0xffffffffu, !teardown && ab.raised())) return false;
     if (__any_sync(0xffffffffu, out)) {
@@ -109,6 +139,10 @@ __device__ __forceinline__ bool lin_wait_longer(uint32_t bar, uint32_t parity, L
 }
 __device__ __forceinline__ bool lin_wait(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site) {
   return __builtin_expect(__all_sync(0xffffffffu, lin_done(bar, parity)), 1) || lin_wait_longer(bar, parity, ab, site);
+}
+template <int CG>
+__device__ __forceinline__ bool lin_wait_acc(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site) {
+  return __builtin_expect(__all_sync(0xffffffffu, lin_done_acc<CG>(bar, parity)), 1) || lin_wait_longer<CG>(bar, parity, ab, site);
 }
 __device__ __forceinline__ void lin_drain(uint32_t bar, uint32_t parity, LinAbort ab, uint32_t site) {
   if (!__all_sync(0xffffffffu, lin_done(bar, parity))) lin_wait_longer(bar, parity, ab, site, true);
@@ -375,7 +409,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
           if (!ok) break;
           const uint32_t off = uint32_t(idx) * stage_bytes, used = empty(idx);
           if (++idx == stages) idx = 0, phase ^= 1u;
-          if (!__all_sync(0xffffffffu, free)) ok = lin_wait(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4);
+          if (!__all_sync(0xffffffffu, free)) ok = lin_wait_acc<CG>(tempty(buf), tphase ^ 1u, ab, kSiteLinear + 4);
           if (!ok) break;
           tc_fence_after();
           if (one) {
@@ -394,7 +428,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
           }
           __syncwarp();
           if (++buf == kSlots) buf = 0, tphase ^= 1u;
-          free = lin_done(tempty(buf), tphase ^ 1u);
+          free = lin_done_acc<CG>(tempty(buf), tphase ^ 1u);
           landed = lin_done(full(idx), phase);
         }
       }
@@ -409,7 +443,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
       bool ok = true;
       for (int u = first; u < P.total; u += step)
         for (int i = 0; i < P.nk && ok; ++i) {
-          ok = lin_wait(tempty(buf), tphase, ab, kSiteLinear + 11);
+          ok = lin_wait_acc<CG>(tempty(buf), tphase, ab, kSiteLinear + 11);
+          tc_fence_after();                        // (passes the warps' order on)
+          tc_fence_before();
           lin_arrive_peer(peer_addr(tempty(buf), 0), ok && lane == 0);
           if (++buf == kSlots) buf = 0, tphase ^= 1u;
         }
@@ -527,7 +563,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_kernel(const __grid_con
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s[e]) : "r"(sg + k * kScaleBytes + block[e]) : "memory");
           const bool last = k % DEEP == DEEP - 1 || kb0 + k == P.nk - 1;       // of its slot
           if (k % DEEP == 0) {
-            ok = lin_wait(tfull(buf), tphase, ab, kSiteLinear + 7) && ok;
+            ok = lin_wait_acc<CG>(tfull(buf), tphase, ab, kSiteLinear + 7) && ok;
             tc_fence_after();
           }
           auto leave = [&]() {
