@@ -459,15 +459,16 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
   sum_p = warp_sum(sum_p);
   loss = warp_sum(loss);
   if (lane == 0) {
-    float keep = 1.f;
+    float keep = 1.f, log2_s = log2f(s);
     if (P.teacher_lse) {
+      if (sum_p > 1.f) log2_s -= log2f(sum_p);     // the gradient is sum_p q - p then
       const float left = sum_p >= 1.f ? 0.f : 1.f - sum_p, ratio = s_top / s_rest;   // log rho = -log(1 + ratio)
       if (left != 0.f) loss += left * (log1pf(-sum_p) + log1pf(ratio));                 // (NaN too)
       if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
     }
     P.loss[row] = any ? weight * loss : 0.f;
     *reinterpret_cast<float4*>(P.stats + row * 4) =
-        any ? make_float4(m, log2f(s), keep, weight) : make_float4(0.f, 0.f, 0.f, 0.f);
+        any ? make_float4(m, log2_s, keep, weight) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 

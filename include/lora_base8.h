@@ -64,8 +64,9 @@ lora_status lora_block8_linear_bwd(const void *dy, const float *dy_scales, const
  *   weight       [M] FP32, or NULL (all 1). A row of weight 0 is not read: its loss is 0, its gradient 0
  *   loss         [M] FP32 (out)
  *   probs        [M][top] FP32 (out): p_i; -1 for what is no entry, and in rows of weight 0
- *   stats        [M][4] FP32 (out): the largest logit m; log2(sum of exp((logit - m) / T)); 1 - r / rho (1 without
- *                teacher_lse, and where rho is 0); the weight. Zeros in rows of weight 0 or without entries
+ *   stats        [M][4] FP32 (out): the largest logit m; log2(sum of exp((logit - m) / T)), with teacher_lse less
+ *                log2(max(sum of p_i, 1)); 1 - r / rho (1 without teacher_lse, and where rho is 0); the weight. Zeros in
+ *                rows of weight 0 or without entries
  * 1 <= V < 2^22, 1 <= top <= 1024, T > 0, finite and no subnormal number. A row without entries has loss 0 and gradient 0.
  */
 lora_status lora_distill_topk_fwd(const void *logits, int type, const void *ids, int id_bytes, const void *teacher,
@@ -73,8 +74,9 @@ lora_status lora_distill_topk_fwd(const void *logits, int type, const void *ids,
                                   int64_t M, int64_t V, int64_t top, float *loss, float *probs, float *stats,
                                   void *stream);
 
-/* Backward pass: dlogits = dloss * weight / T * (q - p_i at entries, q * stats[2] elsewhere), from the
- * forward's probs and stats (the weight among them). Where dloss * weight is 0 the row's gradient is 0 and its
+/* Backward pass, the derivative of the loss: dlogits = dloss * weight / T * (P q - p_i at entries, P q * stats[2] elsewhere),
+ * P = 1 or, with teacher_lse, max(sum of p_i, 1) (a teacher's logits of few bits may sum to more than its
+ * whole vocabulary's), from the forward's probs and stats (P and the weight among them). Where dloss * weight is 0 the row's gradient is 0 and its
  * logits are not read.
  *   dloss    [M] FP32
  *   dlogits  [M][V] of the logits' type, which may be logits itself; or, with scales != NULL, its codes [M][ld]

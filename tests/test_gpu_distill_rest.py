@@ -1,0 +1,138 @@
+"""The loss with the teacher's log-sum-exp where its pieces are far apart, against its definition in 64 bits and that one's
+automatic differentiation."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_distill import BF, F32, INF, _built, bwd, f64, fwd, make, same  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+U32 = 2.0 ** -24
+
+
+def definition(c, dloss, no_rest=False):
+    """(loss, gradient of sum(dloss * loss), parts) in 64 bits, from the formula of include/lora_base8.h; every entry counts.
+    no_rest: r is 0."""
+    T = np.float64(np.float32(c["temperature"]))
+    z = c["logits"].double().requires_grad_()
+    ids = c["ids"].long()
+    log_p = c["teacher"].double() / T - c["teacher_lse"].double()[:, None]
+    p = log_p.exp()
+    log_q = torch.log_softmax(z / T, 1)
+    part = p * (log_p - log_q.gather(1, ids))
+    loss = part.sum(1)
+    r = (1 - p.sum(1)).clamp_min(0)
+    listed = torch.zeros_like(z, dtype=torch.bool).scatter_(1, ids, True)
+    if no_rest:
+        r = torch.zeros_like(r)
+    on = r > 0
+    log_rho = torch.full_like(r, -math.inf)
+    if on.any():
+        others = (z[on] / T).masked_fill(listed[on], -math.inf)
+        log_rho[on] = torch.logsumexp(others, 1) - torch.logsumexp(z[on] / T, 1)
+        loss = loss.index_add(0, on.nonzero()[:, 0], r[on] * (r[on].log() - log_rho[on]))
+    w = torch.ones_like(r) if c["weight"] is None else c["weight"].double()
+    loss = loss * w
+    dz, = torch.autograd.grad((dloss.double() * loss).sum(), z)
+    return loss.detach(), dz, dict(p=p, log_p=log_p, part=part.detach(), r=r, log_rho=log_rho.detach(), listed=listed,
+                                   log_q=log_q.detach(), w=w, T=T)
+
+
+def off_by(c, dloss, loss, dz, k):
+    """How far fp32 may be off: (loss, gradient before its last rounding). A probability is an exponential (2^-21) of an
+    argument right to an ulp of itself; log q adds to that the sums' roundings; r is as far off as the sum of p; a far
+    rest's log2(r / rho) is held, and taken from an exponent again, in fp32."""
+    z, T, v = c["logits"].double(), k["T"], c["logits"].shape[1]
+    far = ((z - z.amax(1, keepdim=True)) / T).abs().clamp_max(1e300)
+    q = k["log_q"].exp()
+    live = torch.where(q > 0, far, 0.0)
+    sums = (v / 16384 + 64) * U32
+    d_log = 2.0 ** -21 * (1 + (q * live).sum(1)) + sums
+    mass = k["p"].sum(1)
+    dr = 2.0 ** -21 * (k["p"] * (1 + k["log_p"].abs())).sum(1)
+    r = k["r"]
+    on = r > 0
+    lr = torch.where(on, (r.clamp_min(1e-300).log() - torch.where(on, k["log_rho"], 0.0)).abs(), 0.0)
+    tol = (mass + r) * d_log + 2.0 ** -21 * (k["part"].abs().sum(1) + mass) + dr * (1 + lr) * on + 2.0 ** -20 * r * lr
+    tol = tol * k["w"].abs() + 2 * U32 * loss.abs()
+    scale = (dloss.double() * k["w"] / T).abs()[:, None]
+    own = q * torch.maximum(mass, torch.ones_like(mass))[:, None]
+    L = torch.where(on, -torch.where(on, k["log_rho"], 0.0) / math.log(2), 0.0)[:, None]
+    rel = 2.0 ** -19 + sums + 2.0 ** -22 * (live + k["log_q"].abs().amin(1, keepdim=True))
+    rest = torch.where(on[:, None] & ~k["listed"], (own - dz / (dloss.double() * k["w"] / T)[:, None]).abs(), 0.0)   # r rho_j
+    t = own * rel + rest * (rel + 2.0 ** -22 * L + torch.where(on, dr / r.clamp_min(1e-300), 0.0)[:, None])
+    t.scatter_add_(1, c["ids"].long(), 2.0 ** -21 * (k["p"] * (1 + k["log_p"].abs()) + own.gather(1, c["ids"].long())))
+    return tol, scale * t
+
+
+def check(c, no_rest=False, seed=1):
+    """The loss and its gradient (as it is and in blocks) of c."""
+    from deterministic_arithmetic_gb300 import block8
+
+    m = len(c["logits"])
+    dl = torch.rand(m, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda") + 0.1
+    loss, probs, stats = fwd(c)
+    got = bwd(c, dl, probs, stats)
+    want, dz, k = definition(c, dl, no_rest)
+    tol, t = off_by(c, dl, want, dz, k)
+    off = (loss.double() - want).abs()
+    assert bool((off <= tol).all()), f"loss off by {float((off / tol).max()):.3g} of the tolerance"
+    half = 2.0 ** -8 if got.dtype == BF else U32
+    bound = t + half * (dz.abs() + t) + 2.0 ** -133
+    off = (got.double() - dz).abs()
+    assert bool((off <= bound).all()), f"gradient off by {float((off / bound).max()):.3g} of the tolerance"
+    full = bwd(dict(c, logits=c["logits"].float()), dl, probs, stats)
+    b, a = bwd(c, dl, probs, stats, block8=True), block8.block8(full)
+    assert same(a.codes, b.codes) and same(a.scales, b.scales)
+    few = {key: (x[1:3].clone() if isinstance(x, torch.Tensor) else x) for key, x in c.items()}
+    alone = fwd(few)
+    assert all(same(x, y[1:3]) for x, y in zip(alone, (loss, probs, stats)))
+    assert same(bwd(few, dl[1:3].clone(), *alone[1:]), got[1:3])
+    return loss, got, k
+
+
+def on_gpu(a, dtype=F32):
+    return torch.from_numpy(a).to("cuda").to(dtype)
+
+
+# ------------------------------------------ entries whose probabilities sum to more than 1
+def peaked(m, v, top, dtype, T, student=None):
+    """Rows with a few logits near 24, the teacher's kept in bf16 (half a step is 0.06 there), its log-sum-exp of the fp32 ones."""
+    rng = np.random.default_rng(m + v)
+    full = rng.standard_normal((m, v)) * 2
+    full[:, :3] = 24 + rng.standard_normal((m, 3))
+    full = on_gpu(full)
+    t, ids = torch.topk(full, top, dim=1)
+    z = full + on_gpu(rng.standard_normal((m, v))) if student is None else full
+    lse = torch.logsumexp(full.double() / T, 1).float()
+    return dict(logits=z.to(dtype), ids=ids, teacher=t.to(BF), teacher_lse=lse, weight=on_gpu(rng.random(m) + 0.5), temperature=T)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0.5, 1.0, 1.5])
+@pytest.mark.parametrize("v", [2000, 2001])
+def test_a_teacher_in_bf16_whose_entries_sum_to_more_than_1(v, T, dtype):
+    c = peaked(64, v, 20, dtype, T)
+    _, got, k = check(c)
+    over = k["p"].sum(1)
+    assert int((over > 1.005).sum()) >= 5 and int((over < 0.995).sum()) >= 5
+    if dtype == F32:                               # a softmax's gradient sums to 0: v roundings of values of up to 1
+        assert float(got.double().sum(1).abs().max()) < 1.6 / T * (v * U32 + 2.0 ** -16)
+
+
+def test_the_gradient_where_they_do_is_that_of_the_losses_differences():
+    c = peaked(64, 2000, 20, F32, 1.0)
+    c["weight"] = None
+    _, probs, stats = fwd(c)
+    over = probs.clamp_min(0).sum(1) > 1.005
+    dl = over.float()
+    dz = bwd(c, dl, probs, stats).double()
+    assert not dz[~over].any()
+    size = dz.norm(dim=1, keepdim=True).clamp_min(1e-30)
+    h = 2.0 ** -10
+    up, down = (definition(dict(c, logits=c["logits"].double() + s * h * dz / size), dl)[0] for s in (1, -1))
+    slope = (up - down)[over] / (2 * h)
+    assert float((slope / size[over, 0] - 1).abs().max()) < 1e-4      # h^2 times the third derivative, and fp32's roundings
