@@ -391,6 +391,20 @@ __device__ __forceinline__ void make_lists(const DistillArgs& P, const Row& r, i
   __syncwarp();
 }
 
+// A rest below 2^-64 of the row, whose sum would lose itself beside the entries': its part of the loss, left (log left - log rho),
+// and what the backward pass takes, 1 - left / rho. Both from log rho, taken from the rest's own maximum. From left / rho = 2^64 on
+// that is held by its logarithm, as -2^64 log2: left rho_j of an element is then one exponential of log2(left / rho) and the
+// element's exponent, where q_j alone may be too small for a float. Of a logarithm above 2^12 a float's rounding would be more
+// than 1e-4 of the gradient: rho counts as 0 there. (Halves: the difference of two of the type's values may pass its largest.)
+constexpr float kFarRest = 0x1p-64f, kFarOver = 0x1p64f, kFarKeep = -0x1p70f, kFarMost = 4096.f;
+__device__ __noinline__ float2 far_rest(float left, float log_left, Part rest, float m, float s, float inv_t, float c) {
+  const float fall = 0.5f * rest.m - 0.5f * m;
+  if (rest.s == 0.f) return make_float2(left != 0.f ? kInf : 0.f, 1.f);
+  const float over = log2f(left) - (2.f * (fall * c) + (log2f(rest.s) - log2f(s)));     // log2(left / rho); NaN stays
+  return make_float2(left != 0.f ? left * (log_left - (2.f * (fall * inv_t) + (logf(rest.s) - logf(s)))) : 0.f,
+                     over > kFarMost ? 1.f : (over < 64.f ? 1.f - exp2f(over) : -kFarOver * over));
+}
+
 // The row's end, from the eight warps' parts: of one warp.
 __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, const Part* warps, int64_t row, float weight, int lane) {
   const float c = kLog2e / P.temperature;
@@ -462,9 +476,16 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
     float keep = 1.f, log2_s = log2f(s);
     if (P.teacher_lse) {
       if (sum_p > 1.f) log2_s -= log2f(sum_p);     // the gradient is sum_p q - p then
-      const float left = sum_p >= 1.f ? 0.f : 1.f - sum_p, ratio = s_top / s_rest;   // log rho = -log(1 + ratio)
-      if (left != 0.f) loss += left * (log1pf(-sum_p) + log1pf(ratio));                 // (NaN too)
-      if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
+      const float left = sum_p >= 1.f ? 0.f : 1.f - sum_p;
+      if (s_rest < s * kFarRest) {
+        const float2 far = far_rest(left, log1pf(-sum_p), rest, m, s, inv_t, c);
+        loss += far.x;
+        keep = far.y;
+      } else {
+        const float ratio = s_top / s_rest;                                             // log rho = -log(1 + ratio)
+        if (left != 0.f) loss += left * (log1pf(-sum_p) + log1pf(ratio));               // (NaN too)
+        if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
+      }
     }
     P.loss[row] = any ? weight * loss : 0.f;
     *reinterpret_cast<float4*>(P.stats + row * 4) =
@@ -751,90 +772,103 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 3 : (OUT8 ? 4 : 5)) d
   __syncthreads();
   // q = 2^((x - m) c - log2 sum): the difference first, which is exact where q is large
   const float c = kLog2e / P.temperature, m = st.x, log_s = -st.y, gr = g * st.z;
-  const int cblocks = (P.V + kBlock - 1) / kBlock;
-  for (int gb = g0 + warp; gb < g1; gb += kWarps * kLoads) {
-    H held[kLoads];
+  // FAR: a row whose rest has the gradient -r rho_j, by way of log2(r / rho) (far_rest). A loop of its own: with a branch in this
+  // one, 4096 x 50257 bf16 took 138 us instead of 127.
+  const auto groups = [&](auto far) {
+    constexpr bool FAR = far.value;
+    const int cblocks = (P.V + kBlock - 1) / kBlock;
+    for (int gb = g0 + warp; gb < g1; gb += kWarps * kLoads) {
+      H held[kLoads];
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int gi = gb + kWarps * k;
-      if (gi >= g1 || zero) continue;
-      if constexpr (LED) held[k].load_led(P.z, base, gi * kGroupElems - lead, P.V, edge, lane);
-      else held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, edge, lane);
-    }
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const int gi = gb + kWarps * k, n = P.V - gi * kGroupElems;
-      if (gi >= g1) break;
-      float v[8];
-      if (zero) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-      } else {
-        float x[8];
-        held[k].settle(first);
-        held[k].get(x);                            // (what lies past the row's end is not stored)
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float2 y = fma2(add2(make_float2(x[e], x[e + 1]), make_float2(-m, -m)), make_float2(c, c), make_float2(log_s, log_s));
-          x[e] = ex2(y.x);
-          x[e + 1] = ex2(y.y);
-          const float2 t = mul2(make_float2(x[e], x[e + 1]), make_float2(gr, gr));
-          v[e] = t.x;
-          v[e + 1] = t.y;
-        }
-        for (int i = L.head[gi - g0]; i >= 0;) {
-          const int2 link = L.link[i];
-          const uint32_t mine = H::elem_of(uint32_t(link.y + lead - gi * kGroupElems), uint32_t(lane));
-          const float pg = pl[i] * g;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = mine == uint32_t(e) ? fmaf(x[e], g, -pg) : v[e];
-          i = link.x;
-        }
+      for (int k = 0; k < kLoads; ++k) {
+        const int gi = gb + kWarps * k;
+        if (gi >= g1 || zero) continue;
+        if constexpr (LED) held[k].load_led(P.z, base, gi * kGroupElems - lead, P.V, edge, lane);
+        else held[k].load(H::place(P.z, base + int64_t(gi) * kGroupElems, first, lane), first, P.V - gi * kGroupElems, edge, lane);
       }
-      if constexpr (LED) {
-        H::store_led(P.dz, base, gi * kGroupElems - lead, P.V, lane, v);
-      } else if constexpr (!OUT8) {
-        H::store(P.dz, base + int64_t(gi) * kGroupElems, n, lane, v);
-      } else {
-        // the two blocks of the group: of 8 consecutive elements a lane, 16 lanes each; else the first and last four
-        // of every lane. (What lies past column V is no value: 0, and written up to the codes' row length.)
-        if (n < kGroupElems) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (H::at(e, lane) >= n) v[e] = 0.f;
-        }
-        uint32_t a[2] = {0u, 0u};
+      for (int k = 0; k < kLoads; ++k) {
+        const int gi = gb + kWarps * k, n = P.V - gi * kGroupElems;
+        if (gi >= g1) break;
+        float v[8];
+        if (zero) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[VEC == 8 ? 0 : e / 4] = max(a[VEC == 8 ? 0 : e / 4], abs_bits(v[e]));
-        if constexpr (VEC == 8) {
-#pragma unroll
-          for (int o = 8; o; o >>= 1) a[0] = max(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+          for (int e = 0; e < 8; ++e) v[e] = 0.f;
         } else {
-          a[0] = __reduce_max_sync(0xffffffffu, a[0]);
-          a[1] = __reduce_max_sync(0xffffffffu, a[1]);
-        }
-        uint8_t* out = static_cast<uint8_t*>(P.dz) + row * ld + int64_t(gi) * kGroupElems;
-        const int nld = int(ld) - gi * kGroupElems;
-        float* sc = P.scales + row * cblocks + 2 * gi;
-        if constexpr (VEC == 8) {
-          const BlockScale s = block_scale(a[0]);
-          if (8 * lane < nld) *reinterpret_cast<uint2*>(out + 8 * lane) = codes8(v, s.inv);
-          if ((lane & 15) == 0 && 8 * lane < n) sc[lane >> 4] = s.scale;
-        } else {
-          const BlockScale s[2] = {block_scale(a[0]), block_scale(a[1])};
+          float x[8];
+          held[k].settle(first);
+          held[k].get(x);                            // (what lies past the row's end is not stored)
 #pragma unroll
-          for (int h = 0; h < 8; h += VEC) {
-            const int at = H::at(h, lane);
-            const float inv = s[h / 4].inv;
-            if (at >= nld) continue;
-            if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(out + at) = codes4(v[h], v[h + 1], v[h + 2], v[h + 3], inv);
-            else out[at] = uint8_t(codes2(v[h], 0.f, inv));
+          for (int e = 0; e < 8; e += 2) {
+            const float2 y = fma2(add2(make_float2(x[e], x[e + 1]), make_float2(-m, -m)), make_float2(c, c), make_float2(log_s, log_s));
+            x[e] = ex2(y.x);
+            x[e + 1] = ex2(y.y);
+            const float2 t = mul2(make_float2(x[e], x[e + 1]), make_float2(gr, gr));
+            v[e] = t.x;
+            v[e + 1] = t.y;
           }
-          if (lane < 2 && 128 * lane < n) sc[lane] = lane == 0 ? s[0].scale : s[1].scale;
+          if constexpr (FAR) {
+            const float lift = st.z * (-1.f / kFarOver);
+            held[k].get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = -g * ex2(fmaf(v[e] - m, c, log_s + lift));
+          }
+          for (int i = L.head[gi - g0]; i >= 0;) {
+            const int2 link = L.link[i];
+            const uint32_t mine = H::elem_of(uint32_t(link.y + lead - gi * kGroupElems), uint32_t(lane));
+            const float pg = pl[i] * g;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = mine == uint32_t(e) ? fmaf(x[e], g, -pg) : v[e];
+            i = link.x;
+          }
+        }
+        if constexpr (LED) {
+          H::store_led(P.dz, base, gi * kGroupElems - lead, P.V, lane, v);
+        } else if constexpr (!OUT8) {
+          H::store(P.dz, base + int64_t(gi) * kGroupElems, n, lane, v);
+        } else {
+          // the two blocks of the group: of 8 consecutive elements a lane, 16 lanes each; else the first and last four
+          // of every lane. (What lies past column V is no value: 0, and written up to the codes' row length.)
+          if (n < kGroupElems) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (H::at(e, lane) >= n) v[e] = 0.f;
+          }
+          uint32_t a[2] = {0u, 0u};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a[VEC == 8 ? 0 : e / 4] = max(a[VEC == 8 ? 0 : e / 4], abs_bits(v[e]));
+          if constexpr (VEC == 8) {
+#pragma unroll
+            for (int o = 8; o; o >>= 1) a[0] = max(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+          } else {
+            a[0] = __reduce_max_sync(0xffffffffu, a[0]);
+            a[1] = __reduce_max_sync(0xffffffffu, a[1]);
+          }
+          uint8_t* out = static_cast<uint8_t*>(P.dz) + row * ld + int64_t(gi) * kGroupElems;
+          const int nld = int(ld) - gi * kGroupElems;
+          float* sc = P.scales + row * cblocks + 2 * gi;
+          if constexpr (VEC == 8) {
+            const BlockScale s = block_scale(a[0]);
+            if (8 * lane < nld) *reinterpret_cast<uint2*>(out + 8 * lane) = codes8(v, s.inv);
+            if ((lane & 15) == 0 && 8 * lane < n) sc[lane >> 4] = s.scale;
+          } else {
+            const BlockScale s[2] = {block_scale(a[0]), block_scale(a[1])};
+#pragma unroll
+            for (int h = 0; h < 8; h += VEC) {
+              const int at = H::at(h, lane);
+              const float inv = s[h / 4].inv;
+              if (at >= nld) continue;
+              if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(out + at) = codes4(v[h], v[h + 1], v[h + 2], v[h + 3], inv);
+              else out[at] = uint8_t(codes2(v[h], 0.f, inv));
+            }
+            if (lane < 2 && 128 * lane < n) sc[lane] = lane == 0 ? s[0].scale : s[1].scale;
+          }
         }
       }
     }
-  }
+  };
+  if (st.z <= kFarKeep) groups(std::true_type{});
+  else groups(std::false_type{});
 }
 
 bool args_ok(int type, int id_bytes, float temperature, int64_t M, int64_t V, int64_t top) {

@@ -65,8 +65,8 @@ lora_status lora_block8_linear_bwd(const void *dy, const float *dy_scales, const
  *   loss         [M] FP32 (out)
  *   probs        [M][top] FP32 (out): p_i; -1 for what is no entry, and in rows of weight 0
  *   stats        [M][4] FP32 (out): the largest logit m; log2(sum of exp((logit - m) / T)), with teacher_lse less
- *                log2(max(sum of p_i, 1)); 1 - r / rho (1 without teacher_lse, and where rho is 0); the weight. Zeros in
- *                rows of weight 0 or without entries
+ *                log2(max(sum of p_i, 1)); 1 - r / rho (1 without teacher_lse, and where rho is 0 or below 2^-4096 r), or,
+ *                from r / rho = 2^64 on, -2^64 log2(r / rho); the weight. Zeros in rows of weight 0 or without entries
  * 1 <= V < 2^22, 1 <= top <= 1024, T > 0, finite and no subnormal number. A row without entries has loss 0 and gradient 0.
  */
 lora_status lora_distill_topk_fwd(const void *logits, int type, const void *ids, int id_bytes, const void *teacher,
@@ -74,10 +74,10 @@ lora_status lora_distill_topk_fwd(const void *logits, int type, const void *ids,
                                   int64_t M, int64_t V, int64_t top, float *loss, float *probs, float *stats,
                                   void *stream);
 
-/* Backward pass, the derivative of the loss: dlogits = dloss * weight / T * (P q - p_i at entries, P q * stats[2] elsewhere),
- * P = 1 or, with teacher_lse, max(sum of p_i, 1) (a teacher's logits of few bits may sum to more than its
- * whole vocabulary's), from the forward's probs and stats (P and the weight among them). Where dloss * weight is 0 the row's gradient is 0 and its
- * logits are not read.
+/* Backward pass, the derivative of the loss: dlogits = dloss * weight / T * (P q - p_i at entries, (P - r / rho) q elsewhere),
+ * P = 1 or, with teacher_lse, max(sum of p_i, 1) (a teacher's logits of few bits may sum to more than its whole
+ * vocabulary's), from the forward's probs and stats (P and the weight among them). Where dloss * weight is 0 the row's
+ * gradient is 0 and its logits are not read.
  *   dloss    [M] FP32
  *   dlogits  [M][V] of the logits' type, which may be logits itself; or, with scales != NULL, its codes [M][ld]
  *            as lora_block8 would give them for the FP32 values, and scales [M][ceil(V / 128)]

@@ -136,3 +136,54 @@ def test_the_gradient_where_they_do_is_that_of_the_losses_differences():
     up, down = (definition(dict(c, logits=c["logits"].double() + s * h * dz / size), dl)[0] for s in (1, -1))
     slope = (up - down)[over] / (2 * h)
     assert float((slope / size[over, 0] - 1).abs().max()) < 1e-4      # h^2 times the third derivative, and fp32's roundings
+
+
+# ------------------------------------------------------------- a rest far below the entries
+def gapped(gap, T, dtype, r=0.05, m=8, v=700, top=12):
+    """The student's unlisted logits lie gap * T below the listed ones; the teacher's unlisted mass is r."""
+    rng = np.random.default_rng(int(gap * 8) + m)
+    z = T * (rng.standard_normal((m, v)) - gap)
+    ids = np.argsort(rng.random((m, v)), 1)[:, :top]
+    np.put_along_axis(z, ids, T * rng.standard_normal((m, top)), 1)
+    t = on_gpu(T * rng.standard_normal((m, top)))
+    lse = (torch.logsumexp(t.double() / T, 1) - math.log1p(-r)).float()
+    return dict(logits=on_gpu(z, dtype), ids=on_gpu(ids, torch.int64), teacher=t, teacher_lse=lse,
+                weight=on_gpu(rng.random(m) + 0.5), temperature=T)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0.1, 0.25, 1.0, 4.0])
+@pytest.mark.parametrize("gap", [20, 42, 46, 60, 85, 90, 120, 700, 2500])
+def test_a_rest_far_below_the_entries(gap, T, dtype):
+    for r in (0.3, 0.01):
+        loss, got, k = check(gapped(gap, T, dtype, r))
+        assert bool(loss.isfinite().all())
+        # the rest's gradient is -r of the row's, however small rho
+        at = torch.where(k["listed"], 0.0, got.double()).sum(1)
+        assert bool((at < 0).all())
+
+
+@pytest.mark.parametrize("v", [701, 40000])
+def test_a_far_rest_of_rows_of_other_lengths(v):
+    for dtype in (BF, F32):
+        check(gapped(100, 0.5, dtype, v=v, top=30))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("gap", [5000, 1e6, None])
+def test_a_rest_further_down_than_the_gradient_knows(gap, dtype):
+    """Below 2^-4096 the rest has no gradient; the loss is still the formula's. None: the type's lowest value."""
+    c = gapped(gap or 10, 1.0, dtype)
+    if gap is None:
+        keep = torch.zeros_like(c["logits"], dtype=torch.bool).scatter_(1, c["ids"], True)
+        c["logits"].masked_fill_(~keep, torch.finfo(dtype).min)
+    dl = torch.ones(8, device="cuda")
+    loss, probs, stats = fwd(c)
+    got = bwd(c, dl, probs, stats)
+    want, dz, k = definition(c, dl)
+    tol, t = off_by(c, dl, want, dz, k)
+    assert bool(((loss.double() - want).abs() <= tol).all()) and bool(loss.isfinite().all())
+    assert not got[~k["listed"]].any()
+    half = 2.0 ** -8 if dtype == BF else U32
+    off = (got.double() - dz).abs()
+    assert bool((off <= t + half * (dz.abs() + t))[k["listed"]].all())
