@@ -397,11 +397,16 @@ __device__ __forceinline__ void make_lists(const DistillArgs& P, const Row& r, i
 // element's exponent, where q_j alone may be too small for a float. Of a logarithm above 2^12 a float's rounding would be more
 // than 1e-4 of the gradient: rho counts as 0 there. (Halves: the difference of two of the type's values may pass its largest.)
 constexpr float kFarRest = 0x1p-64f, kFarOver = 0x1p64f, kFarKeep = -0x1p70f, kFarMost = 4096.f;
-__device__ __noinline__ float2 far_rest(float left, float log_left, Part rest, float m, float s, float inv_t, float c) {
+// A teacher that lists all its mass leaves 0 only up to roundings, in half ulps of 1: 36 of a sum of 1024 p (31 a lane, then five), 2 of
+// the exponentials, 7 (log 1024, the largest sum of p |log p|) of their arguments, a few of the caller's own sum; and |lse| for each
+// rounding on the way to lse. So much is no mass: here, where its logarithm would be all of the loss (1e-7 of a mask's lowest
+// value), it counts as 0. (1/2 at most: lse may be infinite.)
+__device__ __noinline__ float2 far_rest(float left, float log_left, float lse, Part rest, float m, float s, float inv_t, float c) {
+  if (left <= fminf(0.5f, fmaf(8.f, fabsf(lse), 64.f) * 0x1p-24f)) return make_float2(0.f, 1.f);
   const float fall = 0.5f * rest.m - 0.5f * m;
-  if (rest.s == 0.f) return make_float2(left != 0.f ? kInf : 0.f, 1.f);
+  if (rest.s == 0.f) return make_float2(left * kInf, 1.f);                              // (NaN stays)
   const float over = log2f(left) - (2.f * (fall * c) + (log2f(rest.s) - log2f(s)));     // log2(left / rho); NaN stays
-  return make_float2(left != 0.f ? left * (log_left - (2.f * (fall * inv_t) + (logf(rest.s) - logf(s)))) : 0.f,
+  return make_float2(left * (log_left - (2.f * (fall * inv_t) + (logf(rest.s) - logf(s)))),
                      over > kFarMost ? 1.f : (over < 64.f ? 1.f - exp2f(over) : -kFarOver * over));
 }
 
@@ -478,7 +483,7 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
       if (sum_p > 1.f) log2_s -= log2f(sum_p);     // the gradient is sum_p q - p then
       const float left = sum_p >= 1.f ? 0.f : 1.f - sum_p;
       if (s_rest < s * kFarRest) {
-        const float2 far = far_rest(left, log1pf(-sum_p), rest, m, s, inv_t, c);
+        const float2 far = far_rest(left, log1pf(-sum_p), lse, rest, m, s, inv_t, c);
         loss += far.x;
         keep = far.y;
       } else {

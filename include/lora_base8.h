@@ -57,7 +57,9 @@ lora_status lora_block8_linear_bwd(const void *dy, const float *dy_scales, const
  * row's entries i: those with ids[i] in [0, V), teacher[i] not -infinity, and no earlier entry of the same id.
  *   p_i  = exp(teacher[i] / T - L)     L = teacher_lse of the row, or log(sum of exp(teacher[i] / T)) when it is NULL
  *   loss = weight * (sum of p_i (log p_i - log q[ids[i]])  [+ r (log r - log rho), with teacher_lse])
- *          r = max(1 - sum of p_i, 0), rho = sum of q over what is no entry; terms of p_i = 0 or r = 0 are 0
+ *          r = max(1 - sum of p_i, 0), rho = sum of q over what is no entry; terms of p_i = 0 or r = 0 are 0.
+ *          Where rho < 2^-64, an r of (64 + 8 |teacher_lse|) 2^-24 or less is FP32's rounding of 0 (a teacher that lists all
+ *          its mass, a mask that leaves the student nothing else) and counts as 0; a larger one beside rho = 0 is infinite
  *   logits       [M][V] bf16 or fp32 (type)      ids [M][top] int32 or int64 (id_bytes 4 or 8)
  *   teacher      [M][top] bf16 or fp32 (teacher_type)
  *   teacher_lse  [M] FP32, log(sum of exp(t / T)) over the teacher's whole vocabulary, or NULL

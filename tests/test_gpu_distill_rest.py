@@ -187,3 +187,51 @@ def test_a_rest_further_down_than_the_gradient_knows(gap, dtype):
     half = 2.0 ** -8 if dtype == BF else U32
     off = (got.double() - dz).abs()
     assert bool((off <= t + half * (dz.abs() + t))[k["listed"]].all())
+
+
+# -------------------------------------------------------- nothing left to the student's rest
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0.3, 1.0, 3.0])
+@pytest.mark.parametrize("mask", ["all listed", "-inf", "lowest"])
+@pytest.mark.parametrize("at", [0.0, 30.0, -200.0])
+def test_an_r_that_is_rounding_counts_as_0_where_rho_is_nothing(at, mask, T, dtype):
+    """The teacher's listed logits are all it has, so r is 0, and what fp32 leaves of 1 - sum p is not: no such row's loss
+    may be infinite, or a mask's lowest value times it."""
+    m, top, v = 600, 40, 40 if mask == "all listed" else 300
+    rng = np.random.default_rng(int(at) + 300)
+    ids = on_gpu(np.argsort(rng.random((m, v)), 1)[:, :top], torch.int64)
+    t = on_gpu(at + 2 * rng.standard_normal((m, top)))
+    z = torch.full((m, v), -INF if mask == "-inf" else torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    z.scatter_(1, ids, on_gpu(2 * rng.standard_normal((m, top)), dtype))
+    c = dict(logits=z, ids=ids, teacher=t, teacher_lse=torch.logsumexp(t / T, 1), weight=on_gpu(rng.random(m) + 0.5), temperature=T)
+    dl = torch.rand(m, device="cuda") + 0.1
+    loss, probs, stats = fwd(c)
+    got = bwd(c, dl, probs, stats).double()
+    sums = probs.double().sum(1)
+    assert bool((sums < 1).any()) and bool((sums > 1).any())
+    want, _, k = definition(dict(c, logits=z.clamp_min(torch.finfo(dtype).min)), dl, no_rest=True)
+    off = (loss.double() - want).abs()
+    far = (z.double().clamp_min(-1e300) - z.double().amax(1, keepdim=True)).abs() / T
+    q = k["log_q"].exp()
+    tol = 2.0 ** -21 * (1 + torch.where(q > 0, q * far, 0.0).sum(1)) + 65 * U32
+    tol = k["w"] * (k["p"].sum(1) * tol + 2.0 ** -21 * (k["part"].abs().sum(1) + k["p"].sum(1) * (1 + k["log_p"].abs().amax(1))))
+    # (log p - log q as a difference of logits and one of the row's, each of at most 64 there)
+    tol = tol + 4 * 64 * U32 * k["w"] * k["p"].sum(1) + 2 * U32 * want.abs()
+    assert bool((off <= tol).all()), float((off / tol).max())
+    p = torch.zeros_like(q).scatter_(1, ids, k["p"])
+    dz = (dl.double() * k["w"] / T)[:, None] * (q * k["p"].sum(1, keepdim=True).clamp_min(1) - p)
+    arg = 1 + k["log_p"].abs().amax(1, keepdim=True) + torch.where(q > 0, far, 0.0)
+    t_off = (dl.double() * k["w"] / T)[:, None] * (2.0 ** -19 * (q + p) * arg + 70 * U32 * q)
+    assert bool(((got - dz).abs() <= t_off + (2.0 ** -8 if dtype == BF else U32) * dz.abs()).all())
+
+
+def test_a_mass_that_the_student_cannot_have_is_no_rounding():
+    """r = 0.01, rho = 0: the definition's infinity; the gradient is that of the entries."""
+    c = gapped(10, 1.0, F32, r=0.01)
+    keep = torch.zeros_like(c["logits"], dtype=torch.bool).scatter_(1, c["ids"], True)
+    c["logits"].masked_fill_(~keep, -INF)
+    loss, probs, stats = fwd(c)
+    dz = bwd(c, torch.ones(8, device="cuda"), probs, stats)
+    assert bool((loss == INF).all()) and bool(dz.isfinite().all()) and not dz[~keep].any() and bool(dz[keep].any())
+    c["teacher_lse"][:] = INF                      # the teacher lists nothing of its mass
+    assert bool((fwd(c)[0] == INF).all())
