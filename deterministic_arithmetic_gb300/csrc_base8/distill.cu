@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 3 : (OUT8 ? 4 : 5)) d
   const bool edge = at_edge(P, row);
   const float4 st = __ldg(reinterpret_cast<const float4*>(P.stats + row * 4));
   const float g = __ldg(P.dloss + row) * st.w / P.temperature;
-  const bool zero = g == 0.f;
+  const bool zero = g == 0.f || st.w == 0.f;       // (of weight 0 whatever dloss is)
   for (int i = tid; i < g1 - g0; i += kThreads) L.head[i] = -1;
   __syncthreads();
   for (int i = tid; i < P.top && !zero; i += kThreads) {

@@ -78,8 +78,8 @@ lora_status lora_distill_topk_fwd(const void *logits, int type, const void *ids,
 
 /* Backward pass, the derivative of the loss: dlogits = dloss * weight / T * (P q - p_i at entries, (P - r / rho) q elsewhere),
  * P = 1 or, with teacher_lse, max(sum of p_i, 1) (a teacher's logits of few bits may sum to more than its whole
- * vocabulary's), from the forward's probs and stats (P and the weight among them). Where dloss * weight is 0 the row's
- * gradient is 0 and its logits are not read.
+ * vocabulary's), from the forward's probs and stats (P and the weight among them). Where dloss * weight is 0,
+ * and in rows of weight 0 or without entries whatever dloss is, the gradient is 0 and the logits are not read.
  *   dloss    [M] FP32
  *   dlogits  [M][V] of the logits' type, which may be logits itself; or, with scales != NULL, its codes [M][ld]
  *            as lora_block8 would give them for the FP32 values, and scales [M][ceil(V / 128)]

@@ -235,3 +235,26 @@ def test_a_mass_that_the_student_cannot_have_is_no_rounding():
     assert bool((loss == INF).all()) and bool(dz.isfinite().all()) and not dz[~keep].any() and bool(dz[keep].any())
     c["teacher_lse"][:] = INF                      # the teacher lists nothing of its mass
     assert bool((fwd(c)[0] == INF).all())
+
+
+# ------------------------------------------------------------- rows without a gradient
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("v", [1000, 1003])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_rows_of_weight_0_have_no_gradient_whatever_dloss_is(bad, v, dtype):
+    """A mean over no rows, say, has a dloss that is not finite; a row of weight 0 is not read, one without entries has none."""
+    from deterministic_arithmetic_gb300 import block8
+
+    c = make(10, v, 8, dtype, tail=True)
+    c["weight"][4] = 0
+    c["logits"][4] = float("nan")
+    c["ids"][6] = -1
+    loss, probs, stats = fwd(c)
+    dl = torch.ones(10, device="cuda")
+    ok = bwd(c, dl, probs, stats)
+    dl[4] = dl[6] = bad
+    for block in (False, True):
+        dz = bwd(c, dl, probs, stats, block8=block)
+        dz = block8.unblock8(dz) if block else dz
+        assert not dz[4].any() and not dz[6].any() and bool(dz.isfinite().all())
+        assert block or same(dz, ok)
