@@ -2,6 +2,7 @@
 #include "linear.cuh"
 #include "linear_plan.h"
 
+#include <climits>
 #include <mutex>
 
 #include "block8.cuh"
@@ -14,7 +15,11 @@ bool shape_ok(int64_t M, int64_t K, int64_t N) {
   return M >= 0 && M < most && K > 0 && K < most && N > 0 && N < most;
 }
 
-int g_pairs[64];                                   // pairs of CTAs that a device holds at once
+struct LinFit {
+  int pairs;                                       // of CTAs that a device holds at once
+  bool wide;                                       // the kernels of 256 columns have the registers that they share out
+};
+LinFit g_fit[64];
 
 template <int MODE, int CG, int W, int DEEP, bool JOINS = false>
 lora_status launch_as(LinArgs& P, const LinPlan& plan, const void* a, const void* w, int64_t red, int64_t w_rows,
@@ -80,8 +85,8 @@ lora_status linear(const void* a, const float* sa, const void* w, const float* s
   P.out = out;
   P.out_f32 = out_type == LORA_F32;
   P.vec = cols % 4 == 0;
-  const int pairs = g_pairs[dev];
-  const LinPlan plan = lin_plan(MODE == kLinBwd, P.m, P.n, nsm, pairs);
+  const int pairs = g_fit[dev].pairs;
+  const LinPlan plan = lin_plan(MODE == kLinBwd, P.m, P.n, nsm, pairs, g_fit[dev].wide);
   P.boxes = plan.w == 256 && cols % (P.out_f32 ? 4 : 8) == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto go = [&](auto cg, auto width, auto deep) {
@@ -98,16 +103,17 @@ lora_status linear(const void* a, const float* sa, const void* w, const float* s
 }
 
 template <int MODE>
-cudaError_t prepare(int* pairs) {
+cudaError_t prepare(LinFit* fit) {
   cudaError_t e = cudaSuccess;
   auto set = [&](auto kernel) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kLinSmem));
   };
-  // the 256-column kernels share out the registers they are launched with: fewer would leave some waiting for theirs
+  // The 256-column kernels share out the registers that they are launched with: compiled to fewer, some would wait for theirs for
+  // ever. Narrower ones then take their place; nothing else in the library asks.
   auto set_shared = [&](auto kernel) {
     cudaFuncAttributes a;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
-    if (e == cudaSuccess && a.numRegs < kLinRegs) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess && a.numRegs < kLinRegs) fit->wide = false;
     set(kernel);
   };
   set_shared(linear_kernel<MODE, 2, 256, 1, false>);
@@ -127,20 +133,22 @@ cudaError_t prepare(int* pairs) {
   attr[0].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(pairs, linear_kernel<MODE, 2, 256, 1, true>, &cfg) != cudaSuccess) {
+  int pairs = 0;
+  if (cudaOccupancyMaxActiveClusters(&pairs, linear_kernel<MODE, 2, 256, 1, true>, &cfg) != cudaSuccess) {
     cudaGetLastError();                            // (an answer, not an error of a later call)
-    *pairs = 0;
+    pairs = 0;
   }
+  fit->pairs = std::min(fit->pairs, pairs);
   return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t prepare_linear(int dev) {
-  int f = 0, b = 0;
+  LinFit fit{INT_MAX, true};
   cudaError_t e;
-  if ((e = prepare<kLinFwd>(&f)) != cudaSuccess || (e = prepare<kLinBwd>(&b)) != cudaSuccess) return e;
-  g_pairs[dev] = std::min(f, b);
+  if ((e = prepare<kLinFwd>(&fit)) != cudaSuccess || (e = prepare<kLinBwd>(&fit)) != cudaSuccess) return e;
+  g_fit[dev] = fit;
   return cudaSuccess;
 }
 
