@@ -3,7 +3,6 @@
 #include "linear_plan.h"
 
 #include <climits>
-#include <mutex>
 
 #include "block8.cuh"
 
