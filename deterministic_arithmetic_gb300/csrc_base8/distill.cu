@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND>) distill_fwd_kerne
 
 // ---------------------------------------------------------------- backward
 // A CTA takes P.seg groups of a row; each element is written by the thread that read it. OUT8: in 8-bit blocks. Bound by HBM (in
-// blocks, by the instructions of a group too). fp32, two CTAs an SM and three: 2048 x 131072 in blocks 341 and 229 us.
+// blocks, by the instructions of a group too). fp32, two CTAs an SM and three: 2048 x 131072 in blocks 341 and 221 us.
 template <int KIND, int VEC, bool SHIFT, bool OUT8>
 __global__ void __launch_bounds__(kThreads, KIND == kF32 ? 3 : (OUT8 ? 4 : 5)) distill_bwd_kernel(const __grid_constant__ DistillArgs P) {
   constexpr int kLoads = 4;                        // groups of a warp in flight
@@ -1028,7 +1028,7 @@ lora_status lora_distill_topk_bwd(const float* dloss, const void* logits, int ty
   int nsm = 0;
   if ((s = device_ready(&nsm)) != LORA_OK) return s;
   // A CTA's start (its row's statistics, the lists) is the dearer the fewer groups it has: as many as leave every SM some rounds of
-  // CTAs (64 and this: 4096 x 131072 bf16 336 and 314 us, in blocks 400 and 338; 64 x 50257 fp32 7.1 and 5.1).
+  // CTAs (64 and this: 4096 x 131072 bf16 336 and 303 us, in blocks 400 and 319; 64 x 50257 fp32 7.1 and 5.1).
   P.seg = 256;
   while (P.seg > 64 && M * cdiv(P.groups, P.seg) < 12 * nsm) P.seg /= 2;
   if (M * cdiv(P.groups, P.seg) < 2 * nsm) P.seg = 32;

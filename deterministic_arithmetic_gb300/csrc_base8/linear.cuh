@@ -9,7 +9,7 @@
 // order. An output's bits depend on its row, its column and the reduction's length only: not on the
 // tile it falls into, nor on the batch.
 //
-// Large products (8192 x 4096 -> 4096 100 us, 2740 TFLOP/s; 4096 x 17408 -> 5120 275) are bound by a chain: TMEM holds two
+// Large products (8192 x 4096 -> 4096 101 us, 2720 TFLOP/s; 4096 x 17408 -> 5120 279) are bound by a chain: TMEM holds two
 // accumulators of a 256-column tile, and each is filled, told, read and given back; the tensor pipe is 65 % busy. Few rows are bound by
 // an SM's loads, 45 bytes a ns, and by the k-blocks' order (1 x 5120 -> 17408 17.8 us of 13.2 that the memory needs): hence tiles of 32
 // to 256 columns, by which more SMs load.
