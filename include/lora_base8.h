@@ -58,7 +58,7 @@ lora_status lora_block8_linear_bwd(const void *dy, const float *dy_scales, const
  *   p_i  = exp(teacher[i] / T - L)     L = teacher_lse of the row, or log(sum of exp(teacher[i] / T)) when it is NULL
  *   loss = weight * (sum of p_i (log p_i - log q[ids[i]])  [+ r (log r - log rho), with teacher_lse])
  *          r = max(1 - sum of p_i, 0), rho = sum of q over what is no entry; terms of p_i = 0 or r = 0 are 0.
- *          Where rho < 2^-64, an r of (64 + 8 |teacher_lse|) 2^-24 or less is FP32's rounding of 0 (a teacher that lists all
+ *          Where rho < 2^-4096, an r of (64 + 8 |teacher_lse|) 2^-24 or less is FP32's rounding of 0 (a teacher that lists all
  *          its mass, a mask that leaves the student nothing else) and counts as 0; a larger one beside rho = 0 is infinite
  *   logits       [M][V] bf16 or fp32 (type)      ids [M][top] int32 or int64 (id_bytes 4 or 8)
  *   teacher      [M][top] bf16 or fp32 (teacher_type)
@@ -67,7 +67,7 @@ lora_status lora_block8_linear_bwd(const void *dy, const float *dy_scales, const
  *   loss         [M] FP32 (out)
  *   probs        [M][top] FP32 (out): p_i; -1 for what is no entry, and in rows of weight 0
  *   stats        [M][4] FP32 (out): the largest logit m; log2(sum of exp((logit - m) / T)), with teacher_lse less
- *                log2(max(sum of p_i, 1)); 1 - r / rho (1 without teacher_lse, and where rho is 0 or below 2^-4096 r), or,
+ *                log2(max(sum of p_i, 1)); 1 - r / rho (1 without teacher_lse, and where rho < 2^-4096), or,
  *                from r / rho = 2^64 on, -2^64 log2(r / rho); the weight. Zeros in rows of weight 0 or without entries
  * 1 <= V < 2^22, 1 <= top <= 1024, T > 0, finite and no subnormal number. A row without entries has loss 0 and gradient 0.
  */

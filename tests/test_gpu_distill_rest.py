@@ -258,3 +258,17 @@ def test_rows_of_weight_0_have_no_gradient_whatever_dloss_is(bad, v, dtype):
         dz = block8.unblock8(dz) if block else dz
         assert not dz[4].any() and not dz[6].any() and bool(dz.isfinite().all())
         assert block or same(dz, ok)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("r", [2e-6, 1e-5])
+@pytest.mark.parametrize("gap", [50, 100, 2500])
+def test_a_small_r_beside_a_rest_that_is_not_nothing_is_one(gap, r, dtype):
+    """r of a few roundings is the definition's r as long as rho has a logarithm that the gradient knows."""
+    for T in (0.25, 1.0):
+        c = gapped(gap, T, dtype, r)
+        c["teacher"] -= 20 * T
+        c["teacher_lse"] -= 20
+        _, _, k = check(c)
+        # (teacher_lse and the logits near -20 are rounded to 2^-20 each: so far is the r that they give from the one wanted)
+        assert bool(((k["r"] - r).abs() < 2.0 ** -18).all()) and bool((k["r"] > 0).all())
