@@ -391,17 +391,17 @@ __device__ __forceinline__ void make_lists(const DistillArgs& P, const Row& r, i
   __syncwarp();
 }
 
-// A rest below 2^-64 of the row, whose sum would lose itself beside the entries': its part of the loss, left (log left - log rho),
-// and what the backward pass takes, 1 - left / rho. Both from log rho, taken from the rest's own maximum. From left / rho = 2^64 on
-// that is held by its logarithm, as -2^64 log2: left rho_j of an element is then one exponential of log2(left / rho) and the
-// element's exponent, where q_j alone may be too small for a float. Of a logarithm of 2^12 a float's rounding is 1e-4 of the
+// A rest below 2^-32 of the row, whose sum may lose itself beside the entries': its part of the loss, left (log left - log rho),
+// and what the backward pass takes, 1 - left / rho. Both from log rho, taken from the rest's own maximum. From left / rho = 2^32 on
+// (the 1 is no part of that) it is held by its logarithm, as -2^32 log2: left rho_j of an element is then one exponential of
+// log2(left / rho) and the element's exponent, where q_j alone may be too small for a float. Of a logarithm of 2^12 a float's rounding is 1e-4 of the
 // gradient: below that rho counts as 0 there. (Halves: the difference of two of the type's values may pass its largest.)
 //
 // A teacher that lists all its mass leaves 0 only up to roundings, in half ulps of 1: 36 of a sum of 1024 p (31 a lane, then five), 2 of
 // the exponentials, 7 (log 1024, the largest sum of p |log p|) of their arguments, a few of the caller's own sum; and |lse| for each
 // rounding on the way to lse. Where rho counts as 0 so much is no mass: its logarithm would be all of the loss (1e-7 of a mask's
 // lowest value). (1/2 at most: lse may be infinite.)
-constexpr float kFarRest = 0x1p-64f, kFarOver = 0x1p64f, kFarKeep = -0x1p70f, kFarMost = 4096.f;
+constexpr float kFarRest = 0x1p-32f, kFarOver = 0x1p32f, kFarKeep = -0x1p37f, kFarMost = 4096.f;
 __device__ __noinline__ float2 far_rest(float left, float log_left, float lse, Part rest, float m, float s, float inv_t, float c) {
   const float fall = 0.5f * rest.m - 0.5f * m;
   const float log2_rho = rest.s == 0.f ? -kInf : 2.f * (fall * c) + (log2f(rest.s) - log2f(s));
@@ -410,7 +410,7 @@ __device__ __noinline__ float2 far_rest(float left, float log_left, float lse, P
   if (rest.s == 0.f) return make_float2(left * kInf, 1.f);                              // (NaN stays)
   const float over = log2f(left) - log2_rho;                                            // log2(left / rho); NaN stays
   return make_float2(left * (log_left - (2.f * (fall * inv_t) + (logf(rest.s) - logf(s)))),
-                     none ? 1.f : (over < 64.f ? 1.f - exp2f(over) : -kFarOver * over));
+                     none ? 1.f : (over < 32.f ? 1.f - exp2f(over) : -kFarOver * over));
 }
 
 // The row's end, from the eight warps' parts: of one warp.

@@ -68,7 +68,7 @@ lora_status lora_block8_linear_bwd(const void *dy, const float *dy_scales, const
  *   probs        [M][top] FP32 (out): p_i; -1 for what is no entry, and in rows of weight 0
  *   stats        [M][4] FP32 (out): the largest logit m; log2(sum of exp((logit - m) / T)), with teacher_lse less
  *                log2(max(sum of p_i, 1)); 1 - r / rho (1 without teacher_lse, and where rho < 2^-4096), or,
- *                from r / rho = 2^64 on, -2^64 log2(r / rho); the weight. Zeros in rows of weight 0 or without entries
+ *                from r / rho = 2^32 on, -2^32 log2(r / rho); the weight. Zeros in rows of weight 0 or without entries
  * 1 <= V < 2^22, 1 <= top <= 1024, T > 0, finite and no subnormal number. A row without entries has loss 0 and gradient 0.
  */
 lora_status lora_distill_topk_fwd(const void *logits, int type, const void *ids, int id_bytes, const void *teacher,

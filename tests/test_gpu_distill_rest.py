@@ -272,3 +272,24 @@ def test_a_small_r_beside_a_rest_that_is_not_nothing_is_one(gap, r, dtype):
         _, _, k = check(c)
         # (teacher_lse and the logits near -20 are rounded to 2^-20 each: so far is the r that they give from the one wanted)
         assert bool(((k["r"] - r).abs() < 2.0 ** -18).all()) and bool((k["r"] > 0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0.25, 1.0])
+@pytest.mark.parametrize("gap", [20, 28, 36, 44, 52])
+def test_elements_far_below_a_far_rest(gap, T, dtype):
+    """Half of the rest lies 55 T below the other half: q_j is too small for a float, r rho_j is not."""
+    c = gapped(gap, T, dtype)
+    low = torch.ones_like(c["logits"], dtype=torch.bool).scatter_(1, c["ids"], False)
+    low[:, ::2] = False
+    c["logits"][low] -= 55 * T
+    dl = torch.ones(8, device="cuda")
+    loss, probs, stats = fwd(c)
+    got = bwd(c, dl, probs, stats).double()
+    want, dz, k = definition(c, dl)
+    tol, t = off_by(c, dl, want, dz, k)
+    # an exponential below 2^-126 is 0, times an r / rho of 2^32 at most (above, its logarithm is part of the exponent)
+    flushed = (k["w"] / k["T"])[:, None] * 2.0 ** -94
+    assert bool(((got - dz).abs() <= t + flushed + (2.0 ** -8 if dtype == BF else U32) * (dz.abs() + t)).all())
+    assert gap < 36 or bool((got[low] < 0).all())
+    assert bool(((loss.double() - want).abs() <= tol).all())
