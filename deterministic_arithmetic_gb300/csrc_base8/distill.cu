@@ -452,10 +452,10 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
   // row's. The terms of a small divergence cancel, and so keep their digits: what a product or 1 / T leaves is carried along.
   const float inv_t = 1.f / P.temperature, inv_lo = fmaf(-P.temperature, inv_t, 1.f) * inv_t;
   const float log_s = logf(s), log_t = logf(s_teacher), lse = P.teacher_lse ? __ldg(P.teacher_lse + row) : 0.f;
-  // (v / T as a float and its rest)
+  // (v / T as a float and its rest; a mask's lowest value may pass the range, and has none)
   const auto over_t = [&](float v, float* lo) {
     const float h = v * inv_t;
-    *lo = fmaf(v, inv_t, -h) + v * inv_lo;
+    *lo = fabsf(h) < kInf ? fmaf(v, inv_t, -h) + v * inv_lo : 0.f;
     return h;
   };
   float m_lo;

@@ -293,3 +293,31 @@ def test_elements_far_below_a_far_rest(gap, T, dtype):
     assert bool(((got - dz).abs() <= t + flushed + (2.0 ** -8 if dtype == BF else U32) * (dz.abs() + t)).all())
     assert gap < 36 or bool((got[low] < 0).all())
     assert bool(((loss.double() - want).abs() <= tol).all())
+
+
+# --------------------------------------------------------- a teacher's own masks
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("teacher", [BF, F32])
+@pytest.mark.parametrize("T", [0.1, 0.5, 1.0, 2.0])
+def test_entries_of_the_teachers_lowest_value_have_probability_0(T, teacher, tail):
+    """t / T may pass the type's range; the others' probabilities, the loss and the gradient are those of rows without them."""
+    c = make(6, 900, 12, tail=tail, T=T, teacher=teacher)
+    c["teacher"][:4, 8:] = torch.finfo(teacher).min
+    c["teacher"][1, 3] = torch.finfo(teacher).min
+    loss, probs, stats = fwd(c)
+    dz = bwd(c, torch.ones(6, device="cuda"), probs, stats)
+    gone = c["teacher"] == torch.finfo(teacher).min
+    assert bool(loss.isfinite().all()) and bool((probs[gone] == 0).all()) and bool((probs[~gone] > 0).all())
+    want = probs.double()
+    if not tail:                                   # the same entries without them: p are the same to their roundings
+        d = dict(c, teacher=c["teacher"].masked_fill(gone, -INF))
+        l2, p2, _ = fwd(d)
+        assert bool(((probs - p2.clamp_min(0)).abs() <= 2.0 ** -22 * want).all())
+        assert bool(((loss - l2).abs() <= 2.0 ** -20 * l2.abs()).all())
+    else:
+        k = definition(c, torch.ones(6, device="cuda"))
+        assert bool(((want - k[2]["p"]).abs() <= 2.0 ** -20 * k[2]["p"] * (1 + k[2]["log_p"].abs().clamp_max(1e30))).all())
+        tol, t = off_by(c, torch.ones(6, device="cuda"), k[0], k[1], {**k[2], "log_p": k[2]["log_p"].clamp_min(-1e30)})
+        assert bool(((loss.double() - k[0]).abs() <= tol).all())
+        # (an exponential below 2^-126 is 0, times an r / rho of 2^32 at most and weight / T of at most 1.5 / 0.1 < 2^4)
+        assert bool(((dz.double() - k[1]).abs() <= t + U32 * k[1].abs() + 2.0 ** -90).all())
