@@ -277,6 +277,7 @@ struct DistillArgs {
   int64_t M;
   int V, top, groups, places;      // groups of 256 elements of a row; forward: places of a warp
   float temperature;
+  float inv_t, inv_t_lo, c;        // forward: 1 / temperature as the sum of two; log2(e) / temperature
   float *loss, *probs, *stats;
   void* dz;
   float* scales;
@@ -346,6 +347,49 @@ struct Row {
   float *t, *z;                    // the entries' teacher logits, -infinity where dropped; and student logits
 };
 
+// A number as the sum of two floats, of which the second has what the first has not.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+// v / T so (1 / T given so); a mask's lowest value may pass the range, and has no rest.
+__device__ __forceinline__ Two over_t(float v, Two inv_t) {
+  const float h = v * inv_t.hi;
+  return {h, fabsf(h) < kInf ? fmaf(v, inv_t.hi, -h) + v * inv_t.lo : 0.f};
+}
+__device__ const float2 kRoots[32] = {             // 2^(j / 32)
+    {0x1p+0f, 0.f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.11301ep+0f, -0x1.fdb496p-25f},
+    {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f},
+    {0x1.306fep+0f, 0x1.4636e2p-25f}, {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.6247ecp+0f, -0x1.f8b55p-25f},
+    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f}, {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f},
+    {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.cb720ep+0f, -0x1.8837ccp-27f},
+    {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f}, {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.f50766p+0f, -0x1.246ebp-26f}};
+// p = e^(t / T - lse) in units of 2^-50, right to 2^-44 of 1 (a p of e^-64 or less is 0, of more than e is e). By a table and the series of
+// e^g (P. T. P. Tang, 1989): t / T - lse = j log 2 / 32 + g, with log 2 / 32 in three parts, j times the first of which is exact.
+__device__ __forceinline__ int64_t whole_p(float t, float lse, Two inv_t, const float2* roots) {
+  const Two v = over_t(t, inv_t);
+  const bool some = v.hi > lse - 64.f;
+  Two a = two_sum(some ? fminf(v.hi, lse + 1.f) : lse - 64.f, -lse);
+  a.lo += some ? v.lo : 0.f;
+  const float j = rintf(a.hi * 46.166241f), h = j * 0x1.0bfbe8p-20f;
+  const int k = int(j);
+  const float2 root = roots[k & 31];
+  const Two f = two_sum(fmaf(-j, 0x1.62ep-6f, a.hi), -h);
+  const float g = f.hi, gl = f.lo + fmaf(-j, 0x1.cf79acp-45f, a.lo - fmaf(j, 0x1.0bfbe8p-20f, -h));
+  const float q = g * g, ql = fmaf(g, g, -q), u = fmaf(0.5f, q, g), ul = fmaf(0.5f, q, g - u);
+  const float c = q * g * fmaf(g, fmaf(g, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f);
+  const float w = ul + fmaf(0.5f, ql, gl + fmaf(u, gl, c));                             // e^g - 1 = u + w
+  const float x = root.x * u, xl = fmaf(root.x, u, -x), p = __fadd_rn(root.x, x);
+  const float pl = (x - (p - root.x)) + (xl + fmaf(root.y, u, fmaf(root.x, w, root.y)));
+  const float scale = __uint_as_float(uint32_t(127 + 50 + (k >> 5)) << 23);
+  return __float2ll_rn(p * scale) + __float2int_rn(pl * scale);
+}
+
 // The lists, of all lanes. Logits only where they are wanted (the cluster's first CTA).
 __device__ __forceinline__ void make_lists(const DistillArgs& P, const Row& r, int kind, int64_t row, bool logits, int lane) {
   const Lists& L = r.lists;
@@ -391,31 +435,68 @@ __device__ __forceinline__ void make_lists(const DistillArgs& P, const Row& r, i
   __syncwarp();
 }
 
-// A rest below 2^-32 of the row, whose sum may lose itself beside the entries': its part of the loss, left (log left - log rho),
-// and what the backward pass takes, 1 - left / rho. Both from log rho, taken from the rest's own maximum. From left / rho = 2^32 on
-// (the 1 is no part of that) it is held by its logarithm, as -2^32 log2: left rho_j of an element is then one exponential of
-// log2(left / rho) and the element's exponent, where q_j alone may be too small for a float. Of a logarithm of 2^12 a float's rounding is 1e-4 of the
-// gradient: below that rho counts as 0 there. (Halves: the difference of two of the type's values may pass its largest.)
+// 1 - sum p of a row's entries, of the whole warp, where the floats' sum of p is near 1: the listed logits may have all the teacher's
+// mass but 10^-6, of which p and sums in floats leave nothing. The sum is one of whole numbers, and so exact. (Of a teacher of
+// 64 entries that has only such rows, 8192 x 2000 89 -> 98 us, 4096 x 32000 63 -> 69, x 131072 177 -> 177. In doubles, of which GB300
+// makes two operations an SM and cycle, 115, 77 and 182; in every row, while the student's logits are on their way, 107, 72 and 181.)
+__device__ __forceinline__ float rest_of_teacher(const DistillArgs& P, const float* t, float lse, const float2* roots, int lane) {
+  int64_t sum = 0;
+#pragma unroll 1
+  for (int i = lane; i < P.top; i += 32) sum += whole_p(t[i], lse, {P.inv_t, P.inv_t_lo}, roots);    // (-infinity: no entry)
+  constexpr int kHalf = 25;
+  const uint32_t high = __reduce_add_sync(0xffffffffu, uint32_t(sum >> kHalf));
+  const uint32_t low = __reduce_add_sync(0xffffffffu, uint32_t(sum) & ((1u << kHalf) - 1));
+  const int64_t left = (int64_t(1) << 50) - ((int64_t(high) << kHalf) + low);
+  return fmaf(float(int(left >> 24)), 0x1p-26f, float(int(left & 0xFFFFFF)) * 0x1p-50f);
+}
+
+// The end of a row with teacher_lse whose pieces are far apart, or whose listed entries have all the teacher's mass or nearly.
 //
-// A teacher that lists all its mass leaves 0 only up to roundings, in half ulps of 1: 36 of a sum of 1024 p (31 a lane, then five), 2 of
-// the exponentials, 7 (log 1024, the largest sum of p |log p|) of their arguments, a few of the caller's own sum; and |lse| for each
-// rounding on the way to lse. Where rho counts as 0 so much is no mass: its logarithm would be all of the loss (1e-7 of a mask's
-// lowest value). (1/2 at most: lse may be infinite.)
-constexpr float kFarRest = 0x1p-32f, kFarOver = 0x1p32f, kFarKeep = -0x1p37f, kFarMost = 4096.f;
-__device__ __noinline__ float2 far_rest(float left, float log_left, float lse, Part rest, float m, float s, float inv_t, float c) {
-  const float fall = 0.5f * rest.m - 0.5f * m;
-  const float log2_rho = rest.s == 0.f ? -kInf : 2.f * (fall * c) + (log2f(rest.s) - log2f(s));
-  const bool none = log2_rho < -kFarMost;
-  if (left == 0.f || (none && left <= fminf(0.5f, fmaf(8.f, fabsf(lse), 64.f) * 0x1p-24f))) return make_float2(0.f, 1.f);
-  if (rest.s == 0.f) return make_float2(left * kInf, 1.f);                              // (NaN stays)
-  const float over = log2f(left) - log2_rho;                                            // log2(left / rho); NaN stays
-  return make_float2(left * (log_left - (2.f * (fall * inv_t) + (logf(rest.s) - logf(s)))),
-                     none ? 1.f : (over < 32.f ? 1.f - exp2f(over) : -kFarOver * over));
+// A rest below 2^-32 of the row's sum may lose itself beside the entries': log rho is taken from the rest's own maximum. And what the
+// backward pass takes, 1 - r / rho, from r / rho = 2^32 on (the 1 is no part of that) is held by its logarithm, as -2^32 log2: r rho_j of
+// an element is then one exponential of log2(r / rho) and the element's exponent, where q_j alone may be too small for a float.
+// Of a logarithm of 2^12 a float's rounding is 1e-4 of the gradient: below that rho counts as 0 there. (Halves: the
+// difference of two of the type's values may pass its largest.)
+//
+// A teacher that lists all its mass leaves 0 only up to the roundings of its log-sum-exp, in half ulps of 1: up to 64 of a sum of
+// exponentials, and |lse| for each rounding on the way, of t / T, of the largest, of the result. Where rho counts as 0 so much is no
+// mass: its logarithm would be all of the loss (1e-7 of a mask's lowest value). (1/2 at most: lse may be infinite.)
+constexpr float kSmall = 0.0625f, kFarRest = 0x1p-32f, kFarOver = 0x1p32f, kFarKeep = -0x1p37f, kFarMost = 4096.f;
+__device__ __forceinline__ void end_rare(const DistillArgs& P, const float* t, Part rest, float m, float s, float s_rest, float s_top,
+                                         float sum_p, float loss, float lse, const float2* roots, int64_t row, float weight, int lane) {
+  const float c = P.c;
+  float left = 1.f - sum_p, log_left = 0.f, log2_p = 0.f, keep = 1.f;
+  if (left > -1.f && left < kSmall) left = rest_of_teacher(P, t, lse, roots, lane);
+  if (lane != 0) return;
+  if (left > 0.f) {
+    log_left = left < kSmall ? logf(left) : log1pf(-sum_p);
+  } else {                                         // the gradient is sum_p q - p
+    log2_p = left > -1.f ? kLog2e * log1pf(-left) : log2f(sum_p);
+    left = 0.f;
+  }
+  if (s_rest < s * kFarRest) {
+    const float fall = 0.5f * rest.m - 0.5f * m;
+    const float log2_rho = rest.s == 0.f ? -kInf : 2.f * (fall * c) + (log2f(rest.s) - log2f(s));
+    const bool none = log2_rho < -kFarMost;
+    if (none && left <= fminf(0.5f, fmaf(8.f, fabsf(lse), 64.f) * 0x1p-24f)) left = 0.f;
+    if (left != 0.f) {
+      const float over = log2f(left) - log2_rho;                                         // log2(r / rho)
+      loss += rest.s == 0.f ? kInf : left * (log_left - (2.f * (fall * P.inv_t) + (logf(rest.s) - logf(s))));
+      keep = none ? 1.f : (over < 32.f ? 1.f - exp2f(over) : -kFarOver * over);
+    }
+  } else if (left != 0.f) {
+    const float ratio = s_top / s_rest;            // log rho = -log(1 + ratio)
+    loss += left * (log_left + log1pf(ratio));
+    if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
+  }
+  P.loss[row] = weight * loss;
+  *reinterpret_cast<float4*>(P.stats + row * 4) = make_float4(m, log2f(s) - log2_p, keep, weight);
 }
 
 // The row's end, from the eight warps' parts: of one warp.
-__device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, const Part* warps, int64_t row, float weight, int lane) {
-  const float c = kLog2e / P.temperature;
+__device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, const Part* warps, const float2* roots, int64_t row, float weight,
+                                        int lane) {
+  const float c = P.c;
   // the rest of the vocabulary
   Part rest = warps[0];
 #pragma unroll
@@ -450,17 +531,10 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
   const float s_rest = rescale(rest.s, rest.m, m, c), s = P.teacher_lse ? s_rest + s_top : s_rest;
   // log p - log q = (t - z) / T - (norm - log sum exp(z / T)): a difference of an entry's own two logits, and one of the
   // row's. The terms of a small divergence cancel, and so keep their digits: what a product or 1 / T leaves is carried along.
-  const float inv_t = 1.f / P.temperature, inv_lo = fmaf(-P.temperature, inv_t, 1.f) * inv_t;
+  const float inv_t = P.inv_t;
   const float log_s = logf(s), log_t = logf(s_teacher), lse = P.teacher_lse ? __ldg(P.teacher_lse + row) : 0.f;
-  // (v / T as a float and its rest; a mask's lowest value may pass the range, and has none)
-  const auto over_t = [&](float v, float* lo) {
-    const float h = v * inv_t;
-    *lo = fabsf(h) < kInf ? fmaf(v, inv_t, -h) + v * inv_lo : 0.f;
-    return h;
-  };
-  float m_lo;
-  const float m_hi = over_t(m, &m_lo);
-  const float gap = P.teacher_lse ? ((lse - m_hi) - m_lo) - log_s : fmaf(tm - m, inv_t, log_t - log_s);
+  const Two m_t = over_t(m, {P.inv_t, P.inv_t_lo});
+  const float gap = P.teacher_lse ? ((lse - m_t.hi) - m_t.lo) - log_s : fmaf(tm - m, inv_t, log_t - log_s);
   // Logits far from the teacher's (a row whose mask leaves only the type's lowest value) lose the digits of t in t - z:
   // there, log p and log q each from its own maximum.
   const bool near = fabsf(gap) < 64.f;
@@ -470,8 +544,8 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
     const float ti = r.t[i];
     float p = -1.f;
     if (ti != -kInf) {
-      float lo;
-      const float h = over_t(ti, &lo), log_p = P.teacher_lse ? (h - lse) + lo : (ti - tm) * inv_t - log_t;
+      const Two v = over_t(ti, {P.inv_t, P.inv_t_lo});
+      const float log_p = P.teacher_lse ? (v.hi - lse) + v.lo : (ti - tm) * inv_t - log_t;
       p = expf(log_p);
       sum_p += p;
       if (p != 0.f) loss += p * (near ? (ti - r.z[i]) * inv_t - gap : log_p - ((r.z[i] - m) * inv_t - log_s));
@@ -480,24 +554,18 @@ __device__ __forceinline__ void end_row(const DistillArgs& P, const Row& r, cons
   }
   sum_p = warp_sum(sum_p);
   loss = warp_sum(loss);
-  if (lane == 0) {
-    float keep = 1.f, log2_s = log2f(s);
+  if (__builtin_expect(P.teacher_lse && any && (1.f - sum_p < kSmall || s_rest < s * kFarRest), 0)) {
+    end_rare(P, r.t, rest, m, s, s_rest, s_top, sum_p, loss, lse, roots, row, weight, lane);
+  } else if (lane == 0) {
+    float keep = 1.f;
     if (P.teacher_lse) {
-      if (sum_p > 1.f) log2_s -= log2f(sum_p);     // the gradient is sum_p q - p then
-      const float left = sum_p >= 1.f ? 0.f : 1.f - sum_p;
-      if (s_rest < s * kFarRest) {
-        const float2 far = far_rest(left, log1pf(-sum_p), lse, rest, m, s, inv_t, c);
-        loss += far.x;
-        keep = far.y;
-      } else {
-        const float ratio = s_top / s_rest;                                             // log rho = -log(1 + ratio)
-        if (left != 0.f) loss += left * (log1pf(-sum_p) + log1pf(ratio));               // (NaN too)
-        if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
-      }
+      const float left = 1.f - sum_p, ratio = s_top / s_rest;                            // log rho = -log(1 + ratio)
+      loss += left * (log1pf(-sum_p) + log1pf(ratio));
+      if (s_rest != 0.f) keep = 1.f - left * (1.f + ratio);
     }
     P.loss[row] = any ? weight * loss : 0.f;
     *reinterpret_cast<float4*>(P.stats + row * 4) =
-        any ? make_float4(m, log2_s, keep, weight) : make_float4(0.f, 0.f, 0.f, 0.f);
+        any ? make_float4(m, log2f(s), keep, weight) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
@@ -526,6 +594,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND>) distill_fwd_kerne
   __shared__ Part sent[kPlaces][kThreads];         // the threads' places; in a cluster's first CTA all of them
   __shared__ Part parts[2][kWarps];
   __shared__ int64_t rows[2];                      // the rows in turn; -1: no more
+  __shared__ float2 roots[32];                     // kRoots, for the ninth warp
   const int lane = int(lane_id()), warp = int(warp_id()), tid = int(threadIdx.x);
   const int rank = CL > 1 ? int(cluster_rank()) : 0;
   const auto entries = [&](int b) {
@@ -539,6 +608,8 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND>) distill_fwd_kerne
 
   if (warp == kWarps) {
     // ---------------------------------------------------------- the entries
+    if (P.teacher_lse) roots[lane] = kRoots[lane];
+    __syncwarp();
     int64_t next = blockIdx.x / CL, was = -1;
     float weight = 0.f, w_next = P.weight ? __ldg(P.weight + next) : 1.f;
     const int64_t step = gridDim.x / CL;
@@ -565,7 +636,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND>) distill_fwd_kerne
         if constexpr (CL > 1) cluster_sync_all();  // (a cluster has one row)
         if (rank == 0) {
           named_bar(kBarParts + (b ^ 1), kFwdThreads);
-          end_row(P, entries(b ^ 1), parts[b ^ 1], was, weight, lane);
+          end_row(P, entries(b ^ 1), parts[b ^ 1], roots, was, weight, lane);
         }
       }
       if (row < 0) return;
@@ -577,7 +648,7 @@ __global__ void __launch_bounds__(kFwdThreads, kMinCtas<KIND>) distill_fwd_kerne
   // ---------------------------------------------------------------- the stream
   // A set of groups is sent for, taken in, and the next one sent for, of the next row when this one has no more: warps wait in
   // turn.
-  const float c = kLog2e / P.temperature;
+  const float c = P.c;
   constexpr int kBytes = KIND == kF32 ? 4 : 2;
   const int stride = P.places * kWarps, round = stride * kGroupElems;      // groups and elements of a round
   const int sets = (P.groups + stride * kSet - 1) / (stride * kSet);       // of a place
@@ -982,6 +1053,9 @@ lora_status lora_distill_topk_fwd(const void* logits, int type, const void* ids,
   P.teacher_lse = teacher_lse;
   P.weight = weight;
   P.temperature = temperature;
+  P.inv_t = 1.f / temperature;
+  P.inv_t_lo = float(1.0 / double(temperature) - double(P.inv_t));
+  P.c = kLog2e / temperature;
   P.M = M;
   P.V = int(V);
   P.top = int(top);

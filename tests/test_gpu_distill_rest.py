@@ -321,3 +321,38 @@ def test_entries_of_the_teachers_lowest_value_have_probability_0(T, teacher, tai
         assert bool(((loss.double() - k[0]).abs() <= tol).all())
         # (an exponential below 2^-126 is 0, times an r / rho of 2^32 at most and weight / T of at most 1.5 / 0.1 < 2^4)
         assert bool(((dz.double() - k[1]).abs() <= t + U32 * k[1].abs() + 2.0 ** -90).all())
+
+
+# ----------------------------------------------------------------- digits of 1 - sum p
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("v,top,T", [(1000, 256, 0.7), (3001, 256, 0.7), (700, 30, 0.5), (20000, 64, 1.0), (2000, 1024, 1.0), (5000, 100, 2.0)])
+def test_a_small_mass_of_the_rest_has_its_digits(v, top, T, dtype):
+    """r = 1 - sum p of 10^-3 to 10^-7, as a teacher leaves whose listed logits have nearly all its mass: r / rho is right to rho's own
+    roundings, and to 2^-43 / rho (an entry's p to 2^-44 of itself or of 1)."""
+    c = make(200, v, top, dtype, tail=True, T=T)
+    _, _, stats = fwd(c)
+    _, _, k = definition(c, torch.ones(200, device="cuda"))
+    rho = torch.where(k["r"] > 0, k["log_rho"], 0.0).exp()
+    off = (stats[:, 2].double() - (1 - k["r"] / rho)).abs()
+    # rho: exponentials 2^-21, of arguments up to 64 right to 2^-24 of themselves, and the sums; then the stored value's rounding
+    rel = 2.0 ** -21 + 64 * U32 + (v / 16384 + 64) * U32 + 2.0 ** -23
+    bound = k["r"] / rho * rel + 2.0 ** -43 / rho + 2.0 ** -22
+    assert bool((off <= bound).all())
+    if top < 1000:                                 # entries given twice, the second time with another logit: the first counts
+        twice = {key: torch.cat([c[key], c[key][:, :5] + more], 1) for key, more in (("ids", 0), ("teacher", 1.0))}
+        _, probs, stats = fwd(dict(c, **twice))
+        assert bool((probs[:, top:] == -1).all())
+        assert bool(((stats[:, 2].double() - (1 - k["r"] / rho)).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("top", [1, 4, 64])
+@pytest.mark.parametrize("T", [2.0, 4.0])
+def test_a_small_divergence_has_its_digits(T, top, dtype):
+    """A flat teacher and student over a long vocabulary: the listed entries have little of the mass, and the loss is what is left of
+    terms that cancel. Each is right to 2^-20 of the listed mass: p and q of the entries to 2^-21, the logarithms to 2^-22."""
+    c = make(60, 60000, top, dtype, tail=True, T=T)
+    loss, _, _ = fwd(c)
+    want, _, k = definition(c, torch.ones(60, device="cuda"))
+    listed = k["p"].sum(1) + k["log_q"].gather(1, c["ids"]).exp().sum(1)
+    assert bool(((loss.double() - want).abs() <= k["w"] * (2.0 ** -20 * listed * (1 + (k["log_p"] - k["log_q"].gather(1, c["ids"])).abs().amax(1)) + 2.0 ** -22 * want)).all())
