@@ -14,6 +14,7 @@
 #include "../csrc_mlp/elems.cuh"
 #include "base8.h"
 #include "block8.cuh"
+#include "distill.h"
 
 #include <algorithm>
 #include <cfloat>
@@ -1035,7 +1036,16 @@ lora_status lora_distill_topk_fwd(const void* logits, int type, const void* ids,
                                   int teacher_type, const float* teacher_lse, const float* weight, float temperature,
                                   int64_t M, int64_t V, int64_t top, float* loss, float* probs, float* stats,
                                   void* stream) {
-  if (!args_ok(type, id_bytes, temperature, M, V, top) || !type_ok(teacher_type)) return LORA_ERR_SHAPE;
+  return lora_distill_topk_fwd_wide(logits, type, ids, id_bytes, teacher, teacher_type, teacher_lse, weight, temperature, M, V,
+                                    top, loss, probs, stats, stream);
+}
+
+lora_status lora_distill_topk_fwd_wide(const void* logits, int type, const void* ids, int id_bytes, const void* teacher,
+                                       int teacher_type, const float* teacher_lse, const float* weight, double temperature,
+                                       int64_t M, int64_t V, int64_t top, float* loss, float* probs, float* stats,
+                                       void* stream) {
+  const float t = float(temperature);
+  if (!args_ok(type, id_bytes, t, M, V, top) || !type_ok(teacher_type)) return LORA_ERR_SHAPE;
   if (M == 0) return LORA_OK;
   lora_status s = check_ptrs(logits, ids, teacher, static_cast<const void*>(loss), static_cast<const void*>(probs),
                              static_cast<const void*>(stats));
@@ -1052,10 +1062,10 @@ lora_status lora_distill_topk_fwd(const void* logits, int type, const void* ids,
   P.teacher_type = teacher_type;
   P.teacher_lse = teacher_lse;
   P.weight = weight;
-  P.temperature = temperature;
-  P.inv_t = 1.f / temperature;
-  P.inv_t_lo = float(1.0 / double(temperature) - double(P.inv_t));
-  P.c = kLog2e / temperature;
+  P.temperature = t;
+  P.inv_t = 1.f / t;
+  P.inv_t_lo = float(1.0 / temperature - double(P.inv_t));
+  P.c = kLog2e / t;
   P.M = M;
   P.V = int(V);
   P.top = int(top);

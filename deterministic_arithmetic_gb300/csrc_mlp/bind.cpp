@@ -15,7 +15,7 @@
 
 #include <sstream>
 
-#include "../../include/lora_base8.h"
+#include "../csrc_base8/distill.h"
 
 namespace {
 
@@ -499,7 +499,7 @@ PyObject* distill_topk_fwd(PyObject* const* a) {  // logits, ids, teacher, tempe
   const int64_t top = ids.dim() == 2 ? ids.size(1) : 0;
   const void* ip = check_ids(ids, {M, top}, dev, &bytes);
   const void* tp = check_either(teacher, "teacher", {M, top}, dev, &tt);
-  const float temperature = float(number(a[3]));
+  const double temperature = number(a[3]);
   const float* lse = a[4] == Py_None ? nullptr : static_cast<const float*>(check(a[4], "teacher_lse", {M}, F32, dev));
   const float* w = a[5] == Py_None ? nullptr : static_cast<const float*>(check(a[5], "weight", {M}, F32, dev));
   Tensor loss, probs, stats;
@@ -514,8 +514,8 @@ PyObject* distill_topk_fwd(PyObject* const* a) {  // logits, ids, teacher, tempe
     probs = out(a[7], "probs", {M, top}, F32, dev);
     stats = out(a[8], "stats", {M, 4}, F32, dev);
   }
-  done(lora_distill_topk_fwd(zp, type, ip, bytes, tp, tt, lse, w, temperature, M, V, top, loss.data_ptr<float>(),
-                             probs.data_ptr<float>(), stats.data_ptr<float>(), stream(dev)), "lora_distill_topk_fwd");
+  done(lora_distill_topk_fwd_wide(zp, type, ip, bytes, tp, tt, lse, w, temperature, M, V, top, loss.data_ptr<float>(),
+                                  probs.data_ptr<float>(), stats.data_ptr<float>(), stream(dev)), "lora_distill_topk_fwd");
   return tuple(wrap(loss), wrap(probs), wrap(stats));
 }
 

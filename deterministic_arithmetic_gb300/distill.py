@@ -19,7 +19,7 @@ def distill_topk_fwd(logits, ids, teacher, *, temperature: float = 1.0, teacher_
     teacher's logits at ``ids`` [M, top] (int64 or int32, top <= 1024).
 
     An id outside the vocabulary (-1, say), a logit of -infinity and a second entry of an id are no entries.
-    ``teacher_lse`` [M] fp32: log(sum of exp(t / T)) over the teacher's vocabulary. ``weight`` [M] fp32 multiplies
+    ``teacher_lse`` [M] fp32: log(sum of exp(t / T)) over the teacher's vocabulary (``temperature`` counts with its 64 bits). ``weight`` [M] fp32 multiplies
     the loss; rows of weight 0 are not read. ``loss`` [M] is fp32, unreduced, without a factor of T * T; ``probs``
     [M, top] (the teacher's probabilities, -1 for no entry) and ``stats`` [M, 4] are for the backward pass. (New ones of up
     to 1 MiB together lie in one allocation.)"""
